@@ -26,7 +26,7 @@ POS_ONE = 65536
 POS_STRIDE = 32  # int32 words per slot in conv_pos: slot s's position is conv_pos[s, 0]
 CHUNK = 64
 
-ABI_VERSION = 7  # GDN_ABI_VERSION of include/gdn.h that these signatures follow
+ABI_VERSION = 8  # GDN_ABI_VERSION of include/gdn.h that these signatures follow
 DEV_OK = 0
 DEV_BAD_SLOT = 1
 DEV_BAD_ACCEPTED = 2
@@ -35,6 +35,10 @@ DEV_WAIT_TIMEOUT = 4
 DEV_BAD_K = 5
 DEV_INCOMPLETE = 6
 DEV_DUP_SLOT = 7  # libgdn_debug.so only
+DEV_BAD_PAGE = 8
+DEV_NO_PAGES = 9
+DEV_BAD_LENGTH = 10
+DEV_BAD_PARENT = 11
 
 
 class GdnGeometry(ctypes.Structure):
@@ -56,6 +60,20 @@ class GdnGeometry(ctypes.Structure):
     ]
 
 
+class GdnAttnGeometry(ctypes.Structure):
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("max_tree", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, name: str, message: str):
         super().__init__(f"{name}: {message}")
@@ -66,6 +84,8 @@ class GdnError(RuntimeError):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
+_Z = ctypes.c_size_t
 _SIGS = {
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gdn_last_error": (ctypes.c_char_p, []),
@@ -90,6 +110,14 @@ _SIGS = {
                                           _P, _P, _P, _P, _P]),
     "gdn_commit_slots": (ctypes.c_int, [ctypes.POINTER(GdnGeometry), _P, _P, _P, _P, _I, _I, _P, _P, _P]),
     "gdn_prefill_timing_events": (ctypes.c_int, [_P, _P]),
+    "gdn_verify_tree_slots": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "gdn_check_attn_geometry": (ctypes.c_int, [_P, ctypes.c_char_p, _Z]),
+    "gdn_kv_plan": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "gdn_kv_write": (ctypes.c_int, [_P, _P, _P, _P, _L, _P, _L, _P, _I, _P, _P]),
+    "gdn_attn_prefill": (ctypes.c_int, [_P, _P, _L, _P, _L, _P, _L, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P, _P, _P]),
+    "gdn_attn_prefill_workspace_bytes": (_Z, [_P, _I, _I]),
+    "gdn_attn_tree": (ctypes.c_int, [_P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P, _P, _P]),
+    "gdn_attn_tree_workspace_bytes": (_Z, [_P, _I, _I]),
 }
 
 _lib = None
@@ -449,10 +477,255 @@ def checkpoint_count(seq_lens, ckpt_every: int) -> int:
     return sum(int(n) // ckpt_every for n in seq_lens)
 
 
+# --------------------------------------------------------------------------
+# verify over a tree of drafts
+# --------------------------------------------------------------------------
+
+def verify_tree_slots(geom: Geometry, pool: SlotPool, x, a, b, conv_w, slot, parent, snap_slot, o, dev_err=None,
+                      stream=None, k_row=None):
+    """gdn_verify_tree_slots: as verify_k_slots, but draft j of row i continues from draft parent[i][j]
+    (device int32 [batch][k]; -1: from the row's committed state); commit with commit_slots, accepted =
+    1 + the last accepted node.  Without a dev_err, device errors go to ``device_error``'s word."""
+    B, k = x.shape[0], x.shape[1]
+    C, Hv, dv = geom.conv_channels, geom.n_v_heads, geom.d_v
+    _check_pool(geom, pool)
+    _need(x, "x", (B, k, C), geom.dtype)
+    _need(a, "a", (B, k, Hv), geom.dtype)
+    _need(b, "b", (B, k, Hv), geom.dtype)
+    _need(conv_w, "conv_w", (C, geom.conv_width), torch.float32, optional=geom.conv_width == 0)
+    _need(slot, "slot", (B,), torch.int32)
+    _need(parent, "parent", (B, k), torch.int32)
+    _need(snap_slot, "snap_slot", (B, k), torch.int32)
+    _need(k_row, "k_row", (B,), torch.int32, optional=True)
+    _need(o, "o", (B, k, Hv, dv), geom.dtype)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
+    if dev_err is None:
+        dev_err = _default_err(x.device)
+    g = geom.c_struct()
+    _check(lib().gdn_verify_tree_slots(ctypes.byref(g), _ptr(pool.state), _ptr(pool.conv_state),
+                                       _ptr(pool.conv_pos), _ptr(x), _ptr(a), _ptr(b), _ptr(conv_w), _ptr(slot), B,
+                                       k, _ptr(k_row), _ptr(parent), _ptr(snap_slot), _ptr(o), _ptr(dev_err),
+                                       _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# the attention layers of a hybrid stack: paged KV cache and attention over it
+# --------------------------------------------------------------------------
+
+@dataclass(frozen=True)
+class AttnGeometry:
+    """Python mirror of gdn_attn_geometry (see include/gdn.h for every field); scale None: 1/sqrt(d_head)."""
+
+    n_q_heads: int = 24
+    n_kv_heads: int = 4
+    d_head: int = 256
+    page_tokens: int = 16
+    n_pages: int = 1024
+    max_pages: int = 1024
+    max_tree: int = 16
+    dtype: torch.dtype = torch.bfloat16
+    scale: Optional[float] = None
+
+    def c_struct(self) -> GdnAttnGeometry:
+        code = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}[self.dtype]
+        return GdnAttnGeometry(self.n_q_heads, self.n_kv_heads, self.d_head, self.page_tokens, self.n_pages,
+                               self.max_pages, self.max_tree, code,
+                               self.d_head ** -0.5 if self.scale is None else self.scale)
+
+    def check(self):
+        _check(lib().gdn_check_attn_geometry(self._ref(), None, 0))
+
+    def _ref(self):
+        """The C struct by reference, made once per geometry (it is frozen)."""
+        r = self.__dict__.get("_c_ref")
+        if r is None:
+            r = ctypes.byref(self.c_struct())
+            object.__setattr__(self, "_c_ref", r)
+        return r
+
+
+@dataclass
+class KVCache:
+    """Caller-owned K and V pages of one attention layer: dtype [n_pages][H_kv][page_tokens][d_head] each."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+
+    @staticmethod
+    def zeros(geom: AttnGeometry, device="cuda") -> "KVCache":
+        shape = (geom.n_pages, geom.n_kv_heads, geom.page_tokens, geom.d_head)
+        return KVCache(torch.zeros(shape, dtype=geom.dtype, device=device),
+                       torch.zeros(shape, dtype=geom.dtype, device=device))
+
+
+def _same_device(*named):
+    """Every tensor on the current device (the calls launch there): refused otherwise."""
+    cur = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name}: on {t.device}, required: the current device cuda:{cur}")
+
+
+def _need_rows(t: Optional[torch.Tensor], name: str, shape, dtype) -> int:
+    """Rows of heads, any row stride, contiguous within a row; returns the row stride in elements."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, required {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, required {tuple(shape)}")
+    st = t.stride()
+    D = shape[-1]
+    row = st[-3]
+    if shape[-3] == 1:  # one row per leading index: its stride says nothing
+        row = st[0] if len(shape) == 4 and shape[0] > 1 else shape[-2] * D
+    if (st[-1] != 1 or (st[-2] != D and shape[-2] > 1) or (len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * row)
+            or row < 0):
+        raise ValueError(f"{name}: strides {tuple(st)}, required: heads contiguous, rows one stride apart")
+    return row
+
+
+def _check_cache(geom: AttnGeometry, cache: KVCache):
+    shape = (geom.n_pages, geom.n_kv_heads, geom.page_tokens, geom.d_head)
+    _need(cache.k, "cache.k", shape, geom.dtype)
+    _need(cache.v, "cache.v", shape, geom.dtype)
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: must be a contiguous device tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kv_plan(geom: AttnGeometry, kv_len, new_len, free_pages, n_free, block_table, cu_new, slot_map, position,
+            kv_len_out, n_free_out, dev_err=None, stream=None):
+    """gdn_kv_plan: block tables, slot map and positions of the new tokens from the rows' lengths (new_len -1: the
+    row leaves and gives its pages back); slot_map and position may be longer than the new tokens (padding)."""
+    B, N = kv_len.shape[0], slot_map.shape[0]
+    i32 = torch.int32
+    _need(kv_len, "kv_len", (B,), i32)
+    _need(new_len, "new_len", (B,), i32)
+    _need(free_pages, "free_pages", (geom.n_pages,), i32)
+    _need(n_free, "n_free", (1,), i32)
+    _need(block_table, "block_table", (B, geom.max_pages), i32)
+    _need(cu_new, "cu_new", (B + 1,), i32)
+    _need(slot_map, "slot_map", (N,), i32)
+    _need(position, "position", (N,), i32)
+    _need(kv_len_out, "kv_len_out", (B,), i32)
+    _need(n_free_out, "n_free_out", (1,), i32)
+    _need(dev_err, "dev_err", (1,), i32, optional=True)
+    _same_device(("kv_len", kv_len), ("block_table", block_table), ("slot_map", slot_map))
+    if dev_err is None:
+        dev_err = _default_err(kv_len.device)
+    _check(lib().gdn_kv_plan(geom._ref(), kv_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
+                             n_free.data_ptr(), block_table.data_ptr(), B, N, cu_new.data_ptr(), slot_map.data_ptr(),
+                             position.data_ptr(), kv_len_out.data_ptr(), n_free_out.data_ptr(), dev_err.data_ptr(),
+                             _stream(stream)))
+
+
+def kv_write(geom: AttnGeometry, cache: KVCache, k, v, slot_map, dev_err=None, stream=None):
+    """gdn_kv_write: k and v rows [n_tokens][H_kv][d_head] (any row stride) into their cache slots; slot -1 skips."""
+    N = slot_map.shape[0]
+    shape = (N, geom.n_kv_heads, geom.d_head)
+    _check_cache(geom, cache)
+    ks = _need_rows(k, "k", shape, geom.dtype)
+    vs = _need_rows(v, "v", shape, geom.dtype)
+    _need(slot_map, "slot_map", (N,), torch.int32)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
+    _same_device(("cache.k", cache.k), ("k", k), ("v", v), ("slot_map", slot_map))
+    if dev_err is None:
+        dev_err = _default_err(k.device)
+    _check(lib().gdn_kv_write(geom._ref(), cache.k.data_ptr(), cache.v.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs,
+                              slot_map.data_ptr(), N, dev_err.data_ptr(), _stream(stream)))
+
+
+def attn_prefill_workspace_bytes(geom: AttnGeometry, n_tokens: int, n_seqs: int) -> int:
+    return int(lib().gdn_attn_prefill_workspace_bytes(geom._ref(), n_tokens, n_seqs))
+
+
+def alloc_attn_prefill_workspace(geom: AttnGeometry, n_tokens: int, n_seqs: int, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace of the size gdn_attn_prefill_workspace_bytes reports (may be empty)."""
+    return torch.empty(attn_prefill_workspace_bytes(geom, n_tokens, n_seqs), dtype=torch.uint8, device=device)
+
+
+def attn_prefill(geom: AttnGeometry, q, k, v, cu_seqlens, o, workspace=None, cache: Optional[KVCache] = None,
+                 block_table=None, ctx_len=None, dev_err=None, stream=None):
+    """gdn_attn_prefill: causal attention of packed prompts, q [n_tokens][H_q][d_head], k and v
+    [n_tokens][H_kv][d_head] (any row strides), sequence s after ctx_len[s] tokens that are in the cache already
+    (block table row s); ctx_len None: none.  Without a dev_err, device errors go to ``device_error``'s word."""
+    N, S = q.shape[0], cu_seqlens.shape[0] - 1
+    if S < 1:
+        raise ValueError("cu_seqlens: needs at least two entries")
+    qs = _need_rows(q, "q", (N, geom.n_q_heads, geom.d_head), geom.dtype)
+    ks = _need_rows(k, "k", (N, geom.n_kv_heads, geom.d_head), geom.dtype)
+    vs = _need_rows(v, "v", (N, geom.n_kv_heads, geom.d_head), geom.dtype)
+    _need(cu_seqlens, "cu_seqlens", (S + 1,), torch.int32)
+    _need(o, "o", (N, geom.n_q_heads, geom.d_head), geom.dtype)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
+    kc = vc = bt = cl = None
+    if ctx_len is not None:
+        if cache is None:
+            raise ValueError("cache: missing (ctx_len is given)")
+        _check_cache(geom, cache)
+        _need(block_table, "block_table", (S, geom.max_pages), torch.int32)
+        _need(ctx_len, "ctx_len", (S,), torch.int32)
+        _same_device(("cache.k", cache.k), ("block_table", block_table))
+        kc, vc, bt, cl = cache.k.data_ptr(), cache.v.data_ptr(), block_table.data_ptr(), ctx_len.data_ptr()
+    _same_device(("q", q), ("k", k), ("v", v), ("o", o), ("workspace", workspace))
+    ws, nbytes = _workspace(workspace)
+    if dev_err is None:
+        dev_err = _default_err(q.device)
+    _check(lib().gdn_attn_prefill(geom._ref(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                  cu_seqlens.data_ptr(), S, N, kc, vc, bt, cl, ws, nbytes, o.data_ptr(),
+                                  dev_err.data_ptr(), _stream(stream)))
+
+
+def attn_tree_workspace_bytes(geom: AttnGeometry, batch: int, n: int) -> int:
+    return int(lib().gdn_attn_tree_workspace_bytes(geom._ref(), batch, n))
+
+
+def alloc_attn_tree_workspace(geom: AttnGeometry, batch: int, n: int, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace of the size gdn_attn_tree_workspace_bytes reports (may be empty)."""
+    return torch.empty(attn_tree_workspace_bytes(geom, batch, n), dtype=torch.uint8, device=device)
+
+
+def attn_tree(geom: AttnGeometry, cache: KVCache, block_table, ctx_len, q, k, v, parent, o, workspace=None,
+              n_row=None, dev_err=None, stream=None):
+    """gdn_attn_tree: each row's n drafted nodes attend its ctx_len cached tokens, their ancestors among the drafts
+    (parent [batch][n], -1: the cached tokens) and themselves; q [batch][n][H_q][d_head], k and v
+    [batch][n][H_kv][d_head].  n = 1 with parent -1 is the decode step."""
+    B, n = q.shape[0], q.shape[1]
+    _check_cache(geom, cache)
+    qs = _need_rows(q, "q", (B, n, geom.n_q_heads, geom.d_head), geom.dtype)
+    ks = _need_rows(k, "k", (B, n, geom.n_kv_heads, geom.d_head), geom.dtype)
+    vs = _need_rows(v, "v", (B, n, geom.n_kv_heads, geom.d_head), geom.dtype)
+    _need(block_table, "block_table", (B, geom.max_pages), torch.int32)
+    _need(ctx_len, "ctx_len", (B,), torch.int32)
+    _need(parent, "parent", (B, n), torch.int32)
+    _need(n_row, "n_row", (B,), torch.int32, optional=True)
+    _need(o, "o", (B, n, geom.n_q_heads, geom.d_head), geom.dtype)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
+    _same_device(("cache.k", cache.k), ("q", q), ("k", k), ("v", v), ("o", o), ("workspace", workspace))
+    ws, nbytes = _workspace(workspace)
+    if dev_err is None:
+        dev_err = _default_err(q.device)
+    _check(lib().gdn_attn_tree(geom._ref(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, parent.data_ptr(),
+                               None if n_row is None else n_row.data_ptr(), B, n, cache.k.data_ptr(),
+                               cache.v.data_ptr(), block_table.data_ptr(), ctx_len.data_ptr(), ws, nbytes,
+                               o.data_ptr(), dev_err.data_ptr(), _stream(stream)))
+
+
 __all__ = [
     "Geometry", "GdnGeometry", "GdnError", "SlotPool", "lib", "conv_state_step", "decode_step", "verify_k",
     "rollback", "verify_k_slots", "commit_slots", "prefill_chunked", "prefill_chunked_static", "prefill_workspace_bytes", "alloc_prefill_workspace",
     "checkpoint_count", "POS_ONE", "CHUNK",
     "DEV_OK", "DEV_BAD_SLOT", "DEV_BAD_ACCEPTED", "DEV_BAD_SEQLENS", "DEV_WAIT_TIMEOUT", "DEV_BAD_K",
     "DEV_INCOMPLETE", "device_error",
+    "verify_tree_slots", "AttnGeometry", "GdnAttnGeometry", "KVCache", "kv_plan", "kv_write", "attn_prefill",
+    "attn_prefill_workspace_bytes", "alloc_attn_prefill_workspace", "attn_tree", "attn_tree_workspace_bytes",
+    "alloc_attn_tree_workspace", "DEV_BAD_PAGE", "DEV_NO_PAGES", "DEV_BAD_LENGTH", "DEV_BAD_PARENT",
 ]

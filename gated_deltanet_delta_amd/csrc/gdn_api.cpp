@@ -14,36 +14,16 @@
 #include <string>
 
 #include "gdn.h"
+#include "gdn_host.h"
 #include "gdn_internal.h"
 
 namespace {
 
 thread_local std::string g_last_error;
 
-// Debug builds check that a call's slot ids are distinct before its kernels.
-#ifdef GDN_DEBUG_CHECKS
-#define GDN_DEBUG_DISTINCT(name, a, na, b, nb, kb, k_row)                                               \
-  do {                                                                                                 \
-    const int e_ = gdn::launch_check_distinct(a, na, b, nb, kb, k_row, dev_err, stream);               \
-    if (e_ != 0) return fail(GDN_ERR_LAUNCH, "%s: HIP launch of the slot check failed with error %d", name, e_); \
-  } while (0)
-#else
-#define GDN_DEBUG_DISTINCT(name, a, na, b, nb, kb, k_row) \
-  do {                                                  \
-  } while (0)
-#endif
-// kernel-timing events of this thread's next prefill call (gdn_prefill_timing_events)
-thread_local void* g_prefill_ev[2] = {nullptr, nullptr};
-struct PrefillEvents {
-  void* start;
-  void* stop;
-};
-// A pending timing request, taken by the prefill call that begins now.
-PrefillEvents take_prefill_events() {
-  const PrefillEvents ev{g_prefill_ev[0], g_prefill_ev[1]};
-  g_prefill_ev[0] = g_prefill_ev[1] = nullptr;
-  return ev;
-}
+}  // namespace
+
+namespace gdn {
 
 gdn_status fail(gdn_status s, const char* fmt, ...) {
   char buf[512];
@@ -60,23 +40,31 @@ gdn_status ok() {
   return GDN_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+gdn_status launched(int err, const char* what) {
+  if (err != 0) return fail(GDN_ERR_LAUNCH, "%s: HIP launch failed with error %d", what, err);
+  return ok();
+}
 
-#define GDN_NEED_PTR(p, name)                                                     \
-  do {                                                                            \
-    if (!(p)) return fail(GDN_ERR_NULL, "%s: NULL, required: a device pointer", name); \
-    if (!aligned16(p))                                                            \
-      return fail(GDN_ERR_ALIGN, "%s: address %p, required: 16-byte aligned", name, \
-                  static_cast<const void*>(p));                                  \
-  } while (0)
+}  // namespace gdn
 
-#define GDN_NEED_PTR4(p, name)                                                    \
-  do {                                                                            \
-    if (!(p)) return fail(GDN_ERR_NULL, "%s: NULL, required: a device pointer", name); \
-    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)                               \
-      return fail(GDN_ERR_ALIGN, "%s: address %p, required: 4-byte aligned", name, \
-                  static_cast<const void*>(p));                                  \
-  } while (0)
+namespace {
+
+// kernel-timing events of this thread's next prefill call (gdn_prefill_timing_events)
+thread_local void* g_prefill_ev[2] = {nullptr, nullptr};
+struct PrefillEvents {
+  void* start;
+  void* stop;
+};
+// A pending timing request, taken by the prefill call that begins now.
+PrefillEvents take_prefill_events() {
+  const PrefillEvents ev{g_prefill_ev[0], g_prefill_ev[1]};
+  g_prefill_ev[0] = g_prefill_ev[1] = nullptr;
+  return ev;
+}
+
+using gdn::fail;
+using gdn::launched;
+using gdn::ok;
 
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -153,11 +141,6 @@ gdn::StepArgs step_args(const gdn_geometry* g) {
   a.q_scale = g->q_scale;
   a.l2_eps = g->l2_eps;
   return a;
-}
-
-gdn_status launched(int err, const char* what) {
-  if (err != 0) return fail(GDN_ERR_LAUNCH, "%s: HIP launch failed with error %d", what, err);
-  return ok();
 }
 
 gdn_status check_batch(int32_t batch, const gdn_geometry* g) {

@@ -1,0 +1,500 @@
+// Attention for gfx950: causal over packed prompts with cached prefixes, and
+// over a tree of drafts behind a paged cache.
+//
+//   s_rj = scale q_r . k_j,   o_r = sum_j e^(s_rj - m_r) v_j / sum_j e^(s_rj - m_r)
+//
+// in one pass over the keys: with the running maximum m and sum l of a row, a
+// tile of keys gives m' = max(m, max_j s_j), and O and l are scaled by
+// e^(m - m') before the tile's terms are added.  Exponentials are taken base 2
+// of logits scaled by scale log2(e).
+//
+// Rows of a sequence are its (token, query head) pairs for one KV head, token
+// major, so the query heads of a group share the K and V tiles; keys are the
+// sequence's cached tokens (through the block table) followed by its own.  The
+// products are formed transposed, S^T = K Q^T and O^T = V^T P^T: a query row is
+// then a column of every accumulator, its statistics are scalars of the lanes
+// that hold it, and the accumulators of P^T are the operand of the second
+// product as they are.
+//
+// With more than one split of the key axis each split writes its unscaled sums
+// with (m, l), and combine_kernel joins them in a fixed order.
+#include <type_traits>
+
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+namespace {
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// One sequence as a workgroup sees it.
+struct Seq {
+  int64_t row0;   // its first token among the call's
+  int32_t n;      // its tokens (0: nothing to do)
+  int32_t ctx;    // its cached tokens
+  int32_t index;  // block-table row
+};
+
+// Cached tokens of sequence s; false (and reported) if they do not fit the table.
+__device__ __forceinline__ bool seq_ctx(const AttnArgs& A, int s, int32_t* ctx, bool report) {
+  const int32_t c = A.ctx_len ? A.ctx_len[s] : 0;
+  *ctx = c;
+  if (c >= 0 && c <= static_cast<int64_t>(A.max_pages) * A.page) return true;
+  if (report) report_error(A.dev_err, GDN_DEV_BAD_LENGTH);
+  return false;
+}
+
+// Sequence s of a packed batch; n = 0 for one whose description is refused.
+__device__ __forceinline__ Seq packed_seq(const AttnArgs& A, int s, bool report) {
+  Seq q{0, 0, 0, s};
+  const int32_t t0 = A.cu_seqlens[s], t1 = A.cu_seqlens[s + 1];
+  if (t0 < 0 || t1 < t0 || t1 > A.n_tokens || A.cu_seqlens[0] != 0) {
+    if (report) report_error(A.dev_err, GDN_DEV_BAD_SEQLENS);
+    return q;
+  }
+  if (!seq_ctx(A, s, &q.ctx, report)) return q;
+  q.row0 = t0;
+  q.n = t1 - t0;
+  return q;
+}
+
+// Row s of a batch of trees (all lanes of a wave call it together); n = 0 for
+// one whose description is refused.  *path receives, in lane j, the bits of
+// node j's path (its ancestors and itself).
+__device__ __forceinline__ Seq tree_seq(const AttnArgs& A, int s, bool report, uint64_t* path) {
+  const int lane = threadIdx.x & (kWave - 1);
+  Seq q{0, 0, 0, s};
+  const int32_t n = A.n_row ? A.n_row[s] : A.nodes;
+  if (n < 1 || n > A.nodes) {
+    if (report) report_error(A.dev_err, GDN_DEV_BAD_K);
+    return q;
+  }
+  int par = lane < n ? A.parent[static_cast<size_t>(s) * A.nodes + lane] : -1;
+  if (__ballot(par < -1 || (lane < n && par >= lane)) != 0) {
+    if (report) report_error(A.dev_err, GDN_DEV_BAD_PARENT);
+    return q;
+  }
+  // pointer doubling: after step i, bits of the 2^(i+1) nearest nodes of the path
+  uint64_t bits = 1ull << lane;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const int src = par < 0 ? lane : par;
+    const uint32_t lo = __shfl(static_cast<uint32_t>(bits), src, kWave);
+    const uint32_t hi = __shfl(static_cast<uint32_t>(bits >> 32), src, kWave);
+    const int up = __shfl(par, src, kWave);
+    if (par >= 0) {
+      bits |= (static_cast<uint64_t>(hi) << 32) | lo;
+      par = up;
+    }
+  }
+  *path = bits;
+  if (!seq_ctx(A, s, &q.ctx, report)) return q;
+  q.row0 = static_cast<int64_t>(s) * A.nodes;
+  q.n = n;
+  return q;
+}
+
+// Row tiles of a packed batch: sequence s owns the tile ids from
+// floor(cu[s] G / BM) + s on, at least ceil(n_s G / BM) of them, so a tile id
+// finds its sequence without sums over the sequences before it.  Finds the
+// last s with a first id <= id (all lanes of a wave together).
+__device__ __forceinline__ int64_t tile_start(const AttnArgs& A, int s, int bm) {
+  const int64_t t = A.cu_seqlens[s];
+  return (t > 0 ? t : 0) * A.G / bm + s;
+}
+__device__ __forceinline__ int find_seq(const AttnArgs& A, int64_t id, int bm) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int s = 0;
+  for (int base = 0; base < A.n_seqs; base += kWave) {
+    const int i = base + lane;
+    const uint64_t m = __ballot(i < A.n_seqs && tile_start(A, i, bm) <= id);
+    if (m == 0) break;
+    s = base + 63 - __builtin_clzll(m);
+  }
+  return s;
+}
+
+// The address of the K (or V) row of key j: in its page, or among the call's rows.
+template <int ES>
+__device__ __forceinline__ const char* key_row(const AttnArgs& A, const Seq& q, const void* cache, const void* fresh,
+                                               int64_t stride, int kvh, int32_t j) {
+  if (j < q.ctx) {
+    const int32_t e = j / A.page, off = j - e * A.page;
+    int32_t page = A.block_table[static_cast<size_t>(q.index) * A.max_pages + e];
+    if (page < 0 || page >= A.n_pages) {
+      report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+      page = 0;
+    }
+    return static_cast<const char*>(cache) +
+           ((static_cast<size_t>(page) * A.Hk + kvh) * A.page + off) * static_cast<size_t>(A.D) * ES;
+  }
+  return static_cast<const char*>(fresh) +
+         ((q.row0 + (j - q.ctx)) * stride + static_cast<int64_t>(kvh) * A.D) * ES;
+}
+
+__device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Whether any of the 16 bytes' elements is an infinity or a NaN.
+template <bool BF16>
+__device__ __forceinline__ bool any_nonfinite(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+    else bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
+  }
+  return bad;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// The general kernel: 64 rows x 32 keys per step, four waves of 16 rows each,
+// K and V rows staged through LDS.  16x16 tiles: lane l holds rows (keys)
+// 4 (l / 16) + i of column (query row) l % 16.
+// ---------------------------------------------------------------------------
+constexpr int kGenRows = 64, kGenKeys = 32, kGenThreads = 256;
+
+template <int D, bool BF16>
+struct GenShape {
+  static constexpr int ES = BF16 ? 2 : 4;
+  static constexpr int VEC = 16 / ES;               // elements of a 16-byte vector
+  static constexpr int LD = D + VEC;                // LDS row, 16 bytes of padding against bank conflicts
+  static constexpr int VPR = D / VEC;               // vectors of a row
+  static constexpr int TILE_BYTES = kGenKeys * LD * ES;
+};
+
+template <int D, bool BF16, bool TREE>
+__global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
+  using Sh = GenShape<D, BF16>;
+  constexpr int ES = Sh::ES, LD = Sh::LD, NT = D / 16;
+  constexpr int QF = BF16 ? D / 32 : D / 4;  // k-steps of the logits
+  typedef typename std::conditional<BF16, uint16_t, float>::type E;
+  typedef typename std::conditional<BF16, bf16x8_t, float>::type Qf;
+  extern __shared__ __align__(16) char lds[];  // K tile, V tile, P of a tile (rare), flags
+  E* Ks = reinterpret_cast<E*>(lds);
+  E* Vs = reinterpret_cast<E*>(lds + Sh::TILE_BYTES);
+  float* Ps = reinterpret_cast<float*>(lds + 2 * Sh::TILE_BYTES);  // [4 waves][32 keys][16 rows]
+  uint32_t* bad_keys = reinterpret_cast<uint32_t*>(Ps + 4 * kGenKeys * 16);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, col = lane & 15, g = lane >> 4;
+  const int kvh = blockIdx.y, z = blockIdx.z;
+  const bool reporter = tid == 0;
+
+  // ---- the sequence and this tile's rows ----
+  Seq q;
+  uint64_t path = 0;
+  int64_t r0;
+  if constexpr (TREE) {
+    const int per = (A.nodes * A.G + kGenRows - 1) / kGenRows;
+    const int s = blockIdx.x / per;
+    r0 = static_cast<int64_t>(blockIdx.x - s * per) * kGenRows;
+    q = tree_seq(A, s, reporter, &path);
+  } else {
+    const int s = find_seq(A, blockIdx.x, kGenRows);
+    r0 = (blockIdx.x - tile_start(A, s, kGenRows)) * kGenRows;
+    q = packed_seq(A, s, reporter);
+  }
+  const int64_t rows = static_cast<int64_t>(q.n) * A.G;
+  if (q.n == 0 || r0 >= rows) return;
+  const int64_t r = r0 + wave * 16 + col;
+  const bool row_ok = r < rows;
+  const int t = static_cast<int>((row_ok ? r : r0) / A.G);   // this lane's token
+  const int head = kvh * A.G + static_cast<int>((row_ok ? r : r0) % A.G);
+  const int t_first = static_cast<int>(r0 / A.G);
+  const int64_t r_last = r0 + kGenRows < rows ? r0 + kGenRows - 1 : rows - 1;
+  const int t_last = static_cast<int>(r_last / A.G);
+  uint64_t my_path = 0;
+  if constexpr (TREE)
+    my_path = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(path >> 32), t, 64)) << 32) |
+              static_cast<uint32_t>(__shfl(static_cast<uint32_t>(path), t, 64));
+
+  // ---- this split's keys ----
+  const int32_t n_keys = TREE ? q.ctx + q.n : q.ctx + t_last + 1;  // both lengths are below 2^30
+  const int32_t tiles = (n_keys + kGenKeys - 1) / kGenKeys;
+  const int32_t per_split = (tiles + A.n_split - 1) / A.n_split;
+  const int32_t tile_lo = z * per_split, tile_hi = min(tile_lo + per_split, tiles);
+  const int32_t clear = TREE ? q.ctx : q.ctx + t_first + 1;        // keys every row of the tile attends
+
+  // ---- Q operand ----
+  Qf qf[QF];
+  {
+    const char* qp = static_cast<const char*>(A.q) + ((q.row0 + t) * A.q_stride + static_cast<int64_t>(head) * D) * ES;
+#pragma unroll
+    for (int s = 0; s < QF; ++s) {
+      if constexpr (BF16) qf[s] = *reinterpret_cast<const bf16x8_t*>(qp + (s * 32 + g * 8) * 2);
+      else qf[s] = *reinterpret_cast<const float*>(qp + (s * 4 + g) * 4);
+    }
+  }
+  f32x4_t O[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) O[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;  // l: this lane's part of the sum
+
+  for (int32_t kt = tile_lo; kt < tile_hi; ++kt) {
+    const int32_t key0 = kt * kGenKeys;
+    const bool masked = key0 + kGenKeys > clear;
+    __syncthreads();
+    if (masked && tid == 0) *bad_keys = 0;
+    if (masked) __syncthreads();
+    for (int e = tid; e < kGenKeys * Sh::VPR; e += kGenThreads) {
+      const int kr = e / Sh::VPR, w = e % Sh::VPR;
+      const int32_t j = key0 + kr;
+      uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
+      if (j < n_keys) {
+        kv = *reinterpret_cast<const uint4*>(key_row<ES>(A, q, A.k_cache, A.k, A.k_stride, kvh, j) + 16 * w);
+        vv = *reinterpret_cast<const uint4*>(key_row<ES>(A, q, A.v_cache, A.v, A.v_stride, kvh, j) + 16 * w);
+      }
+      if (masked && any_nonfinite<BF16>(vv)) atomicOr(bad_keys, 1u << kr);
+      *reinterpret_cast<uint4*>(Ks + kr * LD + w * Sh::VEC) = kv;
+      *reinterpret_cast<uint4*>(Vs + kr * LD + w * Sh::VEC) = vv;
+    }
+    __syncthreads();
+    // Values that are not finite must not reach rows that do not attend their
+    // key (0 x inf is NaN): such V rows leave the product and are added below.
+    uint32_t bad = 0;
+    if (masked) {
+      bad = *bad_keys;
+      if (bad) {
+        for (int e = tid; e < kGenKeys * Sh::VPR; e += kGenThreads)
+          if ((bad >> (e / Sh::VPR)) & 1u)
+            *reinterpret_cast<uint4*>(Vs + (e / Sh::VPR) * LD + (e % Sh::VPR) * Sh::VEC) = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+      }
+    }
+    // ---- logits, keys 16 kt2 + 4 g + i ----
+    float x[2][4];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2) {
+      f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+      const E* kr = Ks + (16 * k2 + col) * LD;
+#pragma unroll
+      for (int s = 0; s < QF; ++s) {
+        if constexpr (BF16) c = mfma_bf16(*reinterpret_cast<const bf16x8_t*>(kr + s * 32 + g * 8), qf[s], c);
+        else c = mfma_f32(kr[s * 4 + g], qf[s], c);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t j = key0 + 16 * k2 + 4 * g + i;
+        bool seen = true;
+        if (masked) {
+          const int32_t own = j - q.ctx;
+          if constexpr (TREE) seen = own < 0 || (own < q.n && ((my_path >> own) & 1ull));
+          else seen = own <= t;
+        }
+        x[k2][i] = seen ? c[i] * A.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, x[k2][i]);
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float m_new = fmaxf(m, mx);
+    const float ref = m_new == -INFINITY ? 0.f : m_new;  // no key seen yet: all weights 2^-inf = 0
+    const float scale = __builtin_amdgcn_exp2f(m - ref);
+    m = m_new;
+    l *= scale;
+    f32x4_t P[2];
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        P[k2][i] = __builtin_amdgcn_exp2f(x[k2][i] - ref);
+        l += P[k2][i];
+      }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) O[i] *= scale;
+    // ---- O^T += V^T P^T; the contraction runs over keys 4 g + i of both halves ----
+#pragma unroll
+    for (int dt = 0; dt < NT; ++dt) {
+      const E* vc = Vs + 4 * g * LD + 16 * dt + col;
+      if constexpr (BF16) {
+        bf16x8_t a, p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = __builtin_bit_cast(__bf16, vc[i * LD]);
+          a[4 + i] = __builtin_bit_cast(__bf16, vc[(16 + i) * LD]);
+          // weights rounded to bf16 for the matrix instruction: each is off by
+          // at most 2^-9 of itself, which their average over keys reduces
+          p[i] = static_cast<__bf16>(P[0][i]);
+          p[4 + i] = static_cast<__bf16>(P[1][i]);
+        }
+        O[dt] = mfma_bf16(a, p, O[dt]);
+      } else {
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) O[dt] = mfma_f32(vc[(16 * k2 + i) * LD], P[k2][i], O[dt]);
+      }
+    }
+    if (bad) {  // same for the whole workgroup
+      float* pw = Ps + wave * kGenKeys * 16;
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pw[(16 * k2 + 4 * g + i) * 16 + col] = P[k2][i];
+      __syncthreads();
+      for (uint32_t left = bad; left != 0; left &= left - 1) {
+        const int kr = __builtin_ctz(left);
+        const int32_t j = key0 + kr, own = j - q.ctx;
+        bool seen;
+        if constexpr (TREE) seen = own < 0 || (own < q.n && ((my_path >> own) & 1ull));
+        else seen = own <= t;
+        if (!seen) continue;  // also keys past the last
+        const char* vr = key_row<ES>(A, q, A.v_cache, A.v, A.v_stride, kvh, j);
+        const float p = pw[kr * 16 + col];
+#pragma unroll
+        for (int dt = 0; dt < NT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) O[dt][i] += p * load_in<BF16>(vr, 16 * dt + 4 * g + i);
+      }
+    }
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (!row_ok) return;
+  const size_t orow = static_cast<size_t>(q.row0 + t) * A.Hq + head;
+  if (A.n_split == 1) {
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int dt = 0; dt < NT; ++dt) {
+      const size_t at = orow * D + 16 * dt + 4 * g;
+      if constexpr (BF16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.o) + at) =
+            make_uint2(pack2_bf16(O[dt][0] * inv, O[dt][1] * inv), pack2_bf16(O[dt][2] * inv, O[dt][3] * inv));
+      else
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(A.o) + at) = O[dt] * inv;
+    }
+  } else {
+    const size_t part = orow * A.n_split + z;
+    float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
+    if (g == 0) {
+      ml[part * 2] = m;
+      ml[part * 2 + 1] = l;
+    }
+    if (tile_lo < tile_hi) {
+#pragma unroll
+      for (int dt = 0; dt < NT; ++dt)
+        *reinterpret_cast<f32x4_t*>(A.part + part * D + 16 * dt + 4 * g) = O[dt];
+    }
+  }
+}
+
+// Joins the splits of a row: weights 2^(m_z - max m), in the order of z.  D/4
+// lanes per row.  A split that saw no key (its m is -inf and its sum 0) wrote
+// no sums and is left out.
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
+  constexpr int LPR = D / 4, RPW = 256 / LPR;
+  const int c = (threadIdx.x % LPR) * 4;
+  const int64_t orow = static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / LPR;
+  const int64_t total = static_cast<int64_t>(A.n_tokens) * A.Hq;
+  const int64_t tok = (orow < total ? orow : total - 1) / A.Hq;
+  // rows that no workgroup computed (a refused sequence, padding) stay as they are
+  bool live = orow < total;
+  if (A.nodes > 0) {
+    // the wave's rows may belong to several trees: each is checked by the whole wave
+    const int s = static_cast<int>(tok / A.nodes);
+    const int node = static_cast<int>(tok - static_cast<int64_t>(s) * A.nodes);
+    uint64_t todo = __ballot(true);
+    bool ok = false;
+    while (todo != 0) {
+      const int leader = __builtin_ctzll(todo);
+      const int sl = __builtin_amdgcn_readlane(s, leader);
+      uint64_t path;
+      const Seq q = tree_seq(A, sl, false, &path);
+      if (s == sl) ok = node < q.n;
+      todo &= ~__ballot(s == sl);
+    }
+    live &= ok;
+  } else {
+    int lo = 0, hi = A.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (A.cu_seqlens[mid] <= tok) lo = mid;
+      else hi = mid;
+    }
+    const Seq q = packed_seq(A, lo, false);
+    live &= q.n > 0 && tok >= q.row0 && tok < q.row0 + q.n;
+  }
+  if (!live) return;
+  const float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D +
+                    static_cast<size_t>(orow) * A.n_split * 2;
+  float m = -INFINITY;
+  for (int z = 0; z < A.n_split; ++z) m = fmaxf(m, ml[2 * z]);
+  const float ref = m == -INFINITY ? 0.f : m;
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int z = 0; z < A.n_split; ++z) {
+    const float mz = ml[2 * z], lz = ml[2 * z + 1];
+    if (mz == -INFINITY && lz == 0.f) continue;
+    const float w = __builtin_amdgcn_exp2f(mz - ref);
+    l += w * lz;
+    sum += w * load4(A.part + (static_cast<size_t>(orow) * A.n_split + z) * D + c);
+  }
+  sum *= 1.0f / l;
+  const size_t at = static_cast<size_t>(orow) * D + c;
+  if constexpr (BF16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.o) + at) =
+        make_uint2(pack2_bf16(sum[0], sum[1]), pack2_bf16(sum[2], sum[3]));
+  else
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(A.o) + at) = sum;
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+namespace {
+
+// Row tiles (per KV head) of a call.
+int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
+  if (nodes > 0) return static_cast<int64_t>(n_seqs) * ((static_cast<int64_t>(nodes) * G + bm - 1) / bm);
+  return tokens * G / bm + n_seqs;
+}
+
+}  // namespace
+
+int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
+  // two workgroups per CU, and at most 64 parts to join
+  const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, kGenRows) * Hk;
+  const int64_t want = wgs > 0 ? 512 / wgs : 1;
+  return static_cast<int>(want < 1 ? 1 : (want > 64 ? 64 : want));
+}
+
+template <int D, bool BF16>
+static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
+  using Sh = GenShape<D, BF16>;
+  const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, kGenRows);
+  if (tiles > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
+  const dim3 grid(static_cast<unsigned>(tiles), a.Hk, a.n_split);
+  const size_t lds = 2 * Sh::TILE_BYTES + 4 * kGenKeys * 16 * sizeof(float) + 16;
+  if (a.nodes > 0) hipLaunchKernelGGL((attn_general_kernel<D, BF16, true>), grid, dim3(kGenThreads), lds, s, a);
+  else hipLaunchKernelGGL((attn_general_kernel<D, BF16, false>), grid, dim3(kGenThreads), lds, s, a);
+  int e = static_cast<int>(hipGetLastError());
+  if (e == 0 && a.n_split > 1) {
+    const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.Hq, per = 256 / (D / 4);
+    hipLaunchKernelGGL((attn_combine_kernel<D, BF16>), dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256),
+                       0, s, a);
+    e = static_cast<int>(hipGetLastError());
+  }
+  return e;
+}
+
+int launch_attn(const AttnArgs& a, bool bf16, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (a.D) {
+    case 64: return bf16 ? launch_attn_t<64, true>(a, s) : launch_attn_t<64, false>(a, s);
+    case 128: return bf16 ? launch_attn_t<128, true>(a, s) : launch_attn_t<128, false>(a, s);
+    case 256: return bf16 ? launch_attn_t<256, true>(a, s) : launch_attn_t<256, false>(a, s);
+    default: return static_cast<int>(hipErrorInvalidValue);
+  }
+}
+
+}  // namespace gdn

@@ -85,11 +85,12 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 7  /* 4: prefill on the caller's stream alone, workspace independent of n_tokens,
+#define GDN_ABI_VERSION 8  /* 4: prefill on the caller's stream alone, workspace independent of n_tokens,
                               checkpoints at any block size, GDN_DEV_INCOMPLETE;
                               5: gdn_prefill_chunked_static;
                               6: gdn_prefill_timing_events;
-                              7: GDN_DEV_DUP_SLOT (debug builds) */
+                              7: GDN_DEV_DUP_SLOT (debug builds);
+                              8: the paged KV cache and the attention over it, verify over a tree of drafts */
 /* bytes of the library's own prefill workspace, one per GPU (gdn_prefill_chunked_static) */
 #define GDN_PREFILL_STATIC_WORKSPACE_BYTES ((size_t)64 << 20)
 #define GDN_POS_ONE 65536
@@ -116,6 +117,10 @@ typedef enum gdn_status {
 #define GDN_DEV_INCOMPLETE 6     /* prefill: part of the work was never picked up by a workgroup; outputs invalid */
 #define GDN_DEV_DUP_SLOT 7       /* two rows of one call name the same slot; written only by a library built with
                                     GDN_DEBUG_CHECKS (libgdn_debug.so), which checks this before each call's kernels */
+#define GDN_DEV_BAD_PAGE 8       /* a page id, cache slot or free-page count outside the cache */
+#define GDN_DEV_NO_PAGES 9       /* gdn_kv_plan: the free pages do not suffice for every row */
+#define GDN_DEV_BAD_LENGTH 10    /* a cached or new length that is negative or does not fit the row's block table */
+#define GDN_DEV_BAD_PARENT 11    /* a tree node's parent outside [-1, node) */
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 
@@ -394,6 +399,168 @@ gdn_status gdn_verify_k_slots(const gdn_geometry* g, float* state, float* conv_s
 gdn_status gdn_commit_slots(const gdn_geometry* g, const int32_t* slot, const int32_t* k_row,
                             const int32_t* snap_slot, const int32_t* accepted, int32_t batch, int32_t k,
                             int32_t* next_slot, int32_t* dev_err, void* stream);
+
+/*
+ * Verify over a TREE of drafts: gdn_verify_k_slots with a parent per draft.
+ * Node j of row i continues from the state and the conv window of node
+ * parent[i][j] (device int32 [batch][k], -1 <= parent[i][j] < j), or from the
+ * committed ones of slot[i] for -1, so several continuations of one prefix are
+ * verified in one call.  The same per-token math:
+ *   S_j = alpha_j S_p (I - beta_j k_j k_j^T) + beta_j v_j k_j^T, o_j = q_scale S_j q_j,
+ * with S_p the parent's state.  Node j's whole slot goes to snap_slot[i][j]:
+ *   state[s_j]      = S_j,
+ *   conv ring of s_j = the W-1 inputs up to node j along its path (committed
+ *                      history before them), at their ring rows,
+ *   conv_pos[s_j]   = p + depth(j) tokens (depth 1 for a node whose parent is -1).
+ * slot[i]'s state, ring and position are not modified (unlike
+ * gdn_verify_k_slots, which writes the drafts' inputs into slot[i]'s ring).  A
+ * chain (parent[i][j] = j-1) gives gdn_verify_k_slots' snapshots and outputs,
+ * bit for bit.  Commit with gdn_commit_slots, accepted[i] = 1 + the last
+ * accepted node (0: none).
+ * A parent out of range sets GDN_DEV_BAD_PARENT and the row is skipped, as is
+ * a row whose slot id or draft count is out of range.  A snapshot slot id out
+ * of range sets GDN_DEV_BAD_SLOT; that snapshot is not written, and neither
+ * are the outputs and snapshots of the node's descendants.
+ * All other arguments, layouts and errors as gdn_verify_k_slots.
+ */
+gdn_status gdn_verify_tree_slots(const gdn_geometry* g, float* state, float* conv_state, int32_t* conv_pos,
+                                 const void* x, const void* a, const void* b, const float* conv_w,
+                                 const int32_t* slot, int32_t batch, int32_t k, const int32_t* k_row,
+                                 const int32_t* parent, const int32_t* snap_slot, void* o, int32_t* dev_err,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * The attention layers of a hybrid stack: a paged KV cache, the tables that
+ * lead into it, and attention over it.
+ *
+ *  k_cache, v_cache  dtype  [n_pages][H_kv][P][D]     P = page_tokens
+ *  block_table       int32  [batch][max_pages]        entry e of row i: the page of the row's tokens eP .. eP+P-1
+ *  cache slot        int32  page * P + offset         one token's place in the cache (all heads)
+ *  q                 dtype  [rows][H_q][D]            rows q_stride elements apart
+ *  k, v              dtype  [rows][H_kv][D]           rows k_stride / v_stride elements apart
+ *  o                 dtype  [rows][H_q][D]            contiguous
+ *
+ * Query head h reads KV head h / (H_q / H_kv).  Row strides let q, k and v be
+ * the parts of one fused projection row; they are multiples of 16 bytes.
+ * Logits, softmax statistics and outputs are accumulated in fp32; with
+ * GDN_BF16 the softmax weights are rounded to bf16 for the product with V
+ * (an error below the output's own rounding).  K and V rows at masked
+ * positions do not enter a result, whatever they hold (infinities and NaN too).
+ * A page may belong to several rows (a shared prefix) as long as only its
+ * full part is shared; the library keeps no reference counts.
+ * The general conventions above hold: caller-owned buffers, no allocation, no
+ * synchronisation, first device error wins.
+ * ------------------------------------------------------------------------ */
+typedef struct gdn_attn_geometry {
+  int32_t n_q_heads;   /* H_q, a multiple of H_kv */
+  int32_t n_kv_heads;  /* H_kv */
+  int32_t d_head;      /* D: 64, 128 or 256 */
+  int32_t page_tokens; /* P, a multiple of 16 */
+  int32_t n_pages;     /* pages of the cache; n_pages * P <= 2^31 - 1 */
+  int32_t max_pages;   /* entries of a block-table row; max_pages * P < 2^30 */
+  int32_t max_tree;    /* largest node count accepted by gdn_attn_tree (1..64) */
+  int32_t dtype;       /* gdn_dtype of q, k, v, o and of the cache */
+  float scale;         /* logits are scale * q.k; finite and > 0 */
+} gdn_attn_geometry;
+
+/* gdn_check_geometry for the attention geometry. */
+gdn_status gdn_check_attn_geometry(const gdn_attn_geometry* g, char* msg, size_t msg_len);
+
+/*
+ * Block tables and slot maps from the requests' lengths, on the GPU: the host
+ * needs to know neither page ids nor the free list, and the call can sit in a
+ * captured graph.  Row i has kv_len[i] cached tokens and gets new_len[i] more
+ * (device int32 [batch]); new_len[i] = 0 idles, new_len[i] = -1 leaves and gives
+ * its ceil(kv_len / P) pages back.
+ *   free_pages int32 [n_pages], n_free int32 [1]: the free pages, a stack.  The
+ *     leaving rows' pages are pushed first (written at free_pages[n_free ..],
+ *     rows in order); then rows in order take their
+ *     ceil((kv_len + new_len) / P) - ceil(kv_len / P) new pages from its top.
+ *   block_table [batch][max_pages]: new pages are written behind the row's
+ *     entries in use; all others are left as they are.
+ *   cu_new [batch+1] int32: exclusive sums of max(new_len, 0), no value above max_tokens.
+ *   slot_map, position [max_tokens] int32: cache slot and position in its
+ *     request of every new token, rows packed in order; slot -1 and position 0
+ *     behind the last one, so a padded batch runs through gdn_kv_write.
+ *   kv_len_out [batch], n_free_out [1]: the lengths and the free count after the call.
+ * Inputs are not modified (n_free and n_free_out, kv_len and kv_len_out are
+ * different buffers), so a call can be repeated.
+ * Rows whose pages the stack cannot supply set GDN_DEV_NO_PAGES and get none:
+ * their tokens' slots are -1 and kv_len_out[i] = kv_len[i]; rows that need no
+ * new page still succeed.  A negative kv_len, new_len < -1 or a sum beyond
+ * max_pages * P sets GDN_DEV_BAD_LENGTH and the row is treated the same way.
+ * GDN_DEV_BAD_SEQLENS: the new tokens exceed max_tokens; the excess is not
+ * mapped.  GDN_DEV_BAD_PAGE: n_free outside [0, n_pages] or more pages on the
+ * stack than the cache has (the call then writes nothing but slots -1,
+ * positions 0, cu_new, kv_len_out = kv_len and n_free_out = n_free), or a page
+ * id outside the cache (that token's slot is -1).
+ * 1 <= batch <= 4096, 0 <= max_tokens.
+ */
+gdn_status gdn_kv_plan(const gdn_attn_geometry* g, const int32_t* kv_len, const int32_t* new_len,
+                       int32_t* free_pages, const int32_t* n_free, int32_t* block_table, int32_t batch,
+                       int32_t max_tokens, int32_t* cu_new, int32_t* slot_map, int32_t* position,
+                       int32_t* kv_len_out, int32_t* n_free_out, int32_t* dev_err, void* stream);
+
+/*
+ * K and V rows of n_tokens tokens into the cache: k_cache[page][h][offset] =
+ * k[t][h] for slot_map[t] = page * P + offset, v likewise.  Slot -1 is
+ * skipped (padding, rejected drafts); any other slot outside the cache sets
+ * GDN_DEV_BAD_PAGE and is skipped.  Equal slots in one call race.
+ */
+gdn_status gdn_kv_write(const gdn_attn_geometry* g, void* k_cache, void* v_cache, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const int32_t* slot_map, int32_t n_tokens,
+                        int32_t* dev_err, void* stream);
+
+/*
+ * Causal attention over packed prompts: sequence s is rows [cu_seqlens[s],
+ * cu_seqlens[s+1]) of q, k, v and o (cu_seqlens int32 [n_seqs+1], device), and
+ * follows ctx_len[s] tokens in the cache, block table row s (a prefix restored
+ * or prefilled before; ctx_len NULL: none, then k_cache, v_cache and
+ * block_table are not used and may be NULL).  Token t of the sequence attends
+ * the ctx_len[s] cached tokens and rows 0..t of its own k and v; these rows are
+ * read from k and v, whether or not they are in the cache already.
+ * Sequences may be empty; rows of o behind cu_seqlens[n_seqs] <= n_tokens are
+ * left as they are.
+ *   0 <= n_tokens < 2^30.
+ *   workspace: device, >= gdn_attn_prefill_workspace_bytes() (0 where no
+ *   workspace is needed; then it may be NULL).  Calls that share a workspace
+ *   must be ordered on one stream.
+ * Device errors: GDN_DEV_BAD_SEQLENS (cu_seqlens[0] != 0, decreasing, or the
+ * last > n_tokens) and GDN_DEV_BAD_LENGTH (ctx_len outside [0, max_pages * P])
+ * skip the sequence; GDN_DEV_BAD_PAGE: a page id outside the cache, the
+ * sequence's outputs are then not valid.
+ */
+gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_seqlens,
+                            int32_t n_seqs, int32_t n_tokens, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* ctx_len, void* workspace,
+                            size_t workspace_bytes, void* o, int32_t* dev_err, void* stream);
+size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_geometry* g, int32_t n_tokens, int32_t n_seqs);
+
+/*
+ * Attention of a tree of n drafted tokens per row over the cache: node j of row
+ * i attends the row's ctx_len[i] cached tokens, its ancestors among the row's
+ * drafts (parent [batch][n] int32, -1 <= parent[i][j] < j; -1: the node follows
+ * the cached tokens) and itself.  n = 1 with parent -1 is the decode step.
+ *   q [batch][n][H_q][D], k, v [batch][n][H_kv][D] (consecutive nodes one row
+ *   stride apart, row i starting at node i n), o [batch][n][H_q][D].
+ * The drafts' k and v are read from k and v, not from the cache: only what is
+ * accepted is written there, afterwards (gdn_kv_write with slot -1 for the
+ * other nodes).  n_row (int32 [batch], or NULL for n): row i's own node count
+ * in 1..n; later nodes are neither read nor written.
+ *   workspace: device, >= gdn_attn_tree_workspace_bytes(); calls that share a
+ *   workspace must be ordered on one stream.
+ *   1 <= batch, 1 <= n <= max_tree.
+ * Device errors: GDN_DEV_BAD_K (n_row), GDN_DEV_BAD_PARENT and
+ * GDN_DEV_BAD_LENGTH skip the row; GDN_DEV_BAD_PAGE: a page id outside the
+ * cache, the row's outputs are then not valid.
+ */
+gdn_status gdn_attn_tree(const gdn_attn_geometry* g, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, const int32_t* parent,
+                         const int32_t* n_row, int32_t batch, int32_t n, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* ctx_len, void* workspace,
+                         size_t workspace_bytes, void* o, int32_t* dev_err, void* stream);
+size_t gdn_attn_tree_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n);
 
 #ifdef __cplusplus
 }
