@@ -23,7 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 LIB_DEBUG = os.path.join(PKG, "libgdn_debug.so")
 
-HIP_SOURCES = ["gdn_step.hip", "gdn_prefill.hip", "gdn_tree.hip", "gdn_kv.hip", "gdn_attn.hip"]
+HIP_SOURCES = ["gdn_step.hip", "gdn_prefill.hip", "gdn_tree.hip", "gdn_kv.hip", "gdn_attn.hip", "gdn_flash.hip"]
 HOST_SOURCES = ["gdn_api.cpp", "gdn_attn_api.cpp"]
 
 HIPCC_FLAGS = [
@@ -32,6 +32,7 @@ HIPCC_FLAGS = [
     # packed fp32 instructions are kept out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
+    "-Wno-inline-asm",  # m0 in a clobber list
     # MFMA accumulators in VGPRs: the chained products feed them straight to VALU
     # code and the next MFMA, so AGPR<->VGPR copies would only add instructions
     "-mllvm", "-amdgpu-mfma-vgpr-form",

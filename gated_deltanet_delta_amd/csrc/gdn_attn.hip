@@ -20,138 +20,17 @@
 // with (m, l), and combine_kernel joins them in a fixed order.
 #include <type_traits>
 
-#include "gdn_device.h"
-#include "gdn_internal.h"
+#include "gdn_attn_device.h"
 
 namespace gdn {
 
 namespace {
-
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
-// One sequence as a workgroup sees it.
-struct Seq {
-  int64_t row0;   // its first token among the call's
-  int32_t n;      // its tokens (0: nothing to do)
-  int32_t ctx;    // its cached tokens
-  int32_t index;  // block-table row
-};
-
-// Cached tokens of sequence s; false (and reported) if they do not fit the table.
-__device__ __forceinline__ bool seq_ctx(const AttnArgs& A, int s, int32_t* ctx, bool report) {
-  const int32_t c = A.ctx_len ? A.ctx_len[s] : 0;
-  *ctx = c;
-  if (c >= 0 && c <= static_cast<int64_t>(A.max_pages) * A.page) return true;
-  if (report) report_error(A.dev_err, GDN_DEV_BAD_LENGTH);
-  return false;
-}
-
-// Sequence s of a packed batch; n = 0 for one whose description is refused.
-__device__ __forceinline__ Seq packed_seq(const AttnArgs& A, int s, bool report) {
-  Seq q{0, 0, 0, s};
-  const int32_t t0 = A.cu_seqlens[s], t1 = A.cu_seqlens[s + 1];
-  if (t0 < 0 || t1 < t0 || t1 > A.n_tokens || A.cu_seqlens[0] != 0) {
-    if (report) report_error(A.dev_err, GDN_DEV_BAD_SEQLENS);
-    return q;
-  }
-  if (!seq_ctx(A, s, &q.ctx, report)) return q;
-  q.row0 = t0;
-  q.n = t1 - t0;
-  return q;
-}
-
-// Row s of a batch of trees (all lanes of a wave call it together); n = 0 for
-// one whose description is refused.  *path receives, in lane j, the bits of
-// node j's path (its ancestors and itself).
-__device__ __forceinline__ Seq tree_seq(const AttnArgs& A, int s, bool report, uint64_t* path) {
-  const int lane = threadIdx.x & (kWave - 1);
-  Seq q{0, 0, 0, s};
-  const int32_t n = A.n_row ? A.n_row[s] : A.nodes;
-  if (n < 1 || n > A.nodes) {
-    if (report) report_error(A.dev_err, GDN_DEV_BAD_K);
-    return q;
-  }
-  int par = lane < n ? A.parent[static_cast<size_t>(s) * A.nodes + lane] : -1;
-  if (__ballot(par < -1 || (lane < n && par >= lane)) != 0) {
-    if (report) report_error(A.dev_err, GDN_DEV_BAD_PARENT);
-    return q;
-  }
-  // pointer doubling: after step i, bits of the 2^(i+1) nearest nodes of the path
-  uint64_t bits = 1ull << lane;
-#pragma unroll
-  for (int i = 0; i < 6; ++i) {
-    const int src = par < 0 ? lane : par;
-    const uint32_t lo = __shfl(static_cast<uint32_t>(bits), src, kWave);
-    const uint32_t hi = __shfl(static_cast<uint32_t>(bits >> 32), src, kWave);
-    const int up = __shfl(par, src, kWave);
-    if (par >= 0) {
-      bits |= (static_cast<uint64_t>(hi) << 32) | lo;
-      par = up;
-    }
-  }
-  *path = bits;
-  if (!seq_ctx(A, s, &q.ctx, report)) return q;
-  q.row0 = static_cast<int64_t>(s) * A.nodes;
-  q.n = n;
-  return q;
-}
-
-// Row tiles of a packed batch: sequence s owns the tile ids from
-// floor(cu[s] G / BM) + s on, at least ceil(n_s G / BM) of them, so a tile id
-// finds its sequence without sums over the sequences before it.  Finds the
-// last s with a first id <= id (all lanes of a wave together).
-__device__ __forceinline__ int64_t tile_start(const AttnArgs& A, int s, int bm) {
-  const int64_t t = A.cu_seqlens[s];
-  return (t > 0 ? t : 0) * A.G / bm + s;
-}
-__device__ __forceinline__ int find_seq(const AttnArgs& A, int64_t id, int bm) {
-  const int lane = threadIdx.x & (kWave - 1);
-  int s = 0;
-  for (int base = 0; base < A.n_seqs; base += kWave) {
-    const int i = base + lane;
-    const uint64_t m = __ballot(i < A.n_seqs && tile_start(A, i, bm) <= id);
-    if (m == 0) break;
-    s = base + 63 - __builtin_clzll(m);
-  }
-  return s;
-}
-
-// The address of the K (or V) row of key j: in its page, or among the call's rows.
-template <int ES>
-__device__ __forceinline__ const char* key_row(const AttnArgs& A, const Seq& q, const void* cache, const void* fresh,
-                                               int64_t stride, int kvh, int32_t j) {
-  if (j < q.ctx) {
-    const int32_t e = j / A.page, off = j - e * A.page;
-    int32_t page = A.block_table[static_cast<size_t>(q.index) * A.max_pages + e];
-    if (page < 0 || page >= A.n_pages) {
-      report_error(A.dev_err, GDN_DEV_BAD_PAGE);
-      page = 0;
-    }
-    return static_cast<const char*>(cache) +
-           ((static_cast<size_t>(page) * A.Hk + kvh) * A.page + off) * static_cast<size_t>(A.D) * ES;
-  }
-  return static_cast<const char*>(fresh) +
-         ((q.row0 + (j - q.ctx)) * stride + static_cast<int64_t>(kvh) * A.D) * ES;
-}
 
 __device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// Whether any of the 16 bytes' elements is an infinity or a NaN.
-template <bool BF16>
-__device__ __forceinline__ bool any_nonfinite(uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF16) bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-    else bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
-  }
-  return bad;
 }
 
 }  // namespace
@@ -463,7 +342,7 @@ int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
 
 int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
   // two workgroups per CU, and at most 64 parts to join
-  const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, kGenRows) * Hk;
+  const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kFlashRows : kGenRows) * Hk;
   const int64_t want = wgs > 0 ? 512 / wgs : 1;
   return static_cast<int>(want < 1 ? 1 : (want > 64 ? 64 : want));
 }
@@ -475,7 +354,10 @@ static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
   if (tiles > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
   const dim3 grid(static_cast<unsigned>(tiles), a.Hk, a.n_split);
   const size_t lds = 2 * Sh::TILE_BYTES + 4 * kGenKeys * 16 * sizeof(float) + 16;
-  if (a.nodes > 0) hipLaunchKernelGGL((attn_general_kernel<D, BF16, true>), grid, dim3(kGenThreads), lds, s, a);
+  if (BF16 && a.nodes == 0) {
+    const int e = launch_flash_prefill(a, row_tiles(a.n_tokens, a.n_seqs, a.G, 0, kFlashRows), s);
+    if (e != 0) return e;
+  } else if (a.nodes > 0) hipLaunchKernelGGL((attn_general_kernel<D, BF16, true>), grid, dim3(kGenThreads), lds, s, a);
   else hipLaunchKernelGGL((attn_general_kernel<D, BF16, false>), grid, dim3(kGenThreads), lds, s, a);
   int e = static_cast<int>(hipGetLastError());
   if (e == 0 && a.n_split > 1) {

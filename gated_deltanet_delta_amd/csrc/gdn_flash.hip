@@ -1,0 +1,465 @@
+// Attention in bf16 for gfx950 (the formulas and the row and key order:
+// gdn_attn.hip): 32x32x16 matrix instructions on key tiles that the waves of a
+// workgroup share through LDS.
+//
+// A wave owns 32 rows.  S^T = K Q^T takes K as the A operand from LDS and Q^T
+// from registers; lane l then holds row l % 32 and keys 8 (i / 4) + 4 (l / 32) +
+// i % 4 of a block of 32.  O^T = V^T P^T contracts 16 keys per instruction: lane
+// l's eight weights of one instruction are its accumulators 8 ks .. 8 ks + 7 as
+// they are, and V^T's operand is read out of the V tile in the same key order
+// with transposing LDS reads (ds_read_b64_tr_b16).
+//
+// Tiles of 64 keys go from memory to LDS without passing registers
+// (global_load_lds, 16 bytes per lane), the next tile's loads in flight while
+// this one is used.  Rows lie unpadded in LDS, their 16-byte chunks permuted by
+// an XOR with row bits so that both kinds of reads hit all banks: K reads take
+// one chunk of 16 consecutive rows (chunk ^ row % 16), transposing reads four
+// chunks of four consecutive rows (chunk ^ 4 (row % 4)).
+#include "gdn_attn_device.h"
+
+namespace gdn {
+
+namespace {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kKeys = 64;  // keys of a tile
+constexpr int kSchedMfma = 0x8, kSchedLds = 0x100;  // instruction classes of sched_group_barrier: MFMA, LDS reads
+
+// 16 bytes per lane from memory to LDS at `lds` + 16 lane (lds: a byte address,
+// the same in every lane).  Written out because the compiler, which cannot
+// tell the two halves of the double buffer apart, would wait for these loads
+// before every LDS read.  There is no register to return to; the readers are
+// ordered by tile_ready().
+__device__ __forceinline__ void load_lds16(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
+}
+// This wave's loads have landed; then every wave's have, and every wave is
+// done with what it read before.
+__device__ __forceinline__ void tile_ready() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(p)));
+}
+
+__device__ __forceinline__ f32x16_t mfma32x32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// max / sum over the two lanes l and l ^ 32
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+}  // namespace
+
+// RW waves of 32 rows each, times KW waves that share a row block and take
+// 64 / KW keys of every tile each.
+template <int D, int RW, int KW, bool TREE>
+struct Flash {
+  static constexpr int NW = RW * KW, THREADS = 64 * NW, BM = 32 * RW;
+  static constexpr int ROW_BYTES = D * 2;
+  static constexpr int TILE = kKeys * ROW_BYTES;         // K or V of a tile
+  static constexpr int BUF = 2 * TILE;
+  static constexpr int NS = D / 16, NT = D / 32;         // k-steps of the logits, 32-row tiles of O^T
+  static constexpr int KB = 2 / KW;                      // 32-key blocks per wave and tile
+  static constexpr int RPI = 1024 / ROW_BYTES;           // rows of one load instruction
+  static constexpr int WROWS = kKeys / NW;               // rows a wave loads
+  static constexpr int LPR = 64 / RPI;                   // lanes per row
+  static constexpr int CH = D / 8;                       // 16-byte chunks of a row
+  static constexpr int KX = D >= 128 ? 15 : 7;           // bits of the K permutation
+  // LDS: two buffers, then flags (two words: keys whose V row is not finite)
+  static constexpr size_t LDS_TILES = 2 * static_cast<size_t>(BUF);
+  static constexpr size_t LDS = LDS_TILES + 16;
+
+  __device__ static int k_perm(int row) { return D >= 128 ? row & 15 : (row >> 1) & 7; }
+  __device__ static int v_perm(int row) { return D >= 128 ? (row & 3) * 4 : ((row >> 1) & 1) * 4; }
+
+  const AttnArgs& A;
+  char* lds;
+  uint32_t lds0;
+  int lane, wave, rw, kw, col, half;
+  // the unit of work: one KV head of one sequence, a block of rows
+  Seq q;
+  int kvh;
+  bool row_ok;
+  int t, head;         // this lane's token and query head
+  uint64_t path;       // TREE: this lane's row's nodes
+  int32_t n_keys, clear;
+  // base rows of the cached tokens, one 16-row group per lane: lane i holds
+  // ((page * H_kv + kvh) P + offset) of key 1024 ids_at + 16 i
+  int32_t ids_at;
+  int64_t ids;
+  bf16x8_t qf[NS];
+  f32x16_t O[NT];
+  float m, l;          // running maximum (of unscaled logits), this lane's part of the sum
+
+  __device__ Flash(const AttnArgs& a, char* smem) : A(a), lds(smem) {
+    lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    rw = wave / KW;
+    kw = wave % KW;
+    col = lane & 31;
+    half = lane >> 5;
+  }
+
+  // Rows r0 .. r0 + BM - 1 (of n G) of KV head h; q and (TREE) the lane's paths are set.
+  __device__ void begin(int64_t r0, int h, uint64_t node_paths) {
+    kvh = h;
+    const int64_t rows = static_cast<int64_t>(q.n) * A.G;
+    const int64_t r = r0 + rw * 32 + col;
+    row_ok = r < rows;
+    const int32_t rc = static_cast<int32_t>(row_ok ? r - r0 : 0);
+    const int32_t t0 = static_cast<int32_t>(r0 / A.G), h0 = static_cast<int32_t>(r0 - static_cast<int64_t>(t0) * A.G);
+    t = t0 + (h0 + rc) / A.G;
+    head = h * A.G + (h0 + rc) % A.G;
+    const int64_t r_last = r0 + BM < rows ? r0 + BM - 1 : rows - 1;
+    const int32_t t_last = static_cast<int32_t>(r_last / A.G);
+    if constexpr (TREE) {
+      path = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(node_paths >> 32), t, 64)) << 32) |
+             static_cast<uint32_t>(__shfl(static_cast<uint32_t>(node_paths), t, 64));
+      n_keys = q.ctx + q.n;
+      clear = q.ctx;
+    } else {
+      n_keys = q.ctx + t_last + 1;
+      clear = q.ctx + t0 + 1;
+    }
+    const uint16_t* qp = static_cast<const uint16_t*>(A.q) + (q.row0 + t) * A.q_stride + static_cast<int64_t>(head) * D;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(qp + s * 16 + half * 8);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) O[i][e] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+    ids_at = -1;
+  }
+
+  // Base rows of the 16-row groups of keys 1024 at ..: one page lookup per lane.
+  __device__ void fetch_ids(int32_t at) {
+    ids_at = at;
+    const int32_t key = at * 1024 + lane * 16;
+    ids = 0;
+    if (key < q.ctx) {
+      const int32_t e = key / A.page;
+      int32_t page = A.block_table[static_cast<size_t>(q.index) * A.max_pages + e];
+      if (page < 0 || page >= A.n_pages) {
+        report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+        page = 0;
+      }
+      ids = (static_cast<int64_t>(page) * A.Hk + kvh) * A.page + (key - e * A.page);
+    }
+  }
+
+  // Requests tile kt into buffer b.
+  __device__ void request(int32_t kt, int b) {
+    const int32_t key0 = kt * kKeys;
+    const int lrow = lane / LPR, c = lane % LPR;  // this lane's row of an instruction's RPI, its chunk's place
+    const uint32_t dst = lds0 + b * BUF + wave * WROWS * ROW_BYTES;
+    if (key0 + kKeys <= q.ctx) {
+      // all cached: 16-row groups lie in one page each
+      if (ids_at != (kt >> 4)) fetch_ids(kt >> 4);
+#pragma unroll
+      for (int i = 0; i < WROWS / RPI; ++i) {
+        const int row = wave * WROWS + i * RPI;  // first row of the instruction, within the tile
+        const int src = (kt & 15) * 4 + row / 16;
+        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(ids), src);
+        const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(static_cast<uint64_t>(ids) >> 32), src);
+        const int64_t base = (static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo) + row % 16) * ROW_BYTES;
+        const int rr = row + lrow;
+        load_lds16(static_cast<const char*>(A.k_cache) + base + (lrow * ROW_BYTES + 16 * (c ^ k_perm(rr))), dst + i * 1024);
+        load_lds16(static_cast<const char*>(A.v_cache) + base + (lrow * ROW_BYTES + 16 * (c ^ v_perm(rr))),
+                   dst + TILE + i * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < WROWS / RPI; ++i) {
+        const int rr = wave * WROWS + i * RPI + lrow;
+        const int32_t j = min(key0 + rr, n_keys - 1);  // rows past the last key repeat it; no row attends them
+        const char *kp, *vp;
+        if (key0 >= q.ctx) {
+          kp = static_cast<const char*>(A.k) + ((q.row0 + (j - q.ctx)) * A.k_stride + kvh * D) * 2;
+          vp = static_cast<const char*>(A.v) + ((q.row0 + (j - q.ctx)) * A.v_stride + kvh * D) * 2;
+        } else {
+          kp = key_row<2>(A, q, A.k_cache, A.k, A.k_stride, kvh, j);
+          vp = key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j);
+        }
+        load_lds16(kp + 16 * (c ^ k_perm(rr)), dst + i * 1024);
+        load_lds16(vp + 16 * (c ^ v_perm(rr)), dst + TILE + i * 1024);
+      }
+    }
+  }
+
+  // Does this lane's row attend key j?
+  __device__ bool attends(int32_t j) const {
+    const int32_t own = j - q.ctx;
+    if constexpr (TREE) return own < 0 || (own < q.n && ((path >> own) & 1ull));
+    else return own <= t;
+  }
+
+  // Values that are not finite must not reach rows that do not attend their
+  // key (0 x inf is NaN).  In a tile that some row attends in part: finds such
+  // V rows and clears them in LDS; their terms are added by add_bad().
+  __device__ uint64_t clear_bad(char* v) {
+    uint32_t* flags = reinterpret_cast<uint32_t*>(lds + LDS_TILES);
+    if (threadIdx.x < 2) flags[threadIdx.x] = 0;
+    __syncthreads();
+    for (int e = threadIdx.x; e < kKeys * CH; e += THREADS)
+      if (any_nonfinite<true>(*reinterpret_cast<const uint4*>(v + e * 16))) atomicOr(&flags[e / CH / 32], 1u << (e / CH % 32));
+    __syncthreads();
+    const uint64_t bad = (static_cast<uint64_t>(flags[1]) << 32) | flags[0];
+    if (bad != 0) {
+      for (int e = threadIdx.x; e < kKeys * CH; e += THREADS)
+        if ((bad >> (e / CH)) & 1ull) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();  // the flags are read, and the rows cleared, by every wave
+    return bad;
+  }
+
+  // The 32 keys from row `base` of the tile in buffer b on, their logits and
+  // their terms.  MASKED: some row does not attend every key of the tile.
+  template <bool MASKED>
+  __device__ void block(int32_t key0, char* kbuf, char* vbuf, int base, uint64_t bad) {
+    // ---- logits ----
+    f32x16_t S;
+    // The lane's offsets are made anew for every block (the empty asm hides
+    // that they never change): kept across blocks they would push others out
+    // of the 256 registers.
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int kcol = ln & 31, khalf = ln >> 5;
+    const char* krow = kbuf + (base + kcol) * ROW_BYTES;
+    const int kx = k_perm(kcol);  // blocks start at multiples of 32 rows
+#pragma unroll
+    for (int e = 0; e < 16; ++e) S[e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(krow + 16 * ((2 * s + khalf) ^ kx));
+      S = mfma32x32(a, qf[s], S);
+    }
+    // K operands four instructions ahead, no more: registers are short
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, 4, 0);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      if (s < NS - 4) __builtin_amdgcn_sched_group_barrier(kSchedLds, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // ---- running maximum ----
+    float mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if constexpr (MASKED) S[e] = attends(key0 + base + 8 * (e / 4) + 4 * half + e % 4) ? S[e] : -INFINITY;
+      mx = fmaxf(mx, S[e]);
+    }
+    mx = half_max(mx);
+    // The weights are taken against a maximum that may lag: O and l are scaled
+    // only when some row's maximum has grown by more than 2^8 in weight, which
+    // leaves sums and weights far inside their range.
+    if (__any((mx - m) * A.scale_log2 > 8.f)) {
+      const float m_new = fmaxf(m, mx);
+      const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * A.scale_log2);
+      m = m_new;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) O[i] *= f;
+    }
+    const float off = m == -INFINITY ? 0.f : -m * A.scale_log2;
+    // ---- weights; rounded to bf16 for the product: each is off by at most
+    // 2^-8 of itself, below the output's own rounding on average over keys ----
+    bf16x8_t P[2];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      S[e] = __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, off));
+      l += S[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) P[e / 8][e % 8] = static_cast<__bf16>(S[e]);
+    // ---- O^T += V^T P^T ----
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+v"(ln));
+    const int g2 = (ln >> 4) & 1, mrow = (ln & 15) >> 2, quarter = ln & 3;
+    const char* vrow = vbuf + (base + 4 * (ln >> 5) + mrow) * ROW_BYTES + 8 * (quarter & 1);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int dt = 0; dt < NT; ++dt) {
+        const int chunk = (dt * 4 + 2 * g2 + (quarter >> 1)) ^ v_perm(mrow);  // rows differ from mrow by multiples of 4
+        typedef __attribute__((address_space(3))) s16x4_t* lp;
+        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vrow + 16 * ks * ROW_BYTES + 16 * chunk));
+        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vrow + (16 * ks + 8) * ROW_BYTES + 16 * chunk));
+        O[dt] = mfma32x32(__builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), P[ks], O[dt]);
+      }
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, 6, 1);
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
+      if (i < 2 * NT - 3) __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MASKED) {
+      // the terms of the V rows that clear_bad() took out, for the rows that attend them
+      for (uint32_t left = static_cast<uint32_t>(bad >> base); left != 0; left &= left - 1) {
+        const int kr = __builtin_ctz(left);
+        float p = 0.f;  // the weight, in the lanes of half (kr / 4) % 2
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p = (8 * (e / 4) + e % 4) == (kr & ~4) ? S[e] : p;
+        p = __shfl(p, col + 32 * ((kr >> 2) & 1), 64);
+        const int32_t j = key0 + base + kr;
+        if (!attends(j)) continue;
+        const uint16_t* vr =
+            reinterpret_cast<const uint16_t*>(key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j)) + 4 * half;
+#pragma unroll
+        for (int dt = 0; dt < NT; ++dt) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) O[dt][i] += p * bf16_bits_to_f32(vr[dt * 32 + 8 * (i / 4) + i % 4]);
+          asm volatile("" ::: "memory");  // no more than one step's loads at a time in registers
+        }
+      }
+    }
+  }
+
+  // One tile in buffer b.
+  template <bool MASKED>
+  __device__ void tile(int32_t kt, int b) {
+    char* kbuf = lds + b * BUF;
+    uint64_t bad = 0;
+    if constexpr (MASKED) bad = clear_bad(kbuf + TILE);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * kKeys, kbuf, kbuf + TILE, (kw * KB + kb) * 32, bad);
+  }
+
+  // Tiles [lo, hi) of the unit; leaves the sums of this wave's keys in O, m, l.
+  __device__ void keys(int32_t lo, int32_t hi) {
+    if (lo >= hi) return;
+    request(lo, 0);
+    // tiles that every row attends whole, then the others
+    const int32_t mid = max(lo, min(hi, clear / kKeys));
+    int32_t kt = lo;
+    for (; kt < mid; ++kt) {
+      tile_ready();
+      if (kt + 1 < hi) request(kt + 1, (kt + 1 - lo) & 1);
+      tile<false>(kt, (kt - lo) & 1);
+    }
+    for (; kt < hi; ++kt) {
+      tile_ready();
+      if (kt + 1 < hi) request(kt + 1, (kt + 1 - lo) & 1);
+      tile<true>(kt, (kt - lo) & 1);
+    }
+    l = half_sum(l);
+  }
+
+  // Element (dt, i) of O is d = 32 dt + 8 (i / 4) + 4 half + i % 4.
+  __device__ void write_out() {
+    if (!row_ok || kw != 0) return;
+    const float inv = 1.0f / l;
+    uint16_t* o = static_cast<uint16_t*>(A.o) + (static_cast<size_t>(q.row0 + t) * A.Hq + head) * D + 4 * half;
+#pragma unroll
+    for (int dt = 0; dt < NT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint2*>(o + 32 * dt + 2 * i) =
+            make_uint2(pack2_bf16(O[dt][i] * inv, O[dt][i + 1] * inv), pack2_bf16(O[dt][i + 2] * inv, O[dt][i + 3] * inv));
+  }
+  // Unscaled sums and (scaled maximum, sum) of this lane's row.
+  __device__ void write_part(float* sums, float* ml) const {
+#pragma unroll
+    for (int dt = 0; dt < NT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f32x4_t*>(sums + 32 * dt + 2 * i + 4 * half) =
+            f32x4_t{O[dt][i], O[dt][i + 1], O[dt][i + 2], O[dt][i + 3]};
+    if (half == 0) {
+      ml[0] = m * A.scale_log2;
+      ml[1] = l;
+    }
+  }
+
+  // KW waves of a row block: joins their sums in wave kw = 0 (through LDS, the
+  // tile buffers being free).  All waves of the workgroup call it.
+  __device__ void join() {
+    if constexpr (KW == 2) {
+      __syncthreads();
+      float* at = reinterpret_cast<float*>(lds) + rw * 32 * (D + 2);
+      // [element][lane] so that a wave's accesses are consecutive
+      if (kw == 1) {
+#pragma unroll
+        for (int dt = 0; dt < NT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) at[(dt * 16 + i) * 64 + lane] = O[dt][i];
+        if (half == 0) {
+          at[32 * D + col] = m;
+          at[32 * D + 32 + col] = l;
+        }
+      }
+      __syncthreads();
+      if (kw == 0) {
+        const float m1 = at[32 * D + col], l1 = at[32 * D + 32 + col];
+        const float m_new = fmaxf(m, m1);
+        const float f0 = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * A.scale_log2);
+        const float f1 = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m1 - m_new) * A.scale_log2);
+        m = m_new;
+        l = l * f0 + l1 * f1;
+#pragma unroll
+        for (int dt = 0; dt < NT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) O[dt][i] = O[dt][i] * f0 + at[(dt * 16 + i) * 64 + lane] * f1;
+      }
+      __syncthreads();
+    }
+  }
+};
+
+// Packed prompts: one workgroup per (block of rows, KV head, split of the key axis).
+template <int D>
+__global__ __launch_bounds__(512, 2) void flash_prefill_kernel(AttnArgs A) {
+  typedef Flash<D, 8, 1, false> F;
+  extern __shared__ __align__(1024) char smem[];
+  F f(A, smem);
+  // later row blocks attend more keys: they start first
+  const int64_t id = gridDim.x - 1 - blockIdx.x;
+  const int s = uniform(find_seq(A, id, F::BM));
+  const int64_t r0 = uniform((id - tile_start(A, s, F::BM)) * F::BM);
+  f.q = uniform(packed_seq(A, s, threadIdx.x == 0));
+  if (f.q.n == 0 || r0 >= static_cast<int64_t>(f.q.n) * A.G) return;
+  f.begin(r0, blockIdx.y, 0);
+  const int32_t tiles = (f.n_keys + kKeys - 1) / kKeys;
+  const int32_t per = (tiles + A.n_split - 1) / A.n_split;
+  const int32_t lo = min(static_cast<int32_t>(blockIdx.z) * per, tiles), hi = min(lo + per, tiles);
+  f.keys(lo, hi);
+  if (A.n_split == 1) {
+    f.write_out();
+  } else if (f.row_ok) {
+    const size_t part = (static_cast<size_t>(f.q.row0 + f.t) * A.Hq + f.head) * A.n_split + blockIdx.z;
+    float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
+    f.write_part(A.part + part * D, ml + part * 2);
+  }
+}
+
+template <int D>
+static int launch_flash_prefill_t(const AttnArgs& a, int64_t tiles, hipStream_t s) {
+  typedef Flash<D, 8, 1, false> F;
+  hipLaunchKernelGGL((flash_prefill_kernel<D>), dim3(static_cast<unsigned>(tiles), a.Hk, a.n_split), dim3(F::THREADS),
+                     F::LDS, s, a);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_flash_prefill(const AttnArgs& a, int64_t tiles, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (a.D) {
+    case 64: return launch_flash_prefill_t<64>(a, tiles, s);
+    case 128: return launch_flash_prefill_t<128>(a, tiles, s);
+    case 256: return launch_flash_prefill_t<256>(a, tiles, s);
+    default: return static_cast<int>(hipErrorInvalidValue);
+  }
+}
+
+}  // namespace gdn

@@ -162,6 +162,8 @@ inline size_t attn_part_bytes(int64_t tokens, int Hq, int D, int n_split) {
   return n_split <= 1 ? 0 : static_cast<size_t>(tokens) * Hq * n_split * (D + 2) * sizeof(float);
 }
 int launch_attn(const AttnArgs& a, bool bf16, void* stream);
+constexpr int kFlashRows = 256;  // rows of a workgroup of the bf16 prompt attention
+int launch_flash_prefill(const AttnArgs& a, int64_t tiles, void* stream);
 // Debug builds: one small kernel reporting GDN_DEV_DUP_SLOT to *dev_err when
 // two of a call's slot ids are equal: a[0..na), then, for rows i < nb, the
 // ids b[i kb + j] for j < kb, or j < k_row[i] when k_row is given (rows whose
