@@ -18,8 +18,6 @@
 //
 // With more than one split of the key axis each split writes its unscaled sums
 // with (m, l), and combine_kernel joins them in a fixed order.
-#include <type_traits>
-
 #include "gdn_attn_device.h"
 
 namespace gdn {
@@ -29,35 +27,30 @@ namespace {
 __device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// The general kernel: 64 rows x 32 keys per step, four waves of 16 rows each,
-// K and V rows staged through LDS.  16x16 tiles: lane l holds rows (keys)
-// 4 (l / 16) + i of column (query row) l % 16.
+// fp32: 64 rows x 32 keys per step, four waves of 16 rows each, K and V rows
+// staged through LDS.  16x16x4 matrix instructions: lane l holds rows (keys)
+// 4 (l / 16) + i of column (query row) l % 16.  (bf16: gdn_flash.hip.)
 // ---------------------------------------------------------------------------
 constexpr int kGenRows = 64, kGenKeys = 32, kGenThreads = 256;
 
-template <int D, bool BF16>
+template <int D>
 struct GenShape {
-  static constexpr int ES = BF16 ? 2 : 4;
+  static constexpr int ES = 4;
   static constexpr int VEC = 16 / ES;               // elements of a 16-byte vector
   static constexpr int LD = D + VEC;                // LDS row, 16 bytes of padding against bank conflicts
   static constexpr int VPR = D / VEC;               // vectors of a row
   static constexpr int TILE_BYTES = kGenKeys * LD * ES;
 };
 
-template <int D, bool BF16, bool TREE>
-__global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
-  using Sh = GenShape<D, BF16>;
+template <int D, bool TREE>
+__global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
+  using Sh = GenShape<D>;
   constexpr int ES = Sh::ES, LD = Sh::LD, NT = D / 16;
-  constexpr int QF = BF16 ? D / 32 : D / 4;  // k-steps of the logits
-  typedef typename std::conditional<BF16, uint16_t, float>::type E;
-  typedef typename std::conditional<BF16, bf16x8_t, float>::type Qf;
+  constexpr int QF = D / 4;  // k-steps of the logits
+  typedef float E;
   extern __shared__ __align__(16) char lds[];  // K tile, V tile, P of a tile (rare), flags
   E* Ks = reinterpret_cast<E*>(lds);
   E* Vs = reinterpret_cast<E*>(lds + Sh::TILE_BYTES);
@@ -103,14 +96,11 @@ __global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
   const int32_t clear = TREE ? q.ctx : q.ctx + t_first + 1;        // keys every row of the tile attends
 
   // ---- Q operand ----
-  Qf qf[QF];
+  float qf[QF];
   {
     const char* qp = static_cast<const char*>(A.q) + ((q.row0 + t) * A.q_stride + static_cast<int64_t>(head) * D) * ES;
 #pragma unroll
-    for (int s = 0; s < QF; ++s) {
-      if constexpr (BF16) qf[s] = *reinterpret_cast<const bf16x8_t*>(qp + (s * 32 + g * 8) * 2);
-      else qf[s] = *reinterpret_cast<const float*>(qp + (s * 4 + g) * 4);
-    }
+    for (int s = 0; s < QF; ++s) qf[s] = *reinterpret_cast<const float*>(qp + (s * 4 + g) * 4);
   }
   f32x4_t O[NT];
 #pragma unroll
@@ -131,7 +121,7 @@ __global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
         kv = *reinterpret_cast<const uint4*>(key_row<ES>(A, q, A.k_cache, A.k, A.k_stride, kvh, j) + 16 * w);
         vv = *reinterpret_cast<const uint4*>(key_row<ES>(A, q, A.v_cache, A.v, A.v_stride, kvh, j) + 16 * w);
       }
-      if (masked && any_nonfinite<BF16>(vv)) atomicOr(bad_keys, 1u << kr);
+      if (masked && any_nonfinite<false>(vv)) atomicOr(bad_keys, 1u << kr);
       *reinterpret_cast<uint4*>(Ks + kr * LD + w * Sh::VEC) = kv;
       *reinterpret_cast<uint4*>(Vs + kr * LD + w * Sh::VEC) = vv;
     }
@@ -156,10 +146,7 @@ __global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
       f32x4_t c = {0.f, 0.f, 0.f, 0.f};
       const E* kr = Ks + (16 * k2 + col) * LD;
 #pragma unroll
-      for (int s = 0; s < QF; ++s) {
-        if constexpr (BF16) c = mfma_bf16(*reinterpret_cast<const bf16x8_t*>(kr + s * 32 + g * 8), qf[s], c);
-        else c = mfma_f32(kr[s * 4 + g], qf[s], c);
-      }
+      for (int s = 0; s < QF; ++s) c = mfma_f32(kr[s * 4 + g], qf[s], c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int32_t j = key0 + 16 * k2 + 4 * g + i;
@@ -194,24 +181,10 @@ __global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
 #pragma unroll
     for (int dt = 0; dt < NT; ++dt) {
       const E* vc = Vs + 4 * g * LD + 16 * dt + col;
-      if constexpr (BF16) {
-        bf16x8_t a, p;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = __builtin_bit_cast(__bf16, vc[i * LD]);
-          a[4 + i] = __builtin_bit_cast(__bf16, vc[(16 + i) * LD]);
-          // weights rounded to bf16 for the matrix instruction: each is off by
-          // at most 2^-9 of itself, which their average over keys reduces
-          p[i] = static_cast<__bf16>(P[0][i]);
-          p[4 + i] = static_cast<__bf16>(P[1][i]);
-        }
-        O[dt] = mfma_bf16(a, p, O[dt]);
-      } else {
+      for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) O[dt] = mfma_f32(vc[(16 * k2 + i) * LD], P[k2][i], O[dt]);
-      }
+        for (int i = 0; i < 4; ++i) O[dt] = mfma_f32(vc[(16 * k2 + i) * LD], P[k2][i], O[dt]);
     }
     if (bad) {  // same for the whole workgroup
       float* pw = Ps + wave * kGenKeys * 16;
@@ -232,7 +205,7 @@ __global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
 #pragma unroll
         for (int dt = 0; dt < NT; ++dt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) O[dt][i] += p * load_in<BF16>(vr, 16 * dt + 4 * g + i);
+          for (int i = 0; i < 4; ++i) O[dt][i] += p * load_in<false>(vr, 16 * dt + 4 * g + i);
       }
     }
   }
@@ -243,14 +216,8 @@ __global__ __launch_bounds__(kGenThreads) void attn_general_kernel(AttnArgs A) {
   if (A.n_split == 1) {
     const float inv = 1.0f / l;
 #pragma unroll
-    for (int dt = 0; dt < NT; ++dt) {
-      const size_t at = orow * D + 16 * dt + 4 * g;
-      if constexpr (BF16)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.o) + at) =
-            make_uint2(pack2_bf16(O[dt][0] * inv, O[dt][1] * inv), pack2_bf16(O[dt][2] * inv, O[dt][3] * inv));
-      else
-        *reinterpret_cast<f32x4_t*>(static_cast<float*>(A.o) + at) = O[dt] * inv;
-    }
+    for (int dt = 0; dt < NT; ++dt)
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(A.o) + orow * D + 16 * dt + 4 * g) = O[dt] * inv;
   } else {
     const size_t part = orow * A.n_split + z;
     float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
@@ -340,25 +307,34 @@ int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
 
 }  // namespace
 
-int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
+int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int nodes, bool bf16) {
+  if (bf16 && nodes > 0) return 1;
   // two workgroups per CU, and at most 64 parts to join
   const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kFlashRows : kGenRows) * Hk;
   const int64_t want = wgs > 0 ? 512 / wgs : 1;
   return static_cast<int>(want < 1 ? 1 : (want > 64 ? 64 : want));
 }
 
+size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
+  if (bf16 && nodes > 0) return flash_tree_part_bytes(n_seqs, Hk, G, D, nodes);
+  const int n_split = attn_splits(tokens, n_seqs, Hk, G, nodes, bf16);
+  return n_split <= 1 ? 0 : static_cast<size_t>(tokens) * Hk * G * n_split * (D + 2) * sizeof(float);
+}
+
 template <int D, bool BF16>
 static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
-  using Sh = GenShape<D, BF16>;
-  const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, kGenRows);
+  const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, BF16 ? kFlashRows : kGenRows);
   if (tiles > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
-  const dim3 grid(static_cast<unsigned>(tiles), a.Hk, a.n_split);
-  const size_t lds = 2 * Sh::TILE_BYTES + 4 * kGenKeys * 16 * sizeof(float) + 16;
-  if (BF16 && a.nodes == 0) {
-    const int e = launch_flash_prefill(a, row_tiles(a.n_tokens, a.n_seqs, a.G, 0, kFlashRows), s);
+  if constexpr (BF16) {
+    if (a.nodes > 0) return launch_flash_tree(a, s);
+    const int e = launch_flash_prefill(a, tiles, s);
     if (e != 0) return e;
-  } else if (a.nodes > 0) hipLaunchKernelGGL((attn_general_kernel<D, BF16, true>), grid, dim3(kGenThreads), lds, s, a);
-  else hipLaunchKernelGGL((attn_general_kernel<D, BF16, false>), grid, dim3(kGenThreads), lds, s, a);
+  } else {
+    const dim3 grid(static_cast<unsigned>(tiles), a.Hk, a.n_split);
+    const size_t lds = 2 * GenShape<D>::TILE_BYTES + 4 * kGenKeys * 16 * sizeof(float) + 16;
+    if (a.nodes > 0) hipLaunchKernelGGL((attn_f32_kernel<D, true>), grid, dim3(kGenThreads), lds, s, a);
+    else hipLaunchKernelGGL((attn_f32_kernel<D, false>), grid, dim3(kGenThreads), lds, s, a);
+  }
   int e = static_cast<int>(hipGetLastError());
   if (e == 0 && a.n_split > 1) {
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.Hq, per = 256 / (D / 4);

@@ -62,8 +62,11 @@ gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, c
 }
 
 int attn_split(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes) {
-  return gdn::attn_splits(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head, nodes,
-                          g->dtype == GDN_BF16);
+  return gdn::attn_splits(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, nodes, g->dtype == GDN_BF16);
+}
+size_t attn_bytes(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes) {
+  return gdn::attn_part_bytes(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head, nodes,
+                              g->dtype == GDN_BF16);
 }
 
 gdn::AttnArgs attn_args(const gdn_attn_geometry* g, int32_t n_split, void* workspace, int64_t tokens) {
@@ -77,7 +80,7 @@ gdn::AttnArgs attn_args(const gdn_attn_geometry* g, int32_t n_split, void* works
   a.max_pages = g->max_pages;
   a.n_split = n_split;
   a.n_tokens = static_cast<int32_t>(tokens);
-  a.part = n_split > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.part = static_cast<float*>(workspace);  // not used where the call needs none
   a.scale_log2 = static_cast<float>(static_cast<double>(g->scale) * 1.4426950408889634);
   return a;
 }
@@ -178,13 +181,12 @@ gdn_status gdn_kv_write(const gdn_attn_geometry* g, void* k_cache, void* v_cache
 
 size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_geometry* g, int32_t n_tokens, int32_t n_seqs) {
   if (check_attn(g) != GDN_OK || n_tokens < 0 || n_seqs < 1) return 0;
-  return gdn::attn_part_bytes(n_tokens, g->n_q_heads, g->d_head, attn_split(g, n_tokens, n_seqs, 0));
+  return attn_bytes(g, n_tokens, n_seqs, 0);
 }
 
 size_t gdn_attn_tree_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n) {
   if (check_attn(g) != GDN_OK || batch < 1 || n < 1 || n > g->max_tree) return 0;
-  const int64_t rows = static_cast<int64_t>(batch) * n;
-  return gdn::attn_part_bytes(rows, g->n_q_heads, g->d_head, attn_split(g, rows, batch, n));
+  return attn_bytes(g, static_cast<int64_t>(batch) * n, batch, n);
 }
 
 gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q_stride, const void* k,
@@ -201,7 +203,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q
   if ((s = check_stride(g, k_stride, g->n_kv_heads, "k_stride")) != GDN_OK) return s;
   if ((s = check_stride(g, v_stride, g->n_kv_heads, "v_stride")) != GDN_OK) return s;
   const int n_split = attn_split(g, n_tokens, n_seqs, 0);
-  s = check_workspace(workspace, workspace_bytes, gdn::attn_part_bytes(n_tokens, g->n_q_heads, g->d_head, n_split));
+  s = check_workspace(workspace, workspace_bytes, attn_bytes(g, n_tokens, n_seqs, 0));
   if (s != GDN_OK) return s;
   GDN_NEED_PTR4(cu_seqlens, "cu_seqlens");
   if (ctx_len) {
@@ -248,7 +250,7 @@ gdn_status gdn_attn_tree(const gdn_attn_geometry* g, const void* q, int64_t q_st
   if ((s = check_stride(g, v_stride, g->n_kv_heads, "v_stride")) != GDN_OK) return s;
   const int64_t rows = static_cast<int64_t>(batch) * n;
   const int n_split = attn_split(g, rows, batch, n);
-  s = check_workspace(workspace, workspace_bytes, gdn::attn_part_bytes(rows, g->n_q_heads, g->d_head, n_split));
+  s = check_workspace(workspace, workspace_bytes, attn_bytes(g, rows, batch, n));
   if (s != GDN_OK) return s;
   GDN_NEED_PTR(q, "q");
   GDN_NEED_PTR(k, "k");

@@ -76,7 +76,9 @@ struct Flash {
   static constexpr int KX = D >= 128 ? 15 : 7;           // bits of the K permutation
   // LDS: two buffers, then flags (two words: keys whose V row is not finite)
   static constexpr size_t LDS_TILES = 2 * static_cast<size_t>(BUF);
-  static constexpr size_t LDS = LDS_TILES + 16;
+  // join() lays the sums of RW waves and their statistics over the buffers
+  static constexpr size_t LDS_JOIN = KW == 2 ? static_cast<size_t>(BM) * (D + 2) * 4 : 0;
+  static constexpr size_t LDS = LDS_TILES + 16 > LDS_JOIN ? LDS_TILES + 16 : LDS_JOIN;
 
   __device__ static int k_perm(int row) { return D >= 128 ? row & 15 : (row >> 1) & 7; }
   __device__ static int v_perm(int row) { return D >= 128 ? (row & 3) * 4 : ((row >> 1) & 1) * 4; }
@@ -110,27 +112,26 @@ struct Flash {
     half = lane >> 5;
   }
 
-  // Rows r0 .. r0 + BM - 1 (of n G) of KV head h; q and (TREE) the lane's paths are set.
-  __device__ void begin(int64_t r0, int h, uint64_t node_paths) {
+  // The unit: rows r0 .. r0 + BM - 1 (of n G) of KV head h of sequence q.
+  __device__ void begin_keys(int64_t r0, int h) {
     kvh = h;
     const int64_t rows = static_cast<int64_t>(q.n) * A.G;
+    const int64_t r_last = r0 + BM < rows ? r0 + BM - 1 : rows - 1;
+    n_keys = TREE ? q.ctx + q.n : q.ctx + static_cast<int32_t>(r_last / A.G) + 1;
+    clear = TREE ? q.ctx : q.ctx + static_cast<int32_t>(r0 / A.G) + 1;
+    ids_at = -1;
+  }
+  // This lane's row and its Q; node_paths (TREE): lane j holds node j's path.
+  __device__ void begin_rows(int64_t r0, uint64_t node_paths) {
     const int64_t r = r0 + rw * 32 + col;
-    row_ok = r < rows;
+    row_ok = r < static_cast<int64_t>(q.n) * A.G;
     const int32_t rc = static_cast<int32_t>(row_ok ? r - r0 : 0);
     const int32_t t0 = static_cast<int32_t>(r0 / A.G), h0 = static_cast<int32_t>(r0 - static_cast<int64_t>(t0) * A.G);
     t = t0 + (h0 + rc) / A.G;
-    head = h * A.G + (h0 + rc) % A.G;
-    const int64_t r_last = r0 + BM < rows ? r0 + BM - 1 : rows - 1;
-    const int32_t t_last = static_cast<int32_t>(r_last / A.G);
-    if constexpr (TREE) {
+    head = kvh * A.G + (h0 + rc) % A.G;
+    if constexpr (TREE)
       path = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(node_paths >> 32), t, 64)) << 32) |
              static_cast<uint32_t>(__shfl(static_cast<uint32_t>(node_paths), t, 64));
-      n_keys = q.ctx + q.n;
-      clear = q.ctx;
-    } else {
-      n_keys = q.ctx + t_last + 1;
-      clear = q.ctx + t0 + 1;
-    }
     const uint16_t* qp = static_cast<const uint16_t*>(A.q) + (q.row0 + t) * A.q_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
     for (int s = 0; s < NS; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(qp + s * 16 + half * 8);
@@ -140,7 +141,6 @@ struct Flash {
       for (int e = 0; e < 16; ++e) O[i][e] = 0.f;
     m = -INFINITY;
     l = 0.f;
-    ids_at = -1;
   }
 
   // Base rows of the 16-row groups of keys 1024 at ..: one page lookup per lane.
@@ -337,10 +337,9 @@ struct Flash {
     for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * kKeys, kbuf, kbuf + TILE, (kw * KB + kb) * 32, bad);
   }
 
-  // Tiles [lo, hi) of the unit; leaves the sums of this wave's keys in O, m, l.
+  // Tiles [lo, hi) of the unit, the first already requested into buffer 0;
+  // leaves the sums of this wave's keys in O, m, l.
   __device__ void keys(int32_t lo, int32_t hi) {
-    if (lo >= hi) return;
-    request(lo, 0);
     // tiles that every row attends whole, then the others
     const int32_t mid = max(lo, min(hi, clear / kKeys));
     int32_t kt = lo;
@@ -430,17 +429,259 @@ __global__ __launch_bounds__(512, 2) void flash_prefill_kernel(AttnArgs A) {
   const int64_t r0 = uniform((id - tile_start(A, s, F::BM)) * F::BM);
   f.q = uniform(packed_seq(A, s, threadIdx.x == 0));
   if (f.q.n == 0 || r0 >= static_cast<int64_t>(f.q.n) * A.G) return;
-  f.begin(r0, blockIdx.y, 0);
+  f.begin_keys(r0, blockIdx.y);
   const int32_t tiles = (f.n_keys + kKeys - 1) / kKeys;
   const int32_t per = (tiles + A.n_split - 1) / A.n_split;
   const int32_t lo = min(static_cast<int32_t>(blockIdx.z) * per, tiles), hi = min(lo + per, tiles);
-  f.keys(lo, hi);
+  if (lo < hi) f.request(lo, 0);
+  f.begin_rows(r0, 0);
+  if (lo < hi) f.keys(lo, hi);
   if (A.n_split == 1) {
     f.write_out();
   } else if (f.row_ok) {
     const size_t part = (static_cast<size_t>(f.q.row0 + f.t) * A.Hq + f.head) * A.n_split + blockIdx.z;
     float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
     f.write_part(A.part + part * D, ml + part * 2);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Trees of drafts: the key tiles of all units (KV head x block of rows of one
+// row of the batch) lie on one line, row by row, and workgroup w of W takes
+// tiles [w T / W, (w + 1) T / W) of it, whatever the rows' lengths.  A unit that
+// lies in one workgroup's share is written out; the shares of one that does
+// not go to the workspace (at most two per workgroup: its first, begun inside
+// a unit, and its last, ended inside one) and are joined by tree_join_kernel.
+// ---------------------------------------------------------------------------
+struct TreeSplit {
+  int32_t rows_per_unit, units_per_row;  // BM; row blocks x KV heads
+  int32_t workgroups;                    // W
+};
+// Workspace: sums [2 W][BM][D], (max, sum) [2 W][BM][2], then per unit
+// (first workgroup, number of workgroups; 0 or 1: nothing to join).
+__host__ __device__ inline size_t tree_ml_offset(const TreeSplit& t, int D) {
+  return static_cast<size_t>(2) * t.workgroups * t.rows_per_unit * D;
+}
+__host__ __device__ inline size_t tree_meta_offset(const TreeSplit& t, int D) {
+  return tree_ml_offset(t, D) + static_cast<size_t>(4) * t.workgroups * t.rows_per_unit;
+}
+
+template <int D, int RW>
+__global__ __launch_bounds__(128 * RW, 2) void flash_tree_kernel(AttnArgs A, TreeSplit ts) {
+  typedef Flash<D, RW, 2, true> F;
+  extern __shared__ __align__(1024) char smem[];
+  F f(A, smem);
+  const int lane = threadIdx.x & 63;
+  int2* meta = reinterpret_cast<int2*>(A.part + tree_meta_offset(ts, D));
+
+  // ---- the line of tiles: tiles of a unit of row s, and of all its units ----
+  auto row_tiles = [&](int s, int32_t* units) {
+    const int32_t n = A.n_row ? A.n_row[s] : A.nodes, c = A.ctx_len[s];
+    *units = 0;
+    if (n < 1 || n > A.nodes || c < 0 || c > static_cast<int64_t>(A.max_pages) * A.page) return 0;
+    *units = (n * A.G + F::BM - 1) / F::BM * A.Hk;
+    return (c + n + kKeys - 1) / kKeys;
+  };
+  // inclusive sum over the lanes of the tiles of rows base + lane
+  auto scan = [&](int base, int64_t* mine) {
+    int32_t units = 0;
+    const int32_t tiles = base + lane < A.n_seqs ? row_tiles(base + lane, &units) : 0;
+    int64_t inc = *mine = static_cast<int64_t>(tiles) * units;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t up = __shfl_up(inc, d, 64);
+      if (lane >= d) inc += up;
+    }
+    return inc;
+  };
+  int64_t total = 0, mine = 0, inc = 0;
+  for (int base = 0; base < A.n_seqs; base += 64) {
+    inc = scan(base, &mine);
+    total += __shfl(inc, 63, 64);
+  }
+  total = uniform(total);
+  // units without tiles (refused rows, row blocks past a row's nodes) have nothing to join
+  for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
+    int32_t units;
+    row_tiles(s, &units);
+    for (int u = units + threadIdx.x; u < ts.units_per_row; u += F::THREADS)
+      meta[static_cast<size_t>(s) * ts.units_per_row + u] = make_int2(0, 0);
+    if (units == 0) {  // reports what is wrong with it
+      uint64_t p;
+      tree_seq(A, s, threadIdx.x == 0, &p);
+    }
+  }
+  const int64_t W = ts.workgroups < total ? ts.workgroups : total;  // every workgroup has a tile
+  const int64_t w = blockIdx.x;
+  if (w >= W) return;
+  const int64_t first = uniform(w * total / W), last = uniform((w + 1) * total / W);
+
+  // ---- the row that holds tile `first`: the last one that does not begin after it ----
+  int s = 0;
+  int64_t row_at = 0;  // its first tile
+  for (int base = 0;; base += 64) {
+    if (A.n_seqs > 64) inc = scan(base, &mine);  // else it is at hand
+    const int64_t chunk = __shfl(inc, 63, 64);
+    if (row_at + chunk > first) {
+      const int at = 63 - __builtin_clzll(__ballot(base + lane < A.n_seqs && row_at + inc - mine <= first));
+      s = base + at;
+      row_at += __shfl(inc - mine, at, 64);
+      break;
+    }
+    row_at += chunk;
+  }
+  s = uniform(s);
+  row_at = uniform(row_at);
+
+  int seen = -1;  // the row whose paths are at hand
+  uint64_t paths = 0;
+  Seq q{0, 0, 0, 0};
+  for (int64_t at = first; at < last;) {
+    int32_t units;
+    const int32_t tiles = uniform(row_tiles(s, &units));
+    units = uniform(units);
+    if (at >= row_at + static_cast<int64_t>(tiles) * units) {
+      row_at += static_cast<int64_t>(tiles) * units;
+      ++s;
+      continue;
+    }
+    const int32_t unit = static_cast<int32_t>((at - row_at) / tiles);
+    const int64_t unit_at = row_at + static_cast<int64_t>(unit) * tiles;
+    const int32_t lo = static_cast<int32_t>(at - unit_at);
+    const int32_t hi = static_cast<int32_t>(last - unit_at < tiles ? last - unit_at : tiles);
+    const int64_t r0 = static_cast<int64_t>(unit / A.Hk) * F::BM;
+    // the first tile is requested before the row's paths and Q are waited for
+    f.q = Seq{static_cast<int64_t>(s) * A.nodes, uniform(A.n_row ? A.n_row[s] : A.nodes), uniform(A.ctx_len[s]), s};
+    f.begin_keys(r0, unit % A.Hk);
+    f.request(lo, 0);
+    if (seen != s) {
+      q = uniform(tree_seq(A, s, threadIdx.x == 0, &paths));
+      seen = s;
+    }
+    int2* unit_meta = meta + static_cast<size_t>(s) * ts.units_per_row + unit;
+    if (q.n == 0) {  // parents refused
+      if (lo == 0 && threadIdx.x == 0) *unit_meta = make_int2(0, 0);
+      tile_ready();  // the request has landed before the buffer is used again
+    } else {
+      f.begin_rows(r0, paths);
+      f.keys(lo, hi);
+      f.join();
+      if (lo == 0 && hi == tiles) {
+        if (threadIdx.x == 0) *unit_meta = make_int2(0, 1);
+        f.write_out();
+      } else {
+        if (lo == 0 && threadIdx.x == 0) {
+          // the last workgroup of the unit: the largest w' with w' total / W <= its last tile
+          const int64_t end = unit_at + tiles - 1;
+          *unit_meta = make_int2(static_cast<int>(w), static_cast<int>(((end + 1) * W - 1) / total - w) + 1);
+        }
+        if (f.row_ok && f.kw == 0) {
+          const size_t row = (static_cast<size_t>(2) * w + (lo == 0 ? 1 : 0)) * F::BM + f.rw * 32 + f.col;
+          f.write_part(A.part + row * D, A.part + tree_ml_offset(ts, D) + row * 2);
+        }
+      }
+    }
+    at = unit_at + hi;
+  }
+}
+
+// Joins the shares of a unit, in the order of the workgroups.  A wave takes one
+// row: D / 4 lanes hold its elements, 256 / D groups of them every 256 / D-th share.
+template <int D>
+__global__ __launch_bounds__(256) void tree_join_kernel(AttnArgs A, TreeSplit ts) {
+  constexpr int LPR = D / 4, NG = 64 / LPR;
+  const int64_t u = blockIdx.x;
+  const int s = static_cast<int>(u / ts.units_per_row), unit = static_cast<int>(u - static_cast<int64_t>(s) * ts.units_per_row);
+  const int2 mt = *(reinterpret_cast<const int2*>(A.part + tree_meta_offset(ts, D)) + u);
+  const int count = mt.y;
+  if (count <= 1) return;
+  const int lr = blockIdx.y * 4 + threadIdx.x / 64;  // row of the unit
+  const int64_t r = static_cast<int64_t>(unit / A.Hk) * ts.rows_per_unit + lr;
+  const int32_t n = A.n_row ? A.n_row[s] : A.nodes;
+  if (lr >= ts.rows_per_unit || r >= static_cast<int64_t>(n) * A.G) return;
+  const int lane = threadIdx.x & 63, c = (lane % LPR) * 4, g = lane / LPR;
+  const float* ml = A.part + tree_ml_offset(ts, D);
+  auto slot = [&](int i) {
+    return (static_cast<size_t>(2) * (mt.x + i) + (i == 0 ? 1 : 0)) * ts.rows_per_unit + lr;
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < count; i += 64) m = fmaxf(m, ml[slot(i) * 2]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+  const float ref = m == -INFINITY ? 0.f : m;
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = g; i < count; i += NG) {
+    const size_t at = slot(i);
+    const float wt = __builtin_amdgcn_exp2f(ml[at * 2] - ref);
+    l += wt * ml[at * 2 + 1];
+    sum += wt * load4(A.part + at * D + c);
+  }
+#pragma unroll
+  for (int d = LPR; d < 64; d <<= 1) {
+    l += __shfl_xor(l, d, 64);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], d, 64);
+  }
+  if (g != 0) return;
+  sum *= 1.0f / l;
+  const int t = static_cast<int>(r / A.G), head = unit % A.Hk * A.G + static_cast<int>(r % A.G);
+  const size_t at = ((static_cast<size_t>(s) * A.nodes + t) * A.Hq + head) * D + c;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.o) + at) =
+      make_uint2(pack2_bf16(sum[0], sum[1]), pack2_bf16(sum[2], sum[3]));
+}
+
+namespace {
+
+// Row blocks of 32, 64 or 128 rows, the smallest that holds the row's
+// (node, head) pairs of one KV head, 128 at most; as many workgroups as fit the
+// card at once: LDS holds 1, 2 or 4 of them per CU (D 256, 128, 64), and with
+// 128 rows their eight waves of up to 256 registers fill a CU.
+TreeSplit tree_split(int Hk, int G, int D, int nodes) {
+  TreeSplit t;
+  const int rows = nodes * G;
+  t.rows_per_unit = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
+  t.units_per_row = (rows + t.rows_per_unit - 1) / t.rows_per_unit * Hk;
+  const int by_lds = D == 256 ? 1 : (D == 128 ? 2 : 4), by_regs = 128 / t.rows_per_unit;
+  t.workgroups = 256 * (by_lds < by_regs ? by_lds : by_regs);
+  return t;
+}
+
+}  // namespace
+
+size_t flash_tree_part_bytes(int64_t batch, int Hk, int G, int D, int nodes) {
+  const TreeSplit t = tree_split(Hk, G, D, nodes);
+  return tree_meta_offset(t, D) * sizeof(float) + static_cast<size_t>(batch) * t.units_per_row * sizeof(int2);
+}
+
+template <int D, int RW>
+static void launch_tree_rows(const AttnArgs& a, const TreeSplit& t, hipStream_t s) {
+  typedef Flash<D, RW, 2, true> F;
+  hipLaunchKernelGGL((flash_tree_kernel<D, RW>), dim3(t.workgroups), dim3(F::THREADS), F::LDS, s, a, t);
+}
+
+template <int D>
+static int launch_flash_tree_t(const AttnArgs& a, hipStream_t s) {
+  const TreeSplit t = tree_split(a.Hk, a.G, D, a.nodes);
+  if (static_cast<int64_t>(a.n_seqs) * t.units_per_row > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
+  if (t.rows_per_unit == 32) launch_tree_rows<D, 1>(a, t, s);
+  else if (t.rows_per_unit == 64) launch_tree_rows<D, 2>(a, t, s);
+  else launch_tree_rows<D, 4>(a, t, s);
+  int e = static_cast<int>(hipGetLastError());
+  if (e != 0) return e;
+  const int rows = a.nodes * a.G < t.rows_per_unit ? a.nodes * a.G : t.rows_per_unit;
+  hipLaunchKernelGGL((tree_join_kernel<D>), dim3(a.n_seqs * t.units_per_row, (rows + 3) / 4), dim3(256), 0, s, a, t);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_flash_tree(const AttnArgs& a, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (a.D) {
+    case 64: return launch_flash_tree_t<64>(a, s);
+    case 128: return launch_flash_tree_t<128>(a, s);
+    case 256: return launch_flash_tree_t<256>(a, s);
+    default: return static_cast<int>(hipErrorInvalidValue);
   }
 }
 

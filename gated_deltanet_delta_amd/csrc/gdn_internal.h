@@ -155,15 +155,16 @@ int launch_commit_slots(const StepArgs& a, void* stream);
 int launch_verify_tree(const StepArgs& a, bool bf16, void* stream);
 int launch_kv_plan(const KvPlanArgs& a, void* stream);
 int launch_kv_write(const KvWriteArgs& a, void* stream);
-// Splits of the key axis that an attention call uses (1: no workspace), by its
-// row tiles alone, since only the device knows the lengths.
-int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16);
-inline size_t attn_part_bytes(int64_t tokens, int Hq, int D, int n_split) {
-  return n_split <= 1 ? 0 : static_cast<size_t>(tokens) * Hq * n_split * (D + 2) * sizeof(float);
-}
+// Splits of the key axis of an attention call (1: none), by its row tiles
+// alone, since only the device knows the lengths; bf16 trees are split on the device.
+int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int nodes, bool bf16);
+// Workspace of a call: tokens = rows of q (trees: batch x nodes).
+size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16);
 int launch_attn(const AttnArgs& a, bool bf16, void* stream);
 constexpr int kFlashRows = 256;  // rows of a workgroup of the bf16 prompt attention
 int launch_flash_prefill(const AttnArgs& a, int64_t tiles, void* stream);
+int launch_flash_tree(const AttnArgs& a, void* stream);
+size_t flash_tree_part_bytes(int64_t batch, int Hk, int G, int D, int nodes);
 // Debug builds: one small kernel reporting GDN_DEV_DUP_SLOT to *dev_err when
 // two of a call's slot ids are equal: a[0..na), then, for rows i < nb, the
 // ids b[i kb + j] for j < kb, or j < k_row[i] when k_row is given (rows whose
