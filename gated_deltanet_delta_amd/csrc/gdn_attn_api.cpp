@@ -55,8 +55,8 @@ int elem(const gdn_attn_geometry* g) { return g->dtype == GDN_BF16 ? 2 : 4; }
 // A row stride: at least the row, and whole 16-byte vectors.
 gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, const char* name) {
   const int64_t row = static_cast<int64_t>(heads) * g->d_head;
-  if (stride < row || stride * elem(g) % 16 != 0 || stride > (static_cast<int64_t>(1) << 40))
-    return fail(GDN_ERR_RANGE, "%s: %lld, required: >= %lld elements and a multiple of 16 bytes", name,
+  if (stride < row || stride * elem(g) % 16 != 0 || stride >= (1 << 24))
+    return fail(GDN_ERR_RANGE, "%s: %lld, required: >= %lld and < 2^24 elements, and a multiple of 16 bytes", name,
                 static_cast<long long>(stride), static_cast<long long>(row));
   return GDN_OK;
 }

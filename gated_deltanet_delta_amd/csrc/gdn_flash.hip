@@ -35,10 +35,20 @@ constexpr int kSchedMfma = 0x8, kSchedLds = 0x100;  // instruction classes of sc
 __device__ __forceinline__ void load_lds16(const void* g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
+// The same from `base` (one address for all lanes) + off bytes.
+__device__ __forceinline__ void load_lds16(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 // This wave's loads have landed; then every wave's have, and every wave is
-// done with what it read before.
+// done with what it read before.  The wait is the builtin (vmcnt 0, lgkmcnt 0),
+// which the compiler takes into account: it then adds no wait of its own, among
+// this tile's products, for loads issued before.
 __device__ __forceinline__ void tile_ready() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(p)));
@@ -162,36 +172,51 @@ struct Flash {
   // Requests tile kt into buffer b.
   __device__ void request(int32_t kt, int b) {
     const int32_t key0 = kt * kKeys;
-    const int lrow = lane / LPR, c = lane % LPR;  // this lane's row of an instruction's RPI, its chunk's place
-    const uint32_t dst = lds0 + b * BUF + wave * WROWS * ROW_BYTES;
+    // made anew for every tile (the empty asm hides that they never change):
+    // offsets kept across tiles would be spilled, and a reload waits for all
+    // loads in flight
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int lrow = ln / LPR, c = ln % LPR;  // this lane's row of an instruction's RPI, its chunk's place
+    const int wrow = wave * WROWS;
+    const uint32_t dst = lds0 + b * BUF + wrow * ROW_BYTES;
     if (key0 + kKeys <= q.ctx) {
       // all cached: 16-row groups lie in one page each
       if (ids_at != (kt >> 4)) fetch_ids(kt >> 4);
 #pragma unroll
       for (int i = 0; i < WROWS / RPI; ++i) {
-        const int row = wave * WROWS + i * RPI;  // first row of the instruction, within the tile
+        const int row = wrow + i * RPI;  // first row of the instruction, within the tile
         const int src = (kt & 15) * 4 + row / 16;
         const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(ids), src);
         const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(static_cast<uint64_t>(ids) >> 32), src);
         const int64_t base = (static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo) + row % 16) * ROW_BYTES;
-        const int rr = row + lrow;
-        load_lds16(static_cast<const char*>(A.k_cache) + base + (lrow * ROW_BYTES + 16 * (c ^ k_perm(rr))), dst + i * 1024);
-        load_lds16(static_cast<const char*>(A.v_cache) + base + (lrow * ROW_BYTES + 16 * (c ^ v_perm(rr))),
-                   dst + TILE + i * 1024);
+        const uint32_t at = lrow * ROW_BYTES;
+        load_lds16(static_cast<const char*>(A.k_cache) + base, at + 16 * (c ^ k_perm(row + lrow)), dst + i * 1024);
+        load_lds16(static_cast<const char*>(A.v_cache) + base, at + 16 * (c ^ v_perm(row + lrow)), dst + TILE + i * 1024);
       }
-    } else {
+    } else if (key0 >= q.ctx) {
+      // all of the call's own rows (strides are below 2^24 elements); rows past
+      // the last key repeat it, and no row attends them
+      const int64_t first = q.row0 + (key0 - q.ctx);
+      const char* kp = static_cast<const char*>(A.k) + (first * A.k_stride + static_cast<int64_t>(kvh) * D) * 2;
+      const char* vp = static_cast<const char*>(A.v) + (first * A.v_stride + static_cast<int64_t>(kvh) * D) * 2;
+      const uint32_t ks = static_cast<uint32_t>(A.k_stride) * 2, vs = static_cast<uint32_t>(A.v_stride) * 2;
+      const int last = n_keys - 1 - key0;
 #pragma unroll
       for (int i = 0; i < WROWS / RPI; ++i) {
-        const int rr = wave * WROWS + i * RPI + lrow;
-        const int32_t j = min(key0 + rr, n_keys - 1);  // rows past the last key repeat it; no row attends them
-        const char *kp, *vp;
-        if (key0 >= q.ctx) {
-          kp = static_cast<const char*>(A.k) + ((q.row0 + (j - q.ctx)) * A.k_stride + kvh * D) * 2;
-          vp = static_cast<const char*>(A.v) + ((q.row0 + (j - q.ctx)) * A.v_stride + kvh * D) * 2;
-        } else {
-          kp = key_row<2>(A, q, A.k_cache, A.k, A.k_stride, kvh, j);
-          vp = key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j);
-        }
+        const int rr = wrow + i * RPI + lrow;
+        const uint32_t r = min(rr, last);
+        load_lds16(kp, r * ks + 16 * (c ^ k_perm(rr)), dst + i * 1024);
+        load_lds16(vp, r * vs + 16 * (c ^ v_perm(rr)), dst + TILE + i * 1024);
+      }
+    } else {
+      // both kinds: at most one tile of a sequence
+#pragma unroll 1
+      for (int i = 0; i < WROWS / RPI; ++i) {
+        const int rr = wrow + i * RPI + lrow;
+        const int32_t j = min(key0 + rr, n_keys - 1);
+        const char* kp = key_row<2>(A, q, A.k_cache, A.k, A.k_stride, kvh, j);
+        const char* vp = key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j);
         load_lds16(kp + 16 * (c ^ k_perm(rr)), dst + i * 1024);
         load_lds16(vp + 16 * (c ^ v_perm(rr)), dst + TILE + i * 1024);
       }

@@ -441,7 +441,8 @@ gdn_status gdn_verify_tree_slots(const gdn_geometry* g, float* state, float* con
  *  o                 dtype  [rows][H_q][D]            contiguous
  *
  * Query head h reads KV head h / (H_q / H_kv).  Row strides let q, k and v be
- * the parts of one fused projection row; they are multiples of 16 bytes.
+ * the parts of one fused projection row; they are multiples of 16 bytes and
+ * less than 2^24 elements.
  * Logits, softmax statistics and outputs are accumulated in fp32; with
  * GDN_BF16 the softmax weights are rounded to bf16 for the product with V
  * (an error below the output's own rounding).  K and V rows at masked
