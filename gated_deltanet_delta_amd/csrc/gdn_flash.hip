@@ -249,25 +249,39 @@ struct Flash {
     return bad;
   }
 
-  // The 32 keys from row `base` of the tile in buffer b on, their logits and
+  // LDS addresses of this lane's operands in a tile: K rows are read 16 bytes
+  // at k-step s, V rows transposed at O^T tile dt.  The permutations touch the
+  // low bits of s and dt alone, so a few addresses serve a whole tile, the rest
+  // being constant offsets.
+  static constexpr int KA = NS < 8 ? NS : 8, VA = NT < 4 ? NT : 4;
+  __device__ void tile_addresses(int b, uint32_t (&ka)[KA], uint32_t (&va)[VA]) const {
+    int ln = lane;  // made anew per tile, see request()
+    asm volatile("" : "+v"(ln));
+    const uint32_t buf = lds0 + b * BUF + kw * (kKeys / KW) * ROW_BYTES;
+    const int kcol = ln & 31, kx = k_perm(kcol);  // blocks start at multiples of 32 rows
+#pragma unroll
+    for (int s = 0; s < KA; ++s) ka[s] = buf + kcol * ROW_BYTES + 16 * ((2 * s + (ln >> 5)) ^ kx);
+    const int g2 = (ln >> 4) & 1, mrow = (ln & 15) >> 2, quarter = ln & 3;
+    const uint32_t vrow = buf + TILE + (4 * (ln >> 5) + mrow) * ROW_BYTES + 8 * (quarter & 1);
+#pragma unroll
+    for (int dt = 0; dt < VA; ++dt)  // rows of one read differ from mrow by multiples of 4
+      va[dt] = vrow + 16 * ((dt * 4 + 2 * g2 + (quarter >> 1)) ^ v_perm(mrow));
+  }
+
+  // The 32 keys of block kb of this wave's part of a tile: their logits and
   // their terms.  MASKED: some row does not attend every key of the tile.
   template <bool MASKED>
-  __device__ void block(int32_t key0, char* kbuf, char* vbuf, int base, uint64_t bad) {
+  __device__ void block(int32_t key0, int kb, const uint32_t (&ka)[KA], const uint32_t (&va)[VA], uint64_t bad) {
+    typedef __attribute__((address_space(3))) const bf16x8_t* lds_k;
+    typedef __attribute__((address_space(3))) s16x4_t* lds_v;
+    const int base = (kw * KB + kb) * 32;  // first row within the tile
     // ---- logits ----
     f32x16_t S;
-    // The lane's offsets are made anew for every block (the empty asm hides
-    // that they never change): kept across blocks they would push others out
-    // of the 256 registers.
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const int kcol = ln & 31, khalf = ln >> 5;
-    const char* krow = kbuf + (base + kcol) * ROW_BYTES;
-    const int kx = k_perm(kcol);  // blocks start at multiples of 32 rows
 #pragma unroll
     for (int e = 0; e < 16; ++e) S[e] = 0.f;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(krow + 16 * ((2 * s + khalf) ^ kx));
+      const bf16x8_t a = *(lds_k)(ka[s % KA] + (s / KA) * 256 + kb * 32 * ROW_BYTES);
       S = mfma32x32(a, qf[s], S);
     }
     // K operands four instructions ahead, no more: registers are short
@@ -299,28 +313,26 @@ struct Flash {
     }
     const float off = m == -INFINITY ? 0.f : -m * A.scale_log2;
     // ---- weights; rounded to bf16 for the product: each is off by at most
-    // 2^-8 of itself, below the output's own rounding on average over keys ----
+    // 2^-8 of itself, below the output's own rounding on average over keys.  The
+    // sum takes the rounded weights too, two to an instruction ----
     bf16x8_t P[2];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       S[e] = __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, off));
-      l += S[e];
+      P[e / 8][e % 8] = static_cast<__bf16>(S[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) P[e / 8][e % 8] = static_cast<__bf16>(S[e]);
+    for (int e = 0; e < 16; e += 2)
+      l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{P[e / 8][e % 8], P[e / 8][e % 8 + 1]}, bf16x2_t{1.0f, 1.0f}, l, false);
     // ---- O^T += V^T P^T ----
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" : "+v"(ln));
-    const int g2 = (ln >> 4) & 1, mrow = (ln & 15) >> 2, quarter = ln & 3;
-    const char* vrow = vbuf + (base + 4 * (ln >> 5) + mrow) * ROW_BYTES + 8 * (quarter & 1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
       for (int dt = 0; dt < NT; ++dt) {
-        const int chunk = (dt * 4 + 2 * g2 + (quarter >> 1)) ^ v_perm(mrow);  // rows differ from mrow by multiples of 4
-        typedef __attribute__((address_space(3))) s16x4_t* lp;
-        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vrow + 16 * ks * ROW_BYTES + 16 * chunk));
-        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vrow + (16 * ks + 8) * ROW_BYTES + 16 * chunk));
+        const uint32_t at = va[dt % VA] + (dt / VA) * 256 + (kb * 32 + 16 * ks) * ROW_BYTES;
+        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at));
+        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at + 8 * ROW_BYTES));
         O[dt] = mfma32x32(__builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), P[ks], O[dt]);
       }
     __builtin_amdgcn_sched_group_barrier(kSchedLds, 6, 1);
@@ -331,7 +343,8 @@ struct Flash {
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MASKED) {
-      // the terms of the V rows that clear_bad() took out, for the rows that attend them
+      // the terms of the V rows that clear_bad() took out, for the rows that
+      // attend them (their weights are in S, unrounded)
       for (uint32_t left = static_cast<uint32_t>(bad >> base); left != 0; left &= left - 1) {
         const int kr = __builtin_ctz(left);
         float p = 0.f;  // the weight, in the lanes of half (kr / 4) % 2
@@ -355,11 +368,12 @@ struct Flash {
   // One tile in buffer b.
   template <bool MASKED>
   __device__ void tile(int32_t kt, int b) {
-    char* kbuf = lds + b * BUF;
     uint64_t bad = 0;
-    if constexpr (MASKED) bad = clear_bad(kbuf + TILE);
+    if constexpr (MASKED) bad = clear_bad(lds + b * BUF + TILE);
+    uint32_t ka[KA], va[VA];
+    tile_addresses(b, ka, va);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * kKeys, kbuf, kbuf + TILE, (kw * KB + kb) * 32, bad);
+    for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * kKeys, kb, ka, va, bad);
   }
 
   // Tiles [lo, hi) of the unit, the first already requested into buffer 0;
