@@ -2,19 +2,19 @@
 // gdn_attn.hip): 32x32x16 matrix instructions on key tiles that the waves of a
 // workgroup share through LDS.
 //
-// A wave owns 32 rows.  S^T = K Q^T takes K as the A operand from LDS and Q^T
-// from registers; lane l then holds row l % 32 and keys 8 (i / 4) + 4 (l / 32) +
-// i % 4 of a block of 32.  O^T = V^T P^T contracts 16 keys per instruction: lane
-// l's eight weights of one instruction are its accumulators 8 ks .. 8 ks + 7 as
-// they are, and V^T's operand is read out of the V tile in the same key order
-// with transposing LDS reads (ds_read_b64_tr_b16).
+// A wave owns RB blocks of 32 rows.  S^T = K Q^T takes K as the A operand from
+// LDS and Q^T from registers; lane l then holds row l % 32 and keys 8 (i / 4) +
+// 4 (l / 32) + i % 4 of a block of 32.  O^T = V^T P^T contracts 16 keys per
+// instruction: lane l's eight weights of one instruction are its accumulators
+// 8 ks .. 8 ks + 7 as they are, and V^T's operand is read out of the V tile in
+// the same key order with transposing LDS reads (ds_read_b64_tr_b16).
 //
-// Tiles of 64 keys go from memory to LDS without passing registers
-// (global_load_lds, 16 bytes per lane), the next tile's loads in flight while
-// this one is used.  Rows lie unpadded in LDS, their 16-byte chunks permuted by
-// an XOR with row bits so that both kinds of reads hit all banks: K reads take
-// one chunk of 16 consecutive rows (chunk ^ row % 16), transposing reads four
-// chunks of four consecutive rows (chunk ^ 4 (row % 4)).
+// Tiles go from memory to LDS without passing registers (global_load_lds, 16
+// bytes per lane), up to NST - 1 of them in flight while one is used.  Rows lie
+// unpadded in LDS, their 16-byte chunks permuted by an XOR with row bits so that
+// both kinds of reads hit all banks: K reads take one chunk of 16 consecutive
+// rows (chunk ^ row % 16), transposing reads four chunks of four consecutive
+// rows (chunk ^ 4 (row % 4)).
 #include "gdn_attn_device.h"
 
 namespace gdn {
@@ -24,7 +24,6 @@ namespace {
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kKeys = 64;  // keys of a tile
 constexpr int kSchedMfma = 0x8, kSchedLds = 0x100;  // instruction classes of sched_group_barrier: MFMA, LDS reads
 
 // 16 bytes per lane from memory to LDS at `lds` + 16 lane (lds: a byte address,
@@ -40,15 +39,26 @@ __device__ __forceinline__ void load_lds16(const char* base, uint32_t off, uint3
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
-// This wave's loads have landed; then every wave's have, and every wave is
-// done with what it read before.  The wait is the builtin (vmcnt 0, lgkmcnt 0),
+// All but this wave's newest LEFT loads have landed; then every wave's have,
+// and every wave is done with what it read before.  The wait is the builtin,
 // which the compiler takes into account: it then adds no wait of its own, among
-// this tile's products, for loads issued before.
-__device__ __forceinline__ void tile_ready() {
+// a tile's products, for loads issued before.
+template <int LEFT>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(LEFT >= 0 && LEFT < 64, "vmcnt has six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | 0x0070);  // vmcnt LEFT, lgkmcnt 0
+  asm volatile("" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void tile_ready() {
+  wait_loads<LEFT>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+// One 32-bit word per lane from memory to LDS at `lds` + 4 lane.
+__device__ __forceinline__ void load_lds4(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(p)));
@@ -69,26 +79,28 @@ __device__ __forceinline__ float half_sum(float x) {
 
 }  // namespace
 
-// RW waves of 32 rows each, times KW waves that share a row block and take
-// 64 / KW keys of every tile each.
-template <int D, int RW, int KW, bool TREE>
+// NW waves move KT-key tiles through NST buffers; the first RW of them compute,
+// 32 RB rows each.
+template <int D, int RW, int RB, int NW, int KT, int NST, bool TREE>
 struct Flash {
-  static constexpr int NW = RW * KW, THREADS = 64 * NW, BM = 32 * RW;
+  static constexpr int THREADS = 64 * NW, WR = 32 * RB, BM = WR * RW;
   static constexpr int ROW_BYTES = D * 2;
-  static constexpr int TILE = kKeys * ROW_BYTES;         // K or V of a tile
+  static constexpr int TILE = KT * ROW_BYTES;            // K or V of a tile
   static constexpr int BUF = 2 * TILE;
   static constexpr int NS = D / 16, NT = D / 32;         // k-steps of the logits, 32-row tiles of O^T
-  static constexpr int KB = 2 / KW;                      // 32-key blocks per wave and tile
+  static constexpr int KB = KT / 32;                     // 32-key blocks per tile
   static constexpr int RPI = 1024 / ROW_BYTES;           // rows of one load instruction
-  static constexpr int WROWS = kKeys / NW;               // rows a wave loads
+  static constexpr int WROWS = KT / NW;                  // rows a wave loads
+  static constexpr int LPT = 2 * (WROWS / RPI);          // load instructions of a wave and tile
   static constexpr int LPR = 64 / RPI;                   // lanes per row
   static constexpr int CH = D / 8;                       // 16-byte chunks of a row
-  static constexpr int KX = D >= 128 ? 15 : 7;           // bits of the K permutation
-  // LDS: two buffers, then flags (two words: keys whose V row is not finite)
-  static constexpr size_t LDS_TILES = 2 * static_cast<size_t>(BUF);
-  // join() lays the sums of RW waves and their statistics over the buffers
-  static constexpr size_t LDS_JOIN = KW == 2 ? static_cast<size_t>(BM) * (D + 2) * 4 : 0;
-  static constexpr size_t LDS = LDS_TILES + 16 > LDS_JOIN ? LDS_TILES + 16 : LDS_JOIN;
+  static constexpr int GROUP = 16;                       // tokens of a page come in multiples of this
+  static constexpr int TPI = 64 * GROUP / KT;            // tiles whose groups the lanes' page ids cover
+  static_assert(WROWS % RPI == 0 && WROWS > 0 && (NST & (NST - 1)) == 0 && RPI <= GROUP && WROWS % 2 == 0, "shape");
+  // LDS: NST buffers, per wave two rounds of page ids, flags (keys whose V row is not finite)
+  static constexpr size_t LDS_TILES = static_cast<size_t>(NST) * BUF;
+  static constexpr size_t LDS_FLAGS = LDS_TILES + NW * 512;
+  static constexpr size_t LDS = LDS_FLAGS + 16;
 
   __device__ static int k_perm(int row) { return D >= 128 ? row & 15 : (row >> 1) & 7; }
   __device__ static int v_perm(int row) { return D >= 128 ? (row & 3) * 4 : ((row >> 1) & 1) * 4; }
@@ -96,34 +108,33 @@ struct Flash {
   const AttnArgs& A;
   char* lds;
   uint32_t lds0;
-  int lane, wave, rw, kw, col, half;
+  int lane, wave, col, half;
   // the unit of work: one KV head of one sequence, a block of rows
   Seq q;
   int kvh;
-  bool row_ok;
-  int t, head;         // this lane's token and query head
-  uint64_t path;       // TREE: this lane's row's nodes
   int32_t n_keys, clear;
-  // base rows of the cached tokens, one 16-row group per lane: lane i holds
-  // ((page * H_kv + kvh) P + offset) of key 1024 ids_at + 16 i
+  int64_t r0;            // its first row
+  int t[RB];             // this lane's tokens
+  uint64_t path[RB];     // TREE: the rows' nodes
+  // base rows ((page * H_kv + kvh) P + offset) of the cached 16-token groups,
+  // one per lane: lane i holds that of key 1024 ids_at + 16 i
   int32_t ids_at;
   int64_t ids;
-  bf16x8_t qf[NS];
-  f32x16_t O[NT];
-  float m, l;          // running maximum (of unscaled logits), this lane's part of the sum
+  bf16x8_t qf[RB][NS];
+  f32x16_t O[RB][NT];
+  float m[RB], l[RB];    // running maximum (of unscaled logits), this lane's part of the sum
 
   __device__ Flash(const AttnArgs& a, char* smem) : A(a), lds(smem) {
     lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    rw = wave / KW;
-    kw = wave % KW;
     col = lane & 31;
     half = lane >> 5;
   }
 
   // The unit: rows r0 .. r0 + BM - 1 (of n G) of KV head h of sequence q.
-  __device__ void begin_keys(int64_t r0, int h) {
+  __device__ void begin_keys(int64_t first_row, int h) {
+    r0 = first_row;
     kvh = h;
     const int64_t rows = static_cast<int64_t>(q.n) * A.G;
     const int64_t r_last = r0 + BM < rows ? r0 + BM - 1 : rows - 1;
@@ -131,47 +142,63 @@ struct Flash {
     clear = TREE ? q.ctx : q.ctx + static_cast<int32_t>(r0 / A.G) + 1;
     ids_at = -1;
   }
-  // This lane's row and its Q; node_paths (TREE): lane j holds node j's path.
-  __device__ void begin_rows(int64_t r0, uint64_t node_paths) {
-    const int64_t r = r0 + rw * 32 + col;
-    row_ok = r < static_cast<int64_t>(q.n) * A.G;
-    const int32_t rc = static_cast<int32_t>(row_ok ? r - r0 : 0);
+  // This lane's rows and their Q; node_paths (TREE): lane j holds node j's path.
+  // Query head of this lane's row of block rb, and its token; -1: no row (the
+  // token is then the unit's first).
+  __device__ int row_head(int rb, int* token) const {
     const int32_t t0 = static_cast<int32_t>(r0 / A.G), h0 = static_cast<int32_t>(r0 - static_cast<int64_t>(t0) * A.G);
-    t = t0 + (h0 + rc) / A.G;
-    head = kvh * A.G + (h0 + rc) % A.G;
-    if constexpr (TREE)
-      path = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(node_paths >> 32), t, 64)) << 32) |
-             static_cast<uint32_t>(__shfl(static_cast<uint32_t>(node_paths), t, 64));
-    const uint16_t* qp = static_cast<const uint16_t*>(A.q) + (q.row0 + t) * A.q_stride + static_cast<int64_t>(head) * D;
+    const int32_t r = wave * WR + rb * 32 + col;
+    const bool ok = wave < RW && r < static_cast<int64_t>(q.n) * A.G - r0;
+    const int32_t rc = ok ? r : 0;
+    *token = t0 + (h0 + rc) / A.G;
+    return ok ? kvh * A.G + (h0 + rc) % A.G : -1;
+  }
+  __device__ void begin_rows(uint64_t node_paths) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(qp + s * 16 + half * 8);
+    for (int rb = 0; rb < RB; ++rb) {
+      int hd = row_head(rb, &t[rb]);
+      if (hd < 0) hd = kvh * A.G;  // reads some row of the call's
+      if constexpr (TREE)
+        path[rb] = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(node_paths >> 32), t[rb], 64)) << 32) |
+                   static_cast<uint32_t>(__shfl(static_cast<uint32_t>(node_paths), t[rb], 64));
+      const uint16_t* qp = static_cast<const uint16_t*>(A.q) + (q.row0 + t[rb]) * A.q_stride + static_cast<int64_t>(hd) * D;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int s = 0; s < NS; ++s) qf[rb][s] = *reinterpret_cast<const bf16x8_t*>(qp + s * 16 + half * 8);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) O[i][e] = 0.f;
-    m = -INFINITY;
-    l = 0.f;
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) O[rb][i][e] = 0.f;
+      m[rb] = -INFINITY;
+      l[rb] = 0.f;
+    }
   }
 
-  // Base rows of the 16-row groups of keys 1024 at ..: one page lookup per lane.
-  __device__ void fetch_ids(int32_t at) {
+  // Page ids of round `at` (keys 1024 at ..), one 16-token group per lane, into
+  // this wave's LDS: requested a round ahead, so nothing waits for them.
+  __device__ uint32_t ids_lds(int32_t at) const { return LDS_TILES + wave * 512 + (at & 1) * 256; }
+  __device__ void request_ids(int32_t at) {
+    const int32_t key = at * 1024 + lane * GROUP;  // below 2^30 + 2^11
+    load_lds4(A.block_table + static_cast<size_t>(q.index) * A.max_pages + (key < q.ctx ? key / A.page : 0), lds0 + ids_lds(at));
+  }
+  // Takes round `at`, which has landed, into ids; asks for the next.
+  __device__ void take_ids(int32_t at) {
     ids_at = at;
-    const int32_t key = at * 1024 + lane * 16;
+    const int32_t key = at * 1024 + lane * GROUP;
+    int32_t page = *reinterpret_cast<const int32_t*>(lds + ids_lds(at) + 4 * lane);
     ids = 0;
     if (key < q.ctx) {
-      const int32_t e = key / A.page;
-      int32_t page = A.block_table[static_cast<size_t>(q.index) * A.max_pages + e];
       if (page < 0 || page >= A.n_pages) {
         report_error(A.dev_err, GDN_DEV_BAD_PAGE);
         page = 0;
       }
-      ids = (static_cast<int64_t>(page) * A.Hk + kvh) * A.page + (key - e * A.page);
+      ids = (static_cast<int64_t>(page) * A.Hk + kvh) * A.page + (key - key / A.page * A.page);
     }
+    if ((at + 1) * 1024 < q.ctx) request_ids(at + 1);
   }
 
   // Requests tile kt into buffer b.
   __device__ void request(int32_t kt, int b) {
-    const int32_t key0 = kt * kKeys;
+    const int32_t key0 = kt * KT;
     // made anew for every tile (the empty asm hides that they never change):
     // offsets kept across tiles would be spilled, and a reload waits for all
     // loads in flight
@@ -180,16 +207,22 @@ struct Flash {
     const int lrow = ln / LPR, c = ln % LPR;  // this lane's row of an instruction's RPI, its chunk's place
     const int wrow = wave * WROWS;
     const uint32_t dst = lds0 + b * BUF + wrow * ROW_BYTES;
-    if (key0 + kKeys <= q.ctx) {
+    if (key0 + KT <= q.ctx) {
       // all cached: 16-row groups lie in one page each
-      if (ids_at != (kt >> 4)) fetch_ids(kt >> 4);
+      if (ids_at != kt / TPI) {
+        if (ids_at != kt / TPI - 1 || ids_at < 0) {  // the unit's first: not asked for before
+          request_ids(kt / TPI);
+          wait_loads<0>();
+        }
+        take_ids(kt / TPI);
+      }
 #pragma unroll
       for (int i = 0; i < WROWS / RPI; ++i) {
         const int row = wrow + i * RPI;  // first row of the instruction, within the tile
-        const int src = (kt & 15) * 4 + row / 16;
+        const int src = (kt % TPI) * (KT / GROUP) + row / GROUP;
         const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(ids), src);
         const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(static_cast<uint64_t>(ids) >> 32), src);
-        const int64_t base = (static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo) + row % 16) * ROW_BYTES;
+        const int64_t base = (static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo) + row % GROUP) * ROW_BYTES;
         const uint32_t at = lrow * ROW_BYTES;
         load_lds16(static_cast<const char*>(A.k_cache) + base, at + 16 * (c ^ k_perm(row + lrow)), dst + i * 1024);
         load_lds16(static_cast<const char*>(A.v_cache) + base, at + 16 * (c ^ v_perm(row + lrow)), dst + TILE + i * 1024);
@@ -223,26 +256,27 @@ struct Flash {
     }
   }
 
-  // Does this lane's row attend key j?
-  __device__ bool attends(int32_t j) const {
+  // Does this lane's row of block rb attend key j?
+  __device__ bool attends(int rb, int32_t j) const {
     const int32_t own = j - q.ctx;
-    if constexpr (TREE) return own < 0 || (own < q.n && ((path >> own) & 1ull));
-    else return own <= t;
+    if constexpr (TREE) return own < 0 || (own < q.n && ((path[rb] >> own) & 1ull));
+    else return own <= t[rb];
   }
 
   // Values that are not finite must not reach rows that do not attend their
   // key (0 x inf is NaN).  In a tile that some row attends in part: finds such
-  // V rows and clears them in LDS; their terms are added by add_bad().
+  // V rows and clears them in LDS; their terms are added apart in block().
+  // All waves call it.
   __device__ uint64_t clear_bad(char* v) {
-    uint32_t* flags = reinterpret_cast<uint32_t*>(lds + LDS_TILES);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(lds + LDS_FLAGS);
     if (threadIdx.x < 2) flags[threadIdx.x] = 0;
     __syncthreads();
-    for (int e = threadIdx.x; e < kKeys * CH; e += THREADS)
+    for (int e = threadIdx.x; e < KT * CH; e += THREADS)
       if (any_nonfinite<true>(*reinterpret_cast<const uint4*>(v + e * 16))) atomicOr(&flags[e / CH / 32], 1u << (e / CH % 32));
     __syncthreads();
     const uint64_t bad = (static_cast<uint64_t>(flags[1]) << 32) | flags[0];
     if (bad != 0) {
-      for (int e = threadIdx.x; e < kKeys * CH; e += THREADS)
+      for (int e = threadIdx.x; e < KT * CH; e += THREADS)
         if ((bad >> (e / CH)) & 1ull) *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();  // the flags are read, and the rows cleared, by every wave
@@ -254,13 +288,18 @@ struct Flash {
   // low bits of s and dt alone, so a few addresses serve a whole tile, the rest
   // being constant offsets.
   static constexpr int KA = NS < 8 ? NS : 8, VA = NT < 4 ? NT : 4;
-  __device__ void tile_addresses(int b, uint32_t (&ka)[KA], uint32_t (&va)[VA]) const {
+  __device__ void k_addresses(int b, uint32_t (&ka)[KA]) const {
     int ln = lane;  // made anew per tile, see request()
     asm volatile("" : "+v"(ln));
-    const uint32_t buf = lds0 + b * BUF + kw * (kKeys / KW) * ROW_BYTES;
+    const uint32_t buf = lds0 + b * BUF;
     const int kcol = ln & 31, kx = k_perm(kcol);  // blocks start at multiples of 32 rows
 #pragma unroll
     for (int s = 0; s < KA; ++s) ka[s] = buf + kcol * ROW_BYTES + 16 * ((2 * s + (ln >> 5)) ^ kx);
+  }
+  __device__ void v_addresses(int b, uint32_t (&va)[VA]) const {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const uint32_t buf = lds0 + b * BUF;
     const int g2 = (ln >> 4) & 1, mrow = (ln & 15) >> 2, quarter = ln & 3;
     const uint32_t vrow = buf + TILE + (4 * (ln >> 5) + mrow) * ROW_BYTES + 8 * (quarter & 1);
 #pragma unroll
@@ -268,64 +307,81 @@ struct Flash {
       va[dt] = vrow + 16 * ((dt * 4 + 2 * g2 + (quarter >> 1)) ^ v_perm(mrow));
   }
 
-  // The 32 keys of block kb of this wave's part of a tile: their logits and
-  // their terms.  MASKED: some row does not attend every key of the tile.
+  // The 32 keys of block kb of a tile: their logits and their terms.
+  // MASKED: some row does not attend every key of the tile.
   template <bool MASKED>
-  __device__ void block(int32_t key0, int kb, const uint32_t (&ka)[KA], const uint32_t (&va)[VA], uint64_t bad) {
+  __device__ void block(int32_t key0, int kb, int b, const uint32_t (&ka)[KA], uint64_t bad) {
     typedef __attribute__((address_space(3))) const bf16x8_t* lds_k;
     typedef __attribute__((address_space(3))) s16x4_t* lds_v;
-    const int base = (kw * KB + kb) * 32;  // first row within the tile
     // ---- logits ----
-    f32x16_t S;
+    f32x16_t S[RB];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) S[e] = 0.f;
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) S[rb][e] = 0.f;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const bf16x8_t a = *(lds_k)(ka[s % KA] + (s / KA) * 256 + kb * 32 * ROW_BYTES);
-      S = mfma32x32(a, qf[s], S);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) S[rb] = mfma32x32(a, qf[rb][s], S[rb]);
     }
-    // K operands four instructions ahead, no more: registers are short
+    // K operands four steps ahead, no more: registers are short
     __builtin_amdgcn_sched_group_barrier(kSchedLds, 4, 0);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, RB, 0);
       if (s < NS - 4) __builtin_amdgcn_sched_group_barrier(kSchedLds, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
     // ---- running maximum ----
-    float mx = -INFINITY;
+    float mx[RB];
+    bool grown = false;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if constexpr (MASKED) S[e] = attends(key0 + base + 8 * (e / 4) + 4 * half + e % 4) ? S[e] : -INFINITY;
-      mx = fmaxf(mx, S[e]);
+    for (int rb = 0; rb < RB; ++rb) {
+      mx[rb] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if constexpr (MASKED) S[rb][e] = attends(rb, key0 + kb * 32 + 8 * (e / 4) + 4 * half + e % 4) ? S[rb][e] : -INFINITY;
+        mx[rb] = fmaxf(mx[rb], S[rb][e]);
+      }
+      mx[rb] = half_max(mx[rb]);
+      grown |= (mx[rb] - m[rb]) * A.scale_log2 > 8.f;
     }
-    mx = half_max(mx);
     // The weights are taken against a maximum that may lag: O and l are scaled
     // only when some row's maximum has grown by more than 2^8 in weight, which
     // leaves sums and weights far inside their range.
-    if (__any((mx - m) * A.scale_log2 > 8.f)) {
-      const float m_new = fmaxf(m, mx);
-      const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * A.scale_log2);
-      m = m_new;
-      l *= f;
+    if (__any(grown)) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) O[i] *= f;
+      for (int rb = 0; rb < RB; ++rb) {
+        const float m_new = fmaxf(m[rb], mx[rb]);
+        const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[rb] - m_new) * A.scale_log2);
+        m[rb] = m_new;
+        l[rb] *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) O[rb][i] *= f;
+      }
     }
-    const float off = m == -INFINITY ? 0.f : -m * A.scale_log2;
     // ---- weights; rounded to bf16 for the product: each is off by at most
     // 2^-8 of itself, below the output's own rounding on average over keys.  The
     // sum takes the rounded weights too, two to an instruction ----
-    bf16x8_t P[2];
+    bf16x8_t P[RB][2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      S[e] = __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, off));
-      P[e / 8][e % 8] = static_cast<__bf16>(S[e]);
+    for (int rb = 0; rb < RB; ++rb) {
+      const float off = m[rb] == -INFINITY ? 0.f : -m[rb] * A.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        S[rb][e] = __builtin_amdgcn_exp2f(fmaf(S[rb][e], A.scale_log2, off));
+        P[rb][e / 8][e % 8] = static_cast<__bf16>(S[rb][e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e += 2)
+        l[rb] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{P[rb][e / 8][e % 8], P[rb][e / 8][e % 8 + 1]}, bf16x2_t{1.0f, 1.0f},
+                                                l[rb], false);
     }
-#pragma unroll
-    for (int e = 0; e < 16; e += 2)
-      l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{P[e / 8][e % 8], P[e / 8][e % 8 + 1]}, bf16x2_t{1.0f, 1.0f}, l, false);
     // ---- O^T += V^T P^T ----
     __builtin_amdgcn_sched_barrier(0);
+    uint32_t va[VA];
+    v_addresses(b, va);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -333,33 +389,38 @@ struct Flash {
         const uint32_t at = va[dt % VA] + (dt / VA) * 256 + (kb * 32 + 16 * ks) * ROW_BYTES;
         const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at));
         const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at + 8 * ROW_BYTES));
-        O[dt] = mfma32x32(__builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), P[ks], O[dt]);
+        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) O[rb][dt] = mfma32x32(a, P[rb][ks], O[rb][dt]);
       }
     __builtin_amdgcn_sched_group_barrier(kSchedLds, 6, 1);
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, RB, 1);
       if (i < 2 * NT - 3) __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MASKED) {
       // the terms of the V rows that clear_bad() took out, for the rows that
       // attend them (their weights are in S, unrounded)
-      for (uint32_t left = static_cast<uint32_t>(bad >> base); left != 0; left &= left - 1) {
+      for (uint32_t left = static_cast<uint32_t>(bad >> (kb * 32)); left != 0; left &= left - 1) {
         const int kr = __builtin_ctz(left);
-        float p = 0.f;  // the weight, in the lanes of half (kr / 4) % 2
+        const int32_t j = key0 + kb * 32 + kr;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p = (8 * (e / 4) + e % 4) == (kr & ~4) ? S[e] : p;
-        p = __shfl(p, col + 32 * ((kr >> 2) & 1), 64);
-        const int32_t j = key0 + base + kr;
-        if (!attends(j)) continue;
-        const uint16_t* vr =
-            reinterpret_cast<const uint16_t*>(key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j)) + 4 * half;
+        for (int rb = 0; rb < RB; ++rb) {
+          float p = 0.f;  // the weight, in the lanes of half (kr / 4) % 2
 #pragma unroll
-        for (int dt = 0; dt < NT; ++dt) {
+          for (int e = 0; e < 16; ++e) p = (8 * (e / 4) + e % 4) == (kr & ~4) ? S[rb][e] : p;
+          p = __shfl(p, col + 32 * ((kr >> 2) & 1), 64);
+          if (!attends(rb, j)) continue;
+          const uint16_t* vr =
+              reinterpret_cast<const uint16_t*>(key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j)) + 4 * half;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) O[dt][i] += p * bf16_bits_to_f32(vr[dt * 32 + 8 * (i / 4) + i % 4]);
-          asm volatile("" ::: "memory");  // no more than one step's loads at a time in registers
+          for (int dt = 0; dt < NT; ++dt) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) O[rb][dt][i] += p * bf16_bits_to_f32(vr[dt * 32 + 8 * (i / 4) + i % 4]);
+            asm volatile("" ::: "memory");  // no more than one step's loads at a time in registers
+          }
         }
       }
     }
@@ -370,96 +431,79 @@ struct Flash {
   __device__ void tile(int32_t kt, int b) {
     uint64_t bad = 0;
     if constexpr (MASKED) bad = clear_bad(lds + b * BUF + TILE);
-    uint32_t ka[KA], va[VA];
-    tile_addresses(b, ka, va);
+    if (wave < RW) {
+      uint32_t ka[KA];
+      k_addresses(b, ka);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * kKeys, kb, ka, va, bad);
+      for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * KT, kb, b, ka, bad);
+    }
   }
 
+  // Tile kt of [lo, hi) has landed, for every wave; asks for the tile NST - 1 ahead.
+  __device__ void step(int32_t kt, int32_t lo, int32_t hi) {
+    const int32_t newer = hi - 1 - kt;  // tiles asked for after kt: this many, NST - 2 at most
+    if (newer >= NST - 2) tile_ready<(NST - 2) * LPT>();
+    else if (NST > 3 && newer == 1) tile_ready<(NST > 3 ? LPT : 0)>();
+    else tile_ready<0>();
+    if (kt + NST - 1 < hi) request(kt + NST - 1, (kt + NST - 1 - lo) & (NST - 1));
+  }
   // Tiles [lo, hi) of the unit, the first already requested into buffer 0;
-  // leaves the sums of this wave's keys in O, m, l.
+  // leaves the sums in O, m, l.
   __device__ void keys(int32_t lo, int32_t hi) {
+    wait_loads<0>();  // Q is at hand, so no later wait is for it
+#pragma unroll 1
+    for (int i = 1; i < NST - 1 && lo + i < hi; ++i) request(lo + i, i);
     // tiles that every row attends whole, then the others
-    const int32_t mid = max(lo, min(hi, clear / kKeys));
+    const int32_t mid = max(lo, min(hi, clear / KT));
     int32_t kt = lo;
     for (; kt < mid; ++kt) {
-      tile_ready();
-      if (kt + 1 < hi) request(kt + 1, (kt + 1 - lo) & 1);
-      tile<false>(kt, (kt - lo) & 1);
+      step(kt, lo, hi);
+      tile<false>(kt, (kt - lo) & (NST - 1));
     }
     for (; kt < hi; ++kt) {
-      tile_ready();
-      if (kt + 1 < hi) request(kt + 1, (kt + 1 - lo) & 1);
-      tile<true>(kt, (kt - lo) & 1);
+      step(kt, lo, hi);
+      tile<true>(kt, (kt - lo) & (NST - 1));
     }
-    l = half_sum(l);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) l[rb] = half_sum(l[rb]);
   }
 
   // Element (dt, i) of O is d = 32 dt + 8 (i / 4) + 4 half + i % 4.
-  __device__ void write_out() {
-    if (!row_ok || kw != 0) return;
-    const float inv = 1.0f / l;
-    uint16_t* o = static_cast<uint16_t*>(A.o) + (static_cast<size_t>(q.row0 + t) * A.Hq + head) * D + 4 * half;
+  __device__ void write_out(int rb, int head) const {
+    const float inv = 1.0f / l[rb];
+    uint16_t* o = static_cast<uint16_t*>(A.o) + (static_cast<size_t>(q.row0 + t[rb]) * A.Hq + head) * D + 4 * half;
 #pragma unroll
     for (int dt = 0; dt < NT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<uint2*>(o + 32 * dt + 2 * i) =
-            make_uint2(pack2_bf16(O[dt][i] * inv, O[dt][i + 1] * inv), pack2_bf16(O[dt][i + 2] * inv, O[dt][i + 3] * inv));
+        *reinterpret_cast<uint2*>(o + 32 * dt + 2 * i) = make_uint2(pack2_bf16(O[rb][dt][i] * inv, O[rb][dt][i + 1] * inv),
+                                                                    pack2_bf16(O[rb][dt][i + 2] * inv, O[rb][dt][i + 3] * inv));
   }
-  // Unscaled sums and (scaled maximum, sum) of this lane's row.
-  __device__ void write_part(float* sums, float* ml) const {
+  // Unscaled sums and (scaled maximum, sum) of this lane's row of block rb.
+  __device__ void write_part(int rb, float* sums, float* ml) const {
 #pragma unroll
     for (int dt = 0; dt < NT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<f32x4_t*>(sums + 32 * dt + 2 * i + 4 * half) =
-            f32x4_t{O[dt][i], O[dt][i + 1], O[dt][i + 2], O[dt][i + 3]};
+            f32x4_t{O[rb][dt][i], O[rb][dt][i + 1], O[rb][dt][i + 2], O[rb][dt][i + 3]};
     if (half == 0) {
-      ml[0] = m * A.scale_log2;
-      ml[1] = l;
-    }
-  }
-
-  // KW waves of a row block: joins their sums in wave kw = 0 (through LDS, the
-  // tile buffers being free).  All waves of the workgroup call it.
-  __device__ void join() {
-    if constexpr (KW == 2) {
-      __syncthreads();
-      float* at = reinterpret_cast<float*>(lds) + rw * 32 * (D + 2);
-      // [element][lane] so that a wave's accesses are consecutive
-      if (kw == 1) {
-#pragma unroll
-        for (int dt = 0; dt < NT; ++dt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) at[(dt * 16 + i) * 64 + lane] = O[dt][i];
-        if (half == 0) {
-          at[32 * D + col] = m;
-          at[32 * D + 32 + col] = l;
-        }
-      }
-      __syncthreads();
-      if (kw == 0) {
-        const float m1 = at[32 * D + col], l1 = at[32 * D + 32 + col];
-        const float m_new = fmaxf(m, m1);
-        const float f0 = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * A.scale_log2);
-        const float f1 = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m1 - m_new) * A.scale_log2);
-        m = m_new;
-        l = l * f0 + l1 * f1;
-#pragma unroll
-        for (int dt = 0; dt < NT; ++dt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) O[dt][i] = O[dt][i] * f0 + at[(dt * 16 + i) * 64 + lane] * f1;
-      }
-      __syncthreads();
+      ml[0] = m[rb] * A.scale_log2;
+      ml[1] = l[rb];
     }
   }
 };
 
-// Packed prompts: one workgroup per (block of rows, KV head, split of the key axis).
+// Packed prompts: 256 rows per workgroup, 64-key tiles, two buffers.
 template <int D>
-__global__ __launch_bounds__(512, 2) void flash_prefill_kernel(AttnArgs A) {
-  typedef Flash<D, 8, 1, false> F;
+constexpr int prompt_waves() { return D == 256 ? 8 : 4; }
+template <int D>
+using PromptFlash = Flash<D, prompt_waves<D>(), kFlashRows / 32 / prompt_waves<D>(), prompt_waves<D>(), 64, 2, false>;
+
+// One workgroup per (block of rows, KV head, split of the key axis).
+template <int D>
+__global__ __launch_bounds__(64 * prompt_waves<D>(), prompt_waves<D>() / 4) void flash_prefill_kernel(AttnArgs A) {
+  typedef PromptFlash<D> F;
   extern __shared__ __align__(1024) char smem[];
   F f(A, smem);
   // later row blocks attend more keys: they start first
@@ -469,35 +513,43 @@ __global__ __launch_bounds__(512, 2) void flash_prefill_kernel(AttnArgs A) {
   f.q = uniform(packed_seq(A, s, threadIdx.x == 0));
   if (f.q.n == 0 || r0 >= static_cast<int64_t>(f.q.n) * A.G) return;
   f.begin_keys(r0, blockIdx.y);
-  const int32_t tiles = (f.n_keys + kKeys - 1) / kKeys;
+  const int32_t tiles = (f.n_keys + 63) / 64;
   const int32_t per = (tiles + A.n_split - 1) / A.n_split;
   const int32_t lo = min(static_cast<int32_t>(blockIdx.z) * per, tiles), hi = min(lo + per, tiles);
   if (lo < hi) f.request(lo, 0);
-  f.begin_rows(r0, 0);
+  f.begin_rows(0);
   if (lo < hi) f.keys(lo, hi);
-  if (A.n_split == 1) {
-    f.write_out();
-  } else if (f.row_ok) {
-    const size_t part = (static_cast<size_t>(f.q.row0 + f.t) * A.Hq + f.head) * A.n_split + blockIdx.z;
-    float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
-    f.write_part(A.part + part * D, ml + part * 2);
+#pragma unroll
+  for (int rb = 0; rb < F::WR / 32; ++rb) {
+    int t;
+    const int head = f.row_head(rb, &t);
+    if (head < 0) continue;
+    if (A.n_split == 1) {
+      f.write_out(rb, head);
+    } else {
+      const size_t part = (static_cast<size_t>(f.q.row0 + t) * A.Hq + head) * A.n_split + blockIdx.z;
+      float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
+      f.write_part(rb, A.part + part * D, ml + part * 2);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Trees of drafts: the key tiles of all units (KV head x block of rows of one
-// row of the batch) lie on one line, row by row, and workgroup w of W takes
-// tiles [w T / W, (w + 1) T / W) of it, whatever the rows' lengths.  A unit that
-// lies in one workgroup's share is written out; the shares of one that does
-// not go to the workspace (at most two per workgroup: its first, begun inside
-// a unit, and its last, ended inside one) and are joined by tree_join_kernel.
+// row of the batch) lie on one line, row by row, kUnitCost places for what a
+// unit costs apart from its tiles before each unit's, and workgroup w of W takes
+// places [w T / W, (w + 1) T / W) of the T, whatever the rows' lengths.  A unit
+// that lies in one workgroup's share is written out; the shares of one that
+// does not go to the workspace (at most two per workgroup: its first, begun
+// inside a unit, and its last, ended inside one) and are joined by
+// tree_join_kernel.
 // ---------------------------------------------------------------------------
 struct TreeSplit {
   int32_t rows_per_unit, units_per_row;  // BM; row blocks x KV heads
   int32_t workgroups;                    // W
 };
 // Workspace: sums [2 W][BM][D], (max, sum) [2 W][BM][2], then per unit
-// (first workgroup, number of workgroups; 0 or 1: nothing to join).
+// (first workgroup with a tile of it, number of workgroups; 0 or 1: nothing to join).
 __host__ __device__ inline size_t tree_ml_offset(const TreeSplit& t, int D) {
   return static_cast<size_t>(2) * t.workgroups * t.rows_per_unit * D;
 }
@@ -505,27 +557,34 @@ __host__ __device__ inline size_t tree_meta_offset(const TreeSplit& t, int D) {
   return tree_ml_offset(t, D) + static_cast<size_t>(4) * t.workgroups * t.rows_per_unit;
 }
 
+// 32-key tiles in four buffers; waves that have no rows only move tiles.  With
+// few rows a call is bound by memory, and what reaches its rate is many waves
+// with many loads in flight: 256 CUs x 8 waves, 64 - 96 KB per CU.
+constexpr int kTreeKeys = 32, kUnitCost = 4;
 template <int D, int RW>
-__global__ __launch_bounds__(128 * RW, 2) void flash_tree_kernel(AttnArgs A, TreeSplit ts) {
-  typedef Flash<D, RW, 2, true> F;
+using TreeFlash = Flash<D, RW, 1, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
+
+template <int D, int RW>
+__global__ __launch_bounds__((TreeFlash<D, RW>::THREADS), 2) void flash_tree_kernel(AttnArgs A, TreeSplit ts) {
+  typedef TreeFlash<D, RW> F;
   extern __shared__ __align__(1024) char smem[];
   F f(A, smem);
   const int lane = threadIdx.x & 63;
   int2* meta = reinterpret_cast<int2*>(A.part + tree_meta_offset(ts, D));
 
-  // ---- the line of tiles: tiles of a unit of row s, and of all its units ----
+  // ---- the line: tiles of a unit of row s, and its units ----
   auto row_tiles = [&](int s, int32_t* units) {
     const int32_t n = A.n_row ? A.n_row[s] : A.nodes, c = A.ctx_len[s];
     *units = 0;
     if (n < 1 || n > A.nodes || c < 0 || c > static_cast<int64_t>(A.max_pages) * A.page) return 0;
     *units = (n * A.G + F::BM - 1) / F::BM * A.Hk;
-    return (c + n + kKeys - 1) / kKeys;
+    return (c + n + kTreeKeys - 1) / kTreeKeys;
   };
-  // inclusive sum over the lanes of the tiles of rows base + lane
+  // inclusive sum over the lanes of the places of rows base + lane
   auto scan = [&](int base, int64_t* mine) {
     int32_t units = 0;
     const int32_t tiles = base + lane < A.n_seqs ? row_tiles(base + lane, &units) : 0;
-    int64_t inc = *mine = static_cast<int64_t>(tiles) * units;
+    int64_t inc = *mine = static_cast<int64_t>(tiles + kUnitCost) * units;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int64_t up = __shfl_up(inc, d, 64);
@@ -539,7 +598,7 @@ __global__ __launch_bounds__(128 * RW, 2) void flash_tree_kernel(AttnArgs A, Tre
     total += __shfl(inc, 63, 64);
   }
   total = uniform(total);
-  // units without tiles (refused rows, row blocks past a row's nodes) have nothing to join
+  // units without places (refused rows, row blocks past a row's nodes) have nothing to join
   for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
     int32_t units;
     row_tiles(s, &units);
@@ -550,14 +609,14 @@ __global__ __launch_bounds__(128 * RW, 2) void flash_tree_kernel(AttnArgs A, Tre
       tree_seq(A, s, threadIdx.x == 0, &p);
     }
   }
-  const int64_t W = ts.workgroups < total ? ts.workgroups : total;  // every workgroup has a tile
+  const int64_t W = ts.workgroups < total ? ts.workgroups : total;  // every workgroup has a place
   const int64_t w = blockIdx.x;
   if (w >= W) return;
   const int64_t first = uniform(w * total / W), last = uniform((w + 1) * total / W);
 
-  // ---- the row that holds tile `first`: the last one that does not begin after it ----
+  // ---- the row that holds place `first`: the last one that does not begin after it ----
   int s = 0;
-  int64_t row_at = 0;  // its first tile
+  int64_t row_at = 0;  // its first place
   for (int base = 0;; base += 64) {
     if (A.n_seqs > 64) inc = scan(base, &mine);  // else it is at hand
     const int64_t chunk = __shfl(inc, 63, 64);
@@ -577,17 +636,20 @@ __global__ __launch_bounds__(128 * RW, 2) void flash_tree_kernel(AttnArgs A, Tre
   Seq q{0, 0, 0, 0};
   for (int64_t at = first; at < last;) {
     int32_t units;
-    const int32_t tiles = uniform(row_tiles(s, &units));
+    const int32_t tiles = uniform(row_tiles(s, &units)), places = tiles + kUnitCost;
     units = uniform(units);
-    if (at >= row_at + static_cast<int64_t>(tiles) * units) {
-      row_at += static_cast<int64_t>(tiles) * units;
+    if (at >= row_at + static_cast<int64_t>(places) * units) {
+      row_at += static_cast<int64_t>(places) * units;
       ++s;
       continue;
     }
-    const int32_t unit = static_cast<int32_t>((at - row_at) / tiles);
-    const int64_t unit_at = row_at + static_cast<int64_t>(unit) * tiles;
-    const int32_t lo = static_cast<int32_t>(at - unit_at);
-    const int32_t hi = static_cast<int32_t>(last - unit_at < tiles ? last - unit_at : tiles);
+    const int32_t unit = static_cast<int32_t>((at - row_at) / places);
+    const int64_t unit_at = row_at + static_cast<int64_t>(unit) * places;
+    // this share's tiles: none if it holds only places before the first
+    const int32_t lo = max(static_cast<int32_t>(at - unit_at) - kUnitCost, 0);
+    const int32_t hi = static_cast<int32_t>(last - unit_at < places ? last - unit_at : places) - kUnitCost;
+    at = unit_at + hi + kUnitCost;
+    if (lo >= hi) continue;
     const int64_t r0 = static_cast<int64_t>(unit / A.Hk) * F::BM;
     // the first tile is requested before the row's paths and Q are waited for
     f.q = Seq{static_cast<int64_t>(s) * A.nodes, uniform(A.n_row ? A.n_row[s] : A.nodes), uniform(A.ctx_len[s]), s};
@@ -600,27 +662,27 @@ __global__ __launch_bounds__(128 * RW, 2) void flash_tree_kernel(AttnArgs A, Tre
     int2* unit_meta = meta + static_cast<size_t>(s) * ts.units_per_row + unit;
     if (q.n == 0) {  // parents refused
       if (lo == 0 && threadIdx.x == 0) *unit_meta = make_int2(0, 0);
-      tile_ready();  // the request has landed before the buffer is used again
+      wait_loads<0>();
     } else {
-      f.begin_rows(r0, paths);
+      f.begin_rows(paths);
       f.keys(lo, hi);
-      f.join();
-      if (lo == 0 && hi == tiles) {
-        if (threadIdx.x == 0) *unit_meta = make_int2(0, 1);
-        f.write_out();
-      } else {
-        if (lo == 0 && threadIdx.x == 0) {
-          // the last workgroup of the unit: the largest w' with w' total / W <= its last tile
-          const int64_t end = unit_at + tiles - 1;
-          *unit_meta = make_int2(static_cast<int>(w), static_cast<int>(((end + 1) * W - 1) / total - w) + 1);
-        }
-        if (f.row_ok && f.kw == 0) {
-          const size_t row = (static_cast<size_t>(2) * w + (lo == 0 ? 1 : 0)) * F::BM + f.rw * 32 + f.col;
-          f.write_part(A.part + row * D, A.part + tree_ml_offset(ts, D) + row * 2);
+      if (lo == 0 && threadIdx.x == 0) {
+        // the last workgroup of the unit: the largest w' with w' T / W <= its last place
+        const int64_t end = unit_at + places - 1;
+        *unit_meta = make_int2(static_cast<int>(w), static_cast<int>(((end + 1) * W - 1) / total - w) + 1);
+      }
+      int t;
+      const int head = f.row_head(0, &t);
+      if (head >= 0) {
+        if (lo == 0 && hi == tiles) {
+          f.write_out(0, head);
+        } else {
+          const size_t row = (static_cast<size_t>(2) * w + (lo == 0 ? 1 : 0)) * F::BM + f.wave * 32 + f.col;
+          f.write_part(0, A.part + row * D, A.part + tree_ml_offset(ts, D) + row * 2);
         }
       }
     }
-    at = unit_at + hi;
+    __syncthreads();  // every wave is done with the buffers
   }
 }
 
@@ -675,15 +737,13 @@ namespace {
 
 // Row blocks of 32, 64 or 128 rows, the smallest that holds the row's
 // (node, head) pairs of one KV head, 128 at most; as many workgroups as fit the
-// card at once: LDS holds 1, 2 or 4 of them per CU (D 256, 128, 64), and with
-// 128 rows their eight waves of up to 256 registers fill a CU.
+// card at once: LDS holds 1, 2 or 4 of them per CU (D 256, 128, 64).
 TreeSplit tree_split(int Hk, int G, int D, int nodes) {
   TreeSplit t;
   const int rows = nodes * G;
   t.rows_per_unit = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   t.units_per_row = (rows + t.rows_per_unit - 1) / t.rows_per_unit * Hk;
-  const int by_lds = D == 256 ? 1 : (D == 128 ? 2 : 4), by_regs = 128 / t.rows_per_unit;
-  t.workgroups = 256 * (by_lds < by_regs ? by_lds : by_regs);
+  t.workgroups = 256 * (D == 256 ? 1 : (D == 128 ? 2 : (t.rows_per_unit == 128 ? 2 : 4)));
   return t;
 }
 
@@ -696,7 +756,7 @@ size_t flash_tree_part_bytes(int64_t batch, int Hk, int G, int D, int nodes) {
 
 template <int D, int RW>
 static void launch_tree_rows(const AttnArgs& a, const TreeSplit& t, hipStream_t s) {
-  typedef Flash<D, RW, 2, true> F;
+  typedef TreeFlash<D, RW> F;
   hipLaunchKernelGGL((flash_tree_kernel<D, RW>), dim3(t.workgroups), dim3(F::THREADS), F::LDS, s, a, t);
 }
 
@@ -726,7 +786,7 @@ int launch_flash_tree(const AttnArgs& a, void* stream) {
 
 template <int D>
 static int launch_flash_prefill_t(const AttnArgs& a, int64_t tiles, hipStream_t s) {
-  typedef Flash<D, 8, 1, false> F;
+  typedef PromptFlash<D> F;
   hipLaunchKernelGGL((flash_prefill_kernel<D>), dim3(static_cast<unsigned>(tiles), a.Hk, a.n_split), dim3(F::THREADS),
                      F::LDS, s, a);
   return static_cast<int>(hipGetLastError());
