@@ -324,7 +324,7 @@ size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nod
 template <int D, bool BF16>
 static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
   const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, BF16 ? kFlashRows : kGenRows);
-  if (tiles > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
+  if (tiles * a.Hk > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
   if constexpr (BF16) {
     if (a.nodes > 0) return launch_flash_tree(a, s);
     const int e = launch_flash_prefill(a, tiles, s);

@@ -496,7 +496,7 @@ struct Flash {
 
 // Packed prompts: 256 rows per workgroup, 64-key tiles, two buffers.
 template <int D>
-constexpr int prompt_waves() { return D == 256 ? 8 : 4; }
+constexpr int prompt_waves() { return 8; }
 template <int D>
 using PromptFlash = Flash<D, prompt_waves<D>(), kFlashRows / 32 / prompt_waves<D>(), prompt_waves<D>(), 64, 2, false>;
 
@@ -506,16 +506,16 @@ __global__ __launch_bounds__(64 * prompt_waves<D>(), prompt_waves<D>() / 4) void
   typedef PromptFlash<D> F;
   extern __shared__ __align__(1024) char smem[];
   F f(A, smem);
-  // later row blocks attend more keys: they start first
-  const int64_t id = gridDim.x - 1 - blockIdx.x;
+  // later row blocks attend more keys: they start first, those of all heads
+  const int64_t id = gridDim.x / A.Hk - 1 - blockIdx.x / A.Hk;
   const int s = uniform(find_seq(A, id, F::BM));
   const int64_t r0 = uniform((id - tile_start(A, s, F::BM)) * F::BM);
   f.q = uniform(packed_seq(A, s, threadIdx.x == 0));
   if (f.q.n == 0 || r0 >= static_cast<int64_t>(f.q.n) * A.G) return;
-  f.begin_keys(r0, blockIdx.y);
+  f.begin_keys(r0, blockIdx.x % A.Hk);
   const int32_t tiles = (f.n_keys + 63) / 64;
   const int32_t per = (tiles + A.n_split - 1) / A.n_split;
-  const int32_t lo = min(static_cast<int32_t>(blockIdx.z) * per, tiles), hi = min(lo + per, tiles);
+  const int32_t lo = min(static_cast<int32_t>(blockIdx.y) * per, tiles), hi = min(lo + per, tiles);
   if (lo < hi) f.request(lo, 0);
   f.begin_rows(0);
   if (lo < hi) f.keys(lo, hi);
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(64 * prompt_waves<D>(), prompt_waves<D>() / 4) void
     if (A.n_split == 1) {
       f.write_out(rb, head);
     } else {
-      const size_t part = (static_cast<size_t>(f.q.row0 + t) * A.Hq + head) * A.n_split + blockIdx.z;
+      const size_t part = (static_cast<size_t>(f.q.row0 + t) * A.Hq + head) * A.n_split + blockIdx.y;
       float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
       f.write_part(rb, A.part + part * D, ml + part * 2);
     }
@@ -787,8 +787,8 @@ int launch_flash_tree(const AttnArgs& a, void* stream) {
 template <int D>
 static int launch_flash_prefill_t(const AttnArgs& a, int64_t tiles, hipStream_t s) {
   typedef PromptFlash<D> F;
-  hipLaunchKernelGGL((flash_prefill_kernel<D>), dim3(static_cast<unsigned>(tiles), a.Hk, a.n_split), dim3(F::THREADS),
-                     F::LDS, s, a);
+  hipLaunchKernelGGL((flash_prefill_kernel<D>), dim3(static_cast<unsigned>(tiles * a.Hk), a.n_split), dim3(F::THREADS), F::LDS,
+                     s, a);
   return static_cast<int>(hipGetLastError());
 }
 
