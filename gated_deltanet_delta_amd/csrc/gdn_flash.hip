@@ -2,7 +2,7 @@
 // gdn_attn.hip): 32x32x16 matrix instructions on key tiles that the waves of a
 // workgroup share through LDS.
 //
-// A wave owns RB blocks of 32 rows.  S^T = K Q^T takes K as the A operand from
+// A wave owns 32 rows.  S^T = K Q^T takes K as the A operand from
 // LDS and Q^T from registers; lane l then holds row l % 32 and keys 8 (i / 4) +
 // 4 (l / 32) + i % 4 of a block of 32.  O^T = V^T P^T contracts 16 keys per
 // instruction: lane l's eight weights of one instruction are its accumulators
@@ -80,10 +80,10 @@ __device__ __forceinline__ float half_sum(float x) {
 }  // namespace
 
 // NW waves move KT-key tiles through NST buffers; the first RW of them compute,
-// 32 RB rows each.
-template <int D, int RW, int RB, int NW, int KT, int NST, bool TREE>
+// 32 rows each.
+template <int D, int RW, int NW, int KT, int NST, bool TREE>
 struct Flash {
-  static constexpr int THREADS = 64 * NW, WR = 32 * RB, BM = WR * RW;
+  static constexpr int THREADS = 64 * NW, BM = 32 * RW;
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int TILE = KT * ROW_BYTES;            // K or V of a tile
   static constexpr int BUF = 2 * TILE;
@@ -114,15 +114,15 @@ struct Flash {
   int kvh;
   int32_t n_keys, clear;
   int64_t r0;            // its first row
-  int t[RB];             // this lane's tokens
-  uint64_t path[RB];     // TREE: the rows' nodes
+  int t;                 // this lane's token
+  uint64_t path;         // TREE: its row's nodes
   // base rows ((page * H_kv + kvh) P + offset) of the cached 16-token groups,
   // one per lane: lane i holds that of key 1024 ids_at + 16 i
   int32_t ids_at;
   int64_t ids;
-  bf16x8_t qf[RB][NS];
-  f32x16_t O[RB][NT];
-  float m[RB], l[RB];    // running maximum (of unscaled logits), this lane's part of the sum
+  bf16x8_t qf[NS];
+  f32x16_t O[NT];
+  float m, l;            // running maximum (of unscaled logits), this lane's part of the sum
 
   __device__ Flash(const AttnArgs& a, char* smem) : A(a), lds(smem) {
     lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
@@ -142,35 +142,32 @@ struct Flash {
     clear = TREE ? q.ctx : q.ctx + static_cast<int32_t>(r0 / A.G) + 1;
     ids_at = -1;
   }
-  // This lane's rows and their Q; node_paths (TREE): lane j holds node j's path.
-  // Query head of this lane's row of block rb, and its token; -1: no row (the
-  // token is then the unit's first).
-  __device__ int row_head(int rb, int* token) const {
+  // Query head of this lane's row, and its token; -1: no row (the token is then
+  // the unit's first).
+  __device__ int row_head(int* token) const {
     const int32_t t0 = static_cast<int32_t>(r0 / A.G), h0 = static_cast<int32_t>(r0 - static_cast<int64_t>(t0) * A.G);
-    const int32_t r = wave * WR + rb * 32 + col;
+    const int32_t r = wave * 32 + col;
     const bool ok = wave < RW && r < static_cast<int64_t>(q.n) * A.G - r0;
     const int32_t rc = ok ? r : 0;
     *token = t0 + (h0 + rc) / A.G;
     return ok ? kvh * A.G + (h0 + rc) % A.G : -1;
   }
+  // This lane's row and its Q; node_paths (TREE): lane j holds node j's path.
   __device__ void begin_rows(uint64_t node_paths) {
+    int hd = row_head(&t);
+    if (hd < 0) hd = kvh * A.G;  // reads some row of the call's
+    if constexpr (TREE)
+      path = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(node_paths >> 32), t, 64)) << 32) |
+             static_cast<uint32_t>(__shfl(static_cast<uint32_t>(node_paths), t, 64));
+    const uint16_t* qp = static_cast<const uint16_t*>(A.q) + (q.row0 + t) * A.q_stride + static_cast<int64_t>(hd) * D;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      int hd = row_head(rb, &t[rb]);
-      if (hd < 0) hd = kvh * A.G;  // reads some row of the call's
-      if constexpr (TREE)
-        path[rb] = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(node_paths >> 32), t[rb], 64)) << 32) |
-                   static_cast<uint32_t>(__shfl(static_cast<uint32_t>(node_paths), t[rb], 64));
-      const uint16_t* qp = static_cast<const uint16_t*>(A.q) + (q.row0 + t[rb]) * A.q_stride + static_cast<int64_t>(hd) * D;
+    for (int s = 0; s < NS; ++s) qf[s] = *reinterpret_cast<const bf16x8_t*>(qp + s * 16 + half * 8);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) qf[rb][s] = *reinterpret_cast<const bf16x8_t*>(qp + s * 16 + half * 8);
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) O[rb][i][e] = 0.f;
-      m[rb] = -INFINITY;
-      l[rb] = 0.f;
-    }
+      for (int e = 0; e < 16; ++e) O[i][e] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
   }
 
   // Page ids of round `at` (keys 1024 at ..), one 16-token group per lane, into
@@ -256,11 +253,11 @@ struct Flash {
     }
   }
 
-  // Does this lane's row of block rb attend key j?
-  __device__ bool attends(int rb, int32_t j) const {
+  // Does this lane's row attend key j?
+  __device__ bool attends(int32_t j) const {
     const int32_t own = j - q.ctx;
-    if constexpr (TREE) return own < 0 || (own < q.n && ((path[rb] >> own) & 1ull));
-    else return own <= t[rb];
+    if constexpr (TREE) return own < 0 || (own < q.n && ((path >> own) & 1ull));
+    else return own <= t;
   }
 
   // Values that are not finite must not reach rows that do not attend their
@@ -307,121 +304,116 @@ struct Flash {
       va[dt] = vrow + 16 * ((dt * 4 + 2 * g2 + (quarter >> 1)) ^ v_perm(mrow));
   }
 
-  // The 32 keys of block kb of a tile: their logits and their terms.
-  // MASKED: some row does not attend every key of the tile.
-  template <bool MASKED>
-  __device__ void block(int32_t key0, int kb, int b, const uint32_t (&ka)[KA], uint64_t bad) {
+  // Logits of the tile in buffer b.
+  __device__ void logits(int b, f32x16_t (&S)[KB]) const {
     typedef __attribute__((address_space(3))) const bf16x8_t* lds_k;
-    typedef __attribute__((address_space(3))) s16x4_t* lds_v;
-    // ---- logits ----
-    f32x16_t S[RB];
+    uint32_t ka[KA];
+    k_addresses(b, ka);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
+    for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[rb][e] = 0.f;
+      for (int e = 0; e < 16; ++e) S[kb][e] = 0.f;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const bf16x8_t a = *(lds_k)(ka[s % KA] + (s / KA) * 256 + kb * 32 * ROW_BYTES);
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb) S[rb] = mfma32x32(a, qf[rb][s], S[rb]);
+      for (int s = 0; s < NS; ++s) {
+        const bf16x8_t a = *(lds_k)(ka[s % KA] + (s / KA) * 256 + kb * 32 * ROW_BYTES);
+        S[kb] = mfma32x32(a, qf[s], S[kb]);
+      }
     }
     // K operands four steps ahead, no more: registers are short
     __builtin_amdgcn_sched_group_barrier(kSchedLds, 4, 0);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, RB, 0);
-      if (s < NS - 4) __builtin_amdgcn_sched_group_barrier(kSchedLds, 1, 0);
+    for (int s = 0; s < KB * NS; ++s) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      if (s < KB * NS - 4) __builtin_amdgcn_sched_group_barrier(kSchedLds, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    // ---- running maximum ----
-    float mx[RB];
-    bool grown = false;
+  }
+  // Weights of a tile from its logits: rounded to bf16 for the product, each is
+  // off by at most 2^-8 of itself, below the output's own rounding on average
+  // over keys.  The sum takes the rounded weights too, two to an instruction.
+  // MASKED: some row does not attend every key of the tile; S then keeps the
+  // unrounded weights.
+  template <bool MASKED>
+  __device__ void weights(int32_t key0, f32x16_t (&S)[KB], bf16x8_t (&P)[KB][2]) {
+    float mx = -INFINITY;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      mx[rb] = -INFINITY;
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        if constexpr (MASKED) S[rb][e] = attends(rb, key0 + kb * 32 + 8 * (e / 4) + 4 * half + e % 4) ? S[rb][e] : -INFINITY;
-        mx[rb] = fmaxf(mx[rb], S[rb][e]);
+        if constexpr (MASKED) S[kb][e] = attends(key0 + kb * 32 + 8 * (e / 4) + 4 * half + e % 4) ? S[kb][e] : -INFINITY;
+        mx = fmaxf(mx, S[kb][e]);
       }
-      mx[rb] = half_max(mx[rb]);
-      grown |= (mx[rb] - m[rb]) * A.scale_log2 > 8.f;
-    }
+    mx = half_max(mx);
     // The weights are taken against a maximum that may lag: O and l are scaled
     // only when some row's maximum has grown by more than 2^8 in weight, which
     // leaves sums and weights far inside their range.
-    if (__any(grown)) {
+    if (__any((mx - m) * A.scale_log2 > 8.f)) {
+      const float m_new = fmaxf(m, mx);
+      const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * A.scale_log2);
+      m = m_new;
+      l *= f;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        const float m_new = fmaxf(m[rb], mx[rb]);
-        const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[rb] - m_new) * A.scale_log2);
-        m[rb] = m_new;
-        l[rb] *= f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) O[rb][i] *= f;
-      }
+      for (int i = 0; i < NT; ++i) O[i] *= f;
     }
-    // ---- weights; rounded to bf16 for the product: each is off by at most
-    // 2^-8 of itself, below the output's own rounding on average over keys.  The
-    // sum takes the rounded weights too, two to an instruction ----
-    bf16x8_t P[RB][2];
+    const float off = m == -INFINITY ? 0.f : -m * A.scale_log2;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const float off = m[rb] == -INFINITY ? 0.f : -m[rb] * A.scale_log2;
+    for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        S[rb][e] = __builtin_amdgcn_exp2f(fmaf(S[rb][e], A.scale_log2, off));
-        P[rb][e / 8][e % 8] = static_cast<__bf16>(S[rb][e]);
+        S[kb][e] = __builtin_amdgcn_exp2f(fmaf(S[kb][e], A.scale_log2, off));
+        P[kb][e / 8][e % 8] = static_cast<__bf16>(S[kb][e]);
       }
 #pragma unroll
       for (int e = 0; e < 16; e += 2)
-        l[rb] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{P[rb][e / 8][e % 8], P[rb][e / 8][e % 8 + 1]}, bf16x2_t{1.0f, 1.0f},
-                                                l[rb], false);
+        l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{P[kb][e / 8][e % 8], P[kb][e / 8][e % 8 + 1]}, bf16x2_t{1.0f, 1.0f}, l, false);
     }
-    // ---- O^T += V^T P^T ----
     __builtin_amdgcn_sched_barrier(0);
+  }
+  // O^T += V^T P^T for the tile in buffer b.
+  __device__ void terms(int b, const bf16x8_t (&P)[KB][2]) {
+    typedef __attribute__((address_space(3))) s16x4_t* lds_v;
     uint32_t va[VA];
     v_addresses(b, va);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-      for (int dt = 0; dt < NT; ++dt) {
-        const uint32_t at = va[dt % VA] + (dt / VA) * 256 + (kb * 32 + 16 * ks) * ROW_BYTES;
-        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at));
-        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at + 8 * ROW_BYTES));
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) O[rb][dt] = mfma32x32(a, P[rb][ks], O[rb][dt]);
-      }
+        for (int dt = 0; dt < NT; ++dt) {
+          const uint32_t at = va[dt % VA] + (dt / VA) * 256 + (kb * 32 + 16 * ks) * ROW_BYTES;
+          const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at));
+          const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v)(at + 8 * ROW_BYTES));
+          O[dt] = mfma32x32(__builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7)), P[kb][ks], O[dt]);
+        }
     __builtin_amdgcn_sched_group_barrier(kSchedLds, 6, 1);
 #pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, RB, 1);
-      if (i < 2 * NT - 3) __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
+    for (int i = 0; i < KB * 2 * NT; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 1);
+      if (i < KB * 2 * NT - 3) __builtin_amdgcn_sched_group_barrier(kSchedLds, 2, 1);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (MASKED) {
-      // the terms of the V rows that clear_bad() took out, for the rows that
-      // attend them (their weights are in S, unrounded)
-      for (uint32_t left = static_cast<uint32_t>(bad >> (kb * 32)); left != 0; left &= left - 1) {
-        const int kr = __builtin_ctz(left);
-        const int32_t j = key0 + kb * 32 + kr;
+  }
+  // The terms of the V rows that clear_bad() took out of a tile, for the rows
+  // that attend them; S holds the weights.
+  __device__ void bad_terms(int32_t key0, uint64_t bad, const f32x16_t (&S)[KB]) {
+    for (; bad != 0; bad &= bad - 1) {
+      const int kr = __builtin_ctzll(bad);
+      const int32_t j = key0 + kr;
+      float p = 0.f;  // the weight, in the lanes of half (kr / 4) % 2
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          float p = 0.f;  // the weight, in the lanes of half (kr / 4) % 2
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) p = (8 * (e / 4) + e % 4) == (kr & ~4) ? S[rb][e] : p;
-          p = __shfl(p, col + 32 * ((kr >> 2) & 1), 64);
-          if (!attends(rb, j)) continue;
-          const uint16_t* vr =
-              reinterpret_cast<const uint16_t*>(key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j)) + 4 * half;
+        for (int e = 0; e < 16; ++e) p = (kb * 32 + 8 * (e / 4) + e % 4) == (kr & ~4) ? S[kb][e] : p;
+      p = __shfl(p, col + 32 * ((kr >> 2) & 1), 64);
+      if (!attends(j)) continue;
+      const uint16_t* vr = reinterpret_cast<const uint16_t*>(key_row<2>(A, q, A.v_cache, A.v, A.v_stride, kvh, j)) + 4 * half;
 #pragma unroll
-          for (int dt = 0; dt < NT; ++dt) {
+      for (int dt = 0; dt < NT; ++dt) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) O[rb][dt][i] += p * bf16_bits_to_f32(vr[dt * 32 + 8 * (i / 4) + i % 4]);
-            asm volatile("" ::: "memory");  // no more than one step's loads at a time in registers
-          }
-        }
+        for (int i = 0; i < 16; ++i) O[dt][i] += p * bf16_bits_to_f32(vr[dt * 32 + 8 * (i / 4) + i % 4]);
+        asm volatile("" ::: "memory");  // no more than one step's loads at a time in registers
       }
     }
   }
@@ -432,105 +424,171 @@ struct Flash {
     uint64_t bad = 0;
     if constexpr (MASKED) bad = clear_bad(lds + b * BUF + TILE);
     if (wave < RW) {
-      uint32_t ka[KA];
-      k_addresses(b, ka);
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) block<MASKED>(kt * KT, kb, b, ka, bad);
+      f32x16_t S[KB];
+      bf16x8_t P[KB][2];
+      logits(b, S);
+      weights<MASKED>(kt * KT, S, P);
+      terms(b, P);
+      if constexpr (MASKED) bad_terms(kt * KT, bad, S);
     }
   }
 
-  // Tile kt of [lo, hi) has landed, for every wave; asks for the tile NST - 1 ahead.
-  __device__ void step(int32_t kt, int32_t lo, int32_t hi) {
-    const int32_t newer = hi - 1 - kt;  // tiles asked for after kt: this many, NST - 2 at most
-    if (newer >= NST - 2) tile_ready<(NST - 2) * LPT>();
-    else if (NST > 3 && newer == 1) tile_ready<(NST > 3 ? LPT : 0)>();
-    else tile_ready<0>();
-    if (kt + NST - 1 < hi) request(kt + NST - 1, (kt + NST - 1 - lo) & (NST - 1));
+  // Waits until at most `tiles` (0 .. NST - 2) of the newest requests are in flight.
+  __device__ static void wait_tiles(int tiles) {
+    if (tiles >= NST - 2) wait_loads<(NST - 2) * LPT>();
+    else if (NST > 3 && tiles == 1) wait_loads<(NST > 3 ? LPT : 0)>();
+    else wait_loads<0>();
+  }
+  __device__ static void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  // Tiles kt .. end - 1 of [lo, hi), up to tile kt + NST - 2 requested already.
+  template <bool MASKED>
+  __device__ void in_turn(int32_t kt, int32_t end, int32_t lo, int32_t hi) {
+    for (; kt < end; ++kt) {
+      wait_tiles(hi - 1 - kt);
+      barrier();
+      if (kt + NST - 1 < hi) request(kt + NST - 1, (kt + NST - 1 - lo) & (NST - 1));
+      tile<MASKED>(kt, (kt - lo) & (NST - 1));
+    }
   }
   // Tiles [lo, hi) of the unit, the first already requested into buffer 0;
   // leaves the sums in O, m, l.
   __device__ void keys(int32_t lo, int32_t hi) {
     wait_loads<0>();  // Q is at hand, so no later wait is for it
-#pragma unroll 1
-    for (int i = 1; i < NST - 1 && lo + i < hi; ++i) request(lo + i, i);
     // tiles that every row attends whole, then the others
     const int32_t mid = max(lo, min(hi, clear / KT));
-    int32_t kt = lo;
-    for (; kt < mid; ++kt) {
-      step(kt, lo, hi);
-      tile<false>(kt, (kt - lo) & (NST - 1));
-    }
-    for (; kt < hi; ++kt) {
-      step(kt, lo, hi);
-      tile<true>(kt, (kt - lo) & (NST - 1));
-    }
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) l[rb] = half_sum(l[rb]);
+#pragma unroll 1
+    for (int i = 1; i < NST - 1 && lo + i < hi; ++i) request(lo + i, i);
+    in_turn<false>(lo, mid, lo, hi);
+    in_turn<true>(mid, hi, lo, hi);
+    l = half_sum(l);
   }
 
   // Element (dt, i) of O is d = 32 dt + 8 (i / 4) + 4 half + i % 4.
-  __device__ void write_out(int rb, int head) const {
-    const float inv = 1.0f / l[rb];
-    uint16_t* o = static_cast<uint16_t*>(A.o) + (static_cast<size_t>(q.row0 + t[rb]) * A.Hq + head) * D + 4 * half;
+  __device__ void write_out(int head) const {
+    const float inv = 1.0f / l;
+    uint16_t* o = static_cast<uint16_t*>(A.o) + (static_cast<size_t>(q.row0 + t) * A.Hq + head) * D + 4 * half;
 #pragma unroll
     for (int dt = 0; dt < NT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<uint2*>(o + 32 * dt + 2 * i) = make_uint2(pack2_bf16(O[rb][dt][i] * inv, O[rb][dt][i + 1] * inv),
-                                                                    pack2_bf16(O[rb][dt][i + 2] * inv, O[rb][dt][i + 3] * inv));
+        *reinterpret_cast<uint2*>(o + 32 * dt + 2 * i) = make_uint2(pack2_bf16(O[dt][i] * inv, O[dt][i + 1] * inv),
+                                                                    pack2_bf16(O[dt][i + 2] * inv, O[dt][i + 3] * inv));
   }
-  // Unscaled sums and (scaled maximum, sum) of this lane's row of block rb.
-  __device__ void write_part(int rb, float* sums, float* ml) const {
+  // Unscaled sums and (scaled maximum, sum) of this lane's row.
+  __device__ void write_part(float* sums, float* ml) const {
 #pragma unroll
     for (int dt = 0; dt < NT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<f32x4_t*>(sums + 32 * dt + 2 * i + 4 * half) =
-            f32x4_t{O[rb][dt][i], O[rb][dt][i + 1], O[rb][dt][i + 2], O[rb][dt][i + 3]};
+            f32x4_t{O[dt][i], O[dt][i + 1], O[dt][i + 2], O[dt][i + 3]};
     if (half == 0) {
-      ml[0] = m[rb] * A.scale_log2;
-      ml[1] = l[rb];
+      ml[0] = m * A.scale_log2;
+      ml[1] = l;
     }
   }
 };
 
-// Packed prompts: 256 rows per workgroup, 64-key tiles, two buffers.
+// Packed prompts: 256 rows per workgroup, 128 KB (D 64: 64 KB) of tiles.
 template <int D>
-constexpr int prompt_waves() { return 8; }
+constexpr int prompt_keys() { return D == 256 ? 32 : 64; }
 template <int D>
-using PromptFlash = Flash<D, prompt_waves<D>(), kFlashRows / 32 / prompt_waves<D>(), prompt_waves<D>(), 64, 2, false>;
+using PromptFlash = Flash<D, kFlashRows / 32, kFlashRows / 32, prompt_keys<D>(), 4, false>;
+
+// Sum over the wave's lanes, in every lane.
+__device__ __forceinline__ int32_t wave_sum(int32_t v) {
+  v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+  v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);   // lane ^ 2
+  v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);  // 7 - i within 8 lanes
+  v += __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);  // 15 - i within 16 lanes
+  return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+         __builtin_amdgcn_readlane(v, 48);
+}
+
+// Row block number `rank` of a batch of at most 64 sequences, in falling order
+// of the keys that blocks attend (equal ones in order of their sequences), so
+// the longest start first, whatever the order of the sequences.  Block b of a
+// sequence attends ctx + min(n, floor(((b + 1) BM - 1) / G) + 1) keys, more with
+// every b; so the number of blocks of at least `keys` keys is a sum over the
+// sequences, one per lane, and a search over `keys` finds the block.  False:
+// there are no more blocks.  Refused sequences are taken as they come, from rank 0.
+template <int BM>
+__device__ bool ranked_block(const AttnArgs& A, int64_t rank, int* seq, int64_t* r0) {
+  const int lane = threadIdx.x & 63;
+  Seq q{0, 0, 0, 0};
+  if (lane < A.n_seqs) q = packed_seq(A, lane, rank == 0);
+  const int32_t blocks = static_cast<int32_t>((static_cast<int64_t>(q.n) * A.G + BM - 1) / BM);
+  const int32_t r = static_cast<int32_t>(rank);
+  if (r >= wave_sum(blocks)) return false;
+  // the sequence's first block of at least `keys` keys (blocks: none)
+  auto first = [&](int32_t keys) {
+    const int32_t need = keys - q.ctx;
+    if (need <= 1) return 0;
+    return need > q.n ? blocks : static_cast<int32_t>((static_cast<int64_t>(need - 1) * A.G) / BM);
+  };
+  // the largest number of keys that more than r blocks have at least
+  int32_t lo = 1, hi = 0x7fffffff;  // more than r blocks have lo; hi: not so many
+  {
+    int32_t most = q.n > 0 ? q.ctx + q.n : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d, 64));
+    hi = uniform(most) + 1;
+  }
+  while (hi - lo > 1) {
+    const int32_t mid = lo + (hi - lo) / 2;
+    if (wave_sum(blocks - first(mid)) > r) lo = mid;
+    else hi = mid;
+  }
+  // among the blocks of exactly lo keys, at most one per sequence
+  const int32_t b = first(lo);
+  const uint64_t on = __ballot(b < blocks && b != first(lo + 1));
+  int32_t skip = r - wave_sum(blocks - first(lo + 1));
+  uint64_t left = on;
+  for (; skip > 0 && left != 0; --skip) left &= left - 1;
+  if (left == 0) return false;  // only where cu_seqlens is no partition and the counts wrapped
+  const int s = __builtin_ctzll(left);
+  *seq = uniform(s);
+  *r0 = static_cast<int64_t>(__builtin_amdgcn_readlane(b, s)) * BM;
+  return true;
+}
 
 // One workgroup per (block of rows, KV head, split of the key axis).
 template <int D>
-__global__ __launch_bounds__(64 * prompt_waves<D>(), prompt_waves<D>() / 4) void flash_prefill_kernel(AttnArgs A) {
+__global__ __launch_bounds__(PromptFlash<D>::THREADS, 2) void flash_prefill_kernel(AttnArgs A) {
   typedef PromptFlash<D> F;
   extern __shared__ __align__(1024) char smem[];
   F f(A, smem);
-  // later row blocks attend more keys: they start first, those of all heads
-  const int64_t id = gridDim.x / A.Hk - 1 - blockIdx.x / A.Hk;
-  const int s = uniform(find_seq(A, id, F::BM));
-  const int64_t r0 = uniform((id - tile_start(A, s, F::BM)) * F::BM);
+  int s;
+  int64_t r0;
+  if (A.n_seqs <= 64) {
+    if (!ranked_block<F::BM>(A, blockIdx.x / A.Hk, &s, &r0)) return;
+  } else {  // there are many blocks to even out what their order does not
+    const int64_t id = gridDim.x / A.Hk - 1 - blockIdx.x / A.Hk;
+    s = uniform(find_seq(A, id, F::BM));
+    r0 = uniform((id - tile_start(A, s, F::BM)) * F::BM);
+  }
   f.q = uniform(packed_seq(A, s, threadIdx.x == 0));
   if (f.q.n == 0 || r0 >= static_cast<int64_t>(f.q.n) * A.G) return;
   f.begin_keys(r0, blockIdx.x % A.Hk);
-  const int32_t tiles = (f.n_keys + 63) / 64;
+  const int32_t tiles = (f.n_keys + prompt_keys<D>() - 1) / prompt_keys<D>();
   const int32_t per = (tiles + A.n_split - 1) / A.n_split;
   const int32_t lo = min(static_cast<int32_t>(blockIdx.y) * per, tiles), hi = min(lo + per, tiles);
   if (lo < hi) f.request(lo, 0);
   f.begin_rows(0);
   if (lo < hi) f.keys(lo, hi);
-#pragma unroll
-  for (int rb = 0; rb < F::WR / 32; ++rb) {
-    int t;
-    const int head = f.row_head(rb, &t);
-    if (head < 0) continue;
-    if (A.n_split == 1) {
-      f.write_out(rb, head);
-    } else {
-      const size_t part = (static_cast<size_t>(f.q.row0 + t) * A.Hq + head) * A.n_split + blockIdx.y;
-      float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
-      f.write_part(rb, A.part + part * D, ml + part * 2);
-    }
+  int t;
+  const int head = f.row_head(&t);
+  if (head < 0) return;
+  if (A.n_split == 1) {
+    f.write_out(head);
+  } else {
+    const size_t part = (static_cast<size_t>(f.q.row0 + t) * A.Hq + head) * A.n_split + blockIdx.y;
+    float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
+    f.write_part(A.part + part * D, ml + part * 2);
   }
 }
 
@@ -562,7 +620,7 @@ __host__ __device__ inline size_t tree_meta_offset(const TreeSplit& t, int D) {
 // with many loads in flight: 256 CUs x 8 waves, 64 - 96 KB per CU.
 constexpr int kTreeKeys = 32, kUnitCost = 4;
 template <int D, int RW>
-using TreeFlash = Flash<D, RW, 1, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
+using TreeFlash = Flash<D, RW, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
 
 template <int D, int RW>
 __global__ __launch_bounds__((TreeFlash<D, RW>::THREADS), 2) void flash_tree_kernel(AttnArgs A, TreeSplit ts) {
@@ -672,13 +730,13 @@ __global__ __launch_bounds__((TreeFlash<D, RW>::THREADS), 2) void flash_tree_ker
         *unit_meta = make_int2(static_cast<int>(w), static_cast<int>(((end + 1) * W - 1) / total - w) + 1);
       }
       int t;
-      const int head = f.row_head(0, &t);
+      const int head = f.row_head(&t);
       if (head >= 0) {
         if (lo == 0 && hi == tiles) {
-          f.write_out(0, head);
+          f.write_out(head);
         } else {
           const size_t row = (static_cast<size_t>(2) * w + (lo == 0 ? 1 : 0)) * F::BM + f.wave * 32 + f.col;
-          f.write_part(0, A.part + row * D, A.part + tree_ml_offset(ts, D) + row * 2);
+          f.write_part(A.part + row * D, A.part + tree_ml_offset(ts, D) + row * 2);
         }
       }
     }

@@ -69,10 +69,16 @@ def test_workspace_sizes(gdn):
     """Few row tiles split the key axis and need a workspace; many do not."""
     g = gdn.AttnGeometry(max_tree=64)
     assert gdn.attn_prefill_workspace_bytes(g, 100000, 4) == 0
+    # fp32: a part (sums, maximum, sum of weights) per row and split
     per = 24 * (256 + 2) * 4
+    g32 = gdn.AttnGeometry(max_tree=64, dtype=torch.float32)
     for n, b in ((1, 1), (16, 4), (64, 2)):
-        w = gdn.attn_tree_workspace_bytes(g, b, n)
+        w = gdn.attn_tree_workspace_bytes(g32, b, n)
         assert w % (per * b * n) == 0 and 2 <= w // (per * b * n) <= 1024
+    # bf16: parts of at most two blocks of rows (32 at least) per workgroup, so
+    # the batch adds no more than 8 bytes per block of rows
+    one, many = (gdn.attn_tree_workspace_bytes(g, b, 1) for b in (1, 1000))
+    assert one >= 2 * 32 * (256 + 2) * 4 and 0 < many - one <= 8 * 1000 * 4 + 256
 
 
 def test_binding_refuses_host_tensors(gdn):
