@@ -194,11 +194,13 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _need(t: Optional[torch.Tensor], name: str, shape, dtype, optional=False):
+    if t is not None and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
     if t is None:
         if optional:
             return
@@ -562,7 +564,7 @@ def _same_device(*named):
     """Every tensor on the current device (the calls launch there): refused otherwise."""
     cur = torch.cuda.current_device()
     for name, t in named:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"{name}: on {t.device}, required: the current device cuda:{cur}")
 
 
