@@ -17,7 +17,9 @@
 // product as they are.
 //
 // With more than one split of the key axis each split writes its unscaled sums
-// with (m, l), and combine_kernel joins them in a fixed order.
+// with (m, l), and attn_combine_kernel joins them in a fixed order.
+#include <algorithm>
+
 #include "gdn_attn_device.h"
 
 namespace gdn {
@@ -27,14 +29,33 @@ namespace {
 __device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
+// Maximum over the four lanes of a column (lanes l % 16).
+__device__ __forceinline__ float quarter_max(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));  // of rows of 16 lanes: 0 0 2 2 and 1 1 3 3
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));  // of halves: 0 0 and 1 1
+}
 }  // namespace
 
 // ---------------------------------------------------------------------------
 // fp32: 64 rows x 32 keys per step, four waves of 16 rows each, K and V rows
-// staged through LDS.  16x16x4 matrix instructions: lane l holds rows (keys)
-// 4 (l / 16) + i of column (query row) l % 16.  (bf16: gdn_flash.hip.)
+// staged through LDS.  16x16x4 matrix instructions: with c = l % 16, g = l / 16,
+// lane l holds rows 4 g + i of column (query row) c of a product, and element
+// (c, g) of an operand.  What index of a row an operand's element stands for is
+// free as long as both operands agree, and is taken so that four instructions'
+// operands are 16 bytes of LDS: instruction 4 s + i of the logits contracts
+// elements 16 s + 4 g + i of K and Q; instruction i of half h of the keys
+// contracts keys 16 h + 4 g + i (where the weights are), and row c of V^T's block
+// dt stands for d = 64 (dt / 4) + 4 c + dt % 4.  (bf16: gdn_flash.hip.)
+//
+// Bound by the matrix instructions and, as much again, the vector instructions of
+// softmax, addresses and copies between them: 1024 tokens of 8 heads on 2, d 64,
+// behind 4096 cached ones 132 us (73 TFLOP/s; a large fp32 product reaches 154); short prompts (301, 1 and
+// 777 tokens) 30 us, of which the join of the splits is 4.
 // ---------------------------------------------------------------------------
 constexpr int kGenRows = 64, kGenKeys = 32, kGenThreads = 256;
+constexpr int kMaxSplits = 64;  // parts of a row
 
 template <int D>
 struct GenShape {
@@ -76,13 +97,15 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
   }
   const int64_t rows = static_cast<int64_t>(q.n) * A.G;
   if (q.n == 0 || r0 >= rows) return;
-  const int64_t r = r0 + wave * 16 + col;
-  const bool row_ok = r < rows;
-  const int t = static_cast<int>((row_ok ? r : r0) / A.G);   // this lane's token
-  const int head = kvh * A.G + static_cast<int>((row_ok ? r : r0) % A.G);
-  const int t_first = static_cast<int>(r0 / A.G);
-  const int64_t r_last = r0 + kGenRows < rows ? r0 + kGenRows - 1 : rows - 1;
-  const int t_last = static_cast<int>(r_last / A.G);
+  const int32_t left = static_cast<int32_t>(rows - r0 < kGenRows ? rows - r0 : kGenRows);  // rows of the tile
+  const int t_first = uniform(static_cast<int32_t>(r0 / A.G));
+  const int h_first = uniform(static_cast<int32_t>(r0 - static_cast<int64_t>(t_first) * A.G));
+  const int32_t r = wave * 16 + col;
+  const bool row_ok = r < left;
+  const int32_t rh = h_first + (row_ok ? r : 0);
+  const int t = t_first + rh / A.G;   // this lane's token
+  const int head = kvh * A.G + rh % A.G;
+  const int t_last = t_first + (h_first + left - 1) / A.G;
   uint64_t my_path = 0;
   if constexpr (TREE)
     my_path = (static_cast<uint64_t>(__shfl(static_cast<uint32_t>(path >> 32), t, 64)) << 32) |
@@ -100,32 +123,82 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
   {
     const char* qp = static_cast<const char*>(A.q) + ((q.row0 + t) * A.q_stride + static_cast<int64_t>(head) * D) * ES;
 #pragma unroll
-    for (int s = 0; s < QF; ++s) qf[s] = *reinterpret_cast<const float*>(qp + (s * 4 + g) * 4);
+    for (int s = 0; s < QF; s += 4) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(qp + (s * 4 + 4 * g) * ES);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[s + i] = v[i];
+    }
   }
   f32x4_t O[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) O[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;  // l: this lane's part of the sum
 
+  // ---- tiles through registers: vector i of this thread belongs to key
+  // kr0 + i KSTEP of a tile.  Page ids are read two tiles ahead, rows one ----
+  constexpr int NV = kGenKeys * Sh::VPR / kGenThreads, KSTEP = kGenThreads / Sh::VPR;
+  const int kr0 = tid / Sh::VPR, w = tid % Sh::VPR;
+  int32_t page[NV], off[NV];
+  uint4 kreg[NV], vreg[NV];
+  auto read_ids = [&](int32_t kt) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int32_t j = min(kt * kGenKeys + kr0 + i * KSTEP, q.ctx - 1);
+      page[i] = off[i] = 0;
+      if (j >= 0) {
+        const int32_t e = static_cast<int32_t>(static_cast<uint32_t>(j) / static_cast<uint32_t>(A.page));
+        off[i] = j - e * A.page;
+        page[i] = A.block_table[static_cast<size_t>(q.index) * A.max_pages + e];
+      }
+    }
+  };
+  auto read_rows = [&](int32_t kt) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int32_t j = min(kt * kGenKeys + kr0 + i * KSTEP, n_keys - 1);  // past the last: the last, which no row attends there
+      const char *kp, *vp;
+      if (j < q.ctx) {
+        int32_t pg = page[i];
+        if (pg < 0 || pg >= A.n_pages) {
+          report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+          pg = 0;
+        }
+        const size_t at = ((static_cast<size_t>(pg) * A.Hk + kvh) * A.page + off[i]) * static_cast<size_t>(D) * ES;
+        kp = static_cast<const char*>(A.k_cache) + at;
+        vp = static_cast<const char*>(A.v_cache) + at;
+      } else {
+        const int64_t row = q.row0 + (j - q.ctx), head_at = static_cast<int64_t>(kvh) * D;
+        kp = static_cast<const char*>(A.k) + (row * A.k_stride + head_at) * ES;
+        vp = static_cast<const char*>(A.v) + (row * A.v_stride + head_at) * ES;
+      }
+      kreg[i] = *reinterpret_cast<const uint4*>(kp + 16 * w);
+      vreg[i] = *reinterpret_cast<const uint4*>(vp + 16 * w);
+    }
+  };
+  if (tile_lo < tile_hi) {
+    read_ids(tile_lo);
+    read_rows(tile_lo);
+    read_ids(tile_lo + 1);
+  }
+
   for (int32_t kt = tile_lo; kt < tile_hi; ++kt) {
     const int32_t key0 = kt * kGenKeys;
     const bool masked = key0 + kGenKeys > clear;
-    __syncthreads();
+    lds_barrier();
     if (masked && tid == 0) *bad_keys = 0;
-    if (masked) __syncthreads();
-    for (int e = tid; e < kGenKeys * Sh::VPR; e += kGenThreads) {
-      const int kr = e / Sh::VPR, w = e % Sh::VPR;
-      const int32_t j = key0 + kr;
-      uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-      if (j < n_keys) {
-        kv = *reinterpret_cast<const uint4*>(key_row<ES>(A, q, A.k_cache, A.k, A.k_stride, kvh, j) + 16 * w);
-        vv = *reinterpret_cast<const uint4*>(key_row<ES>(A, q, A.v_cache, A.v, A.v_stride, kvh, j) + 16 * w);
-      }
-      if (masked && any_nonfinite<false>(vv)) atomicOr(bad_keys, 1u << kr);
-      *reinterpret_cast<uint4*>(Ks + kr * LD + w * Sh::VEC) = kv;
-      *reinterpret_cast<uint4*>(Vs + kr * LD + w * Sh::VEC) = vv;
+    if (masked) lds_barrier();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int kr = kr0 + i * KSTEP;
+      if (masked && any_nonfinite<false>(vreg[i])) atomicOr(bad_keys, 1u << kr);
+      *reinterpret_cast<uint4*>(Ks + kr * LD + w * Sh::VEC) = kreg[i];
+      *reinterpret_cast<uint4*>(Vs + kr * LD + w * Sh::VEC) = vreg[i];
     }
-    __syncthreads();
+    if (kt + 1 < tile_hi) {
+      read_rows(kt + 1);
+      read_ids(kt + 2);
+    }
+    lds_barrier();
     // Values that are not finite must not reach rows that do not attend their
     // key (0 x inf is NaN): such V rows leave the product and are added below.
     uint32_t bad = 0;
@@ -135,33 +208,36 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
         for (int e = tid; e < kGenKeys * Sh::VPR; e += kGenThreads)
           if ((bad >> (e / Sh::VPR)) & 1u)
             *reinterpret_cast<uint4*>(Vs + (e / Sh::VPR) * LD + (e % Sh::VPR) * Sh::VEC) = make_uint4(0, 0, 0, 0);
-        __syncthreads();
+        lds_barrier();
       }
     }
     // ---- logits, keys 16 kt2 + 4 g + i ----
-    float x[2][4];
-    float mx = -INFINITY;
+    f32x4_t x[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int k2 = 0; k2 < 2; ++k2) {
-      f32x4_t c = {0.f, 0.f, 0.f, 0.f};
-      const E* kr = Ks + (16 * k2 + col) * LD;
-#pragma unroll
-      for (int s = 0; s < QF; ++s) c = mfma_f32(kr[s * 4 + g], qf[s], c);
+    for (int s = 0; s < QF; s += 4) {
+      const f32x4_t k0 = *reinterpret_cast<const f32x4_t*>(Ks + col * LD + s * 4 + 4 * g);
+      const f32x4_t k1 = *reinterpret_cast<const f32x4_t*>(Ks + (16 + col) * LD + s * 4 + 4 * g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int32_t j = key0 + 16 * k2 + 4 * g + i;
+        x[0] = mfma_f32(k0[i], qf[s + i], x[0]);
+        x[1] = mfma_f32(k1[i], qf[s + i], x[1]);
+      }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         bool seen = true;
         if (masked) {
-          const int32_t own = j - q.ctx;
+          const int32_t own = key0 + 16 * k2 + 4 * g + i - q.ctx;
           if constexpr (TREE) seen = own < 0 || (own < q.n && ((my_path >> own) & 1ull));
           else seen = own <= t;
         }
-        x[k2][i] = seen ? c[i] * A.scale_log2 : -INFINITY;
+        x[k2][i] = seen ? x[k2][i] * A.scale_log2 : -INFINITY;
         mx = fmaxf(mx, x[k2][i]);
       }
-    }
-    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    mx = quarter_max(mx);
     const float m_new = fmaxf(m, mx);
     const float ref = m_new == -INFINITY ? 0.f : m_new;  // no key seen yet: all weights 2^-inf = 0
     const float scale = __builtin_amdgcn_exp2f(m - ref);
@@ -175,24 +251,28 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
         P[k2][i] = __builtin_amdgcn_exp2f(x[k2][i] - ref);
         l += P[k2][i];
       }
+    if (__any(scale != 1.f)) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) O[i] *= scale;
+      for (int i = 0; i < NT; ++i) O[i] *= scale;
+    }
     // ---- O^T += V^T P^T; the contraction runs over keys 4 g + i of both halves ----
 #pragma unroll
-    for (int dt = 0; dt < NT; ++dt) {
-      const E* vc = Vs + 4 * g * LD + 16 * dt + col;
+    for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) O[dt] = mfma_f32(vc[(16 * k2 + i) * LD], P[k2][i], O[dt]);
-    }
+        for (int dt = 0; dt < NT; dt += 4) {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(Vs + (16 * k2 + 4 * g + i) * LD + 16 * dt + 4 * col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) O[dt + e] = mfma_f32(v[e], P[k2][i], O[dt + e]);
+        }
     if (bad) {  // same for the whole workgroup
       float* pw = Ps + wave * kGenKeys * 16;
 #pragma unroll
       for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) pw[(16 * k2 + 4 * g + i) * 16 + col] = P[k2][i];
-      __syncthreads();
+      lds_barrier();
       for (uint32_t left = bad; left != 0; left &= left - 1) {
         const int kr = __builtin_ctz(left);
         const int32_t j = key0 + kr, own = j - q.ctx;
@@ -205,7 +285,7 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
 #pragma unroll
         for (int dt = 0; dt < NT; ++dt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) O[dt][i] += p * load_in<false>(vr, 16 * dt + 4 * g + i);
+          for (int i = 0; i < 4; ++i) O[dt][i] += p * load_in<false>(vr, 64 * (dt / 4) + 16 * g + 4 * i + dt % 4);
       }
     }
   }
@@ -213,11 +293,16 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
   l += __shfl_xor(l, 32, 64);
   if (!row_ok) return;
   const size_t orow = static_cast<size_t>(q.row0 + t) * A.Hq + head;
-  if (A.n_split == 1) {
-    const float inv = 1.0f / l;
+  auto write = [&](float* to, float by) {
 #pragma unroll
-    for (int dt = 0; dt < NT; ++dt)
-      *reinterpret_cast<f32x4_t*>(static_cast<float*>(A.o) + orow * D + 16 * dt + 4 * g) = O[dt] * inv;
+    for (int dt = 0; dt < NT; dt += 4)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4_t*>(to + 16 * dt + 16 * g + 4 * i) =
+            f32x4_t{O[dt][i], O[dt + 1][i], O[dt + 2][i], O[dt + 3][i]} * by;
+  };
+  if (A.n_split == 1) {
+    write(static_cast<float*>(A.o) + orow * D, 1.0f / l);
   } else {
     const size_t part = orow * A.n_split + z;
     float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D;
@@ -225,66 +310,62 @@ __global__ __launch_bounds__(kGenThreads) void attn_f32_kernel(AttnArgs A) {
       ml[part * 2] = m;
       ml[part * 2 + 1] = l;
     }
-    if (tile_lo < tile_hi) {
-#pragma unroll
-      for (int dt = 0; dt < NT; ++dt)
-        *reinterpret_cast<f32x4_t*>(A.part + part * D + 16 * dt + 4 * g) = O[dt];
-    }
+    if (tile_lo < tile_hi) write(A.part + part * D, 1.0f);
   }
 }
 
-// Joins the splits of a row: weights 2^(m_z - max m), in the order of z.  D/4
-// lanes per row.  A split that saw no key (its m is -inf and its sum 0) wrote
-// no sums and is left out.
+// Joins the splits of a row: weights 2^(m_z - max m).  A wave takes one row:
+// D / 4 lanes hold its elements, 256 / D groups of them every 256 / D-th split.
+// A split that saw no key (its m is -inf and its sum 0) wrote no sums and is
+// left out.
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
-  constexpr int LPR = D / 4, RPW = 256 / LPR;
-  const int c = (threadIdx.x % LPR) * 4;
-  const int64_t orow = static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / LPR;
-  const int64_t total = static_cast<int64_t>(A.n_tokens) * A.Hq;
-  const int64_t tok = (orow < total ? orow : total - 1) / A.Hq;
+  constexpr int LPR = D / 4, NG = kWave / LPR;
+  const int lane = threadIdx.x & (kWave - 1), c = (lane % LPR) * 4, g = lane / LPR;
+  const int64_t orow = static_cast<int64_t>(blockIdx.x) * 4 + uniform(static_cast<int32_t>(threadIdx.x / kWave));
+  if (orow >= static_cast<int64_t>(A.n_tokens) * A.Hq) return;
+  const int32_t tok = static_cast<int32_t>(orow / A.Hq);
   // rows that no workgroup computed (a refused sequence, padding) stay as they are
-  bool live = orow < total;
   if (A.nodes > 0) {
-    // the wave's rows may belong to several trees: each is checked by the whole wave
-    const int s = static_cast<int>(tok / A.nodes);
-    const int node = static_cast<int>(tok - static_cast<int64_t>(s) * A.nodes);
-    uint64_t todo = __ballot(true);
-    bool ok = false;
-    while (todo != 0) {
-      const int leader = __builtin_ctzll(todo);
-      const int sl = __builtin_amdgcn_readlane(s, leader);
-      uint64_t path;
-      const Seq q = tree_seq(A, sl, false, &path);
-      if (s == sl) ok = node < q.n;
-      todo &= ~__ballot(s == sl);
-    }
-    live &= ok;
+    uint64_t path;
+    const int s = tok / A.nodes;
+    if (tok - s * A.nodes >= tree_seq(A, s, false, &path).n) return;
   } else {
-    int lo = 0, hi = A.n_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (A.cu_seqlens[mid] <= tok) lo = mid;
-      else hi = mid;
+    int s = 0;  // the last sequence that does not begin after the token
+    for (int base = 0; base < A.n_seqs; base += kWave) {
+      const uint64_t on = __ballot(base + lane < A.n_seqs && A.cu_seqlens[min(base + lane, A.n_seqs - 1)] <= tok);
+      if (on == 0) break;
+      s = base + 63 - __builtin_clzll(on);
     }
-    const Seq q = packed_seq(A, lo, false);
-    live &= q.n > 0 && tok >= q.row0 && tok < q.row0 + q.n;
+    const Seq q = packed_seq(A, s, false);
+    if (q.n == 0 || tok < q.row0 || tok >= q.row0 + q.n) return;
   }
-  if (!live) return;
-  const float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D +
-                    static_cast<size_t>(orow) * A.n_split * 2;
-  float m = -INFINITY;
-  for (int z = 0; z < A.n_split; ++z) m = fmaxf(m, ml[2 * z]);
+  const float* ml = A.part + static_cast<size_t>(A.n_tokens) * A.Hq * A.n_split * D + static_cast<size_t>(orow) * A.n_split * 2;
+  const float* sums = A.part + static_cast<size_t>(orow) * A.n_split * D + c;
+  static_assert(kMaxSplits <= kWave, "a lane per split");
+  const bool mine = lane < A.n_split;
+  const float mz = mine ? ml[2 * lane] : -INFINITY, lz = mine ? ml[2 * lane + 1] : 0.f;
+  float m = mz;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
   const float ref = m == -INFINITY ? 0.f : m;
+  const float weight = mz == -INFINITY && lz == 0.f ? 0.f : __builtin_amdgcn_exp2f(mz - ref);
+  const float l = group_sum<kWave>(weight * lz);
+  const uint64_t on = __ballot(!(mz == -INFINITY && lz == 0.f));
   f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int z = 0; z < A.n_split; ++z) {
-    const float mz = ml[2 * z], lz = ml[2 * z + 1];
-    if (mz == -INFINITY && lz == 0.f) continue;
-    const float w = __builtin_amdgcn_exp2f(mz - ref);
-    l += w * lz;
-    sum += w * load4(A.part + (static_cast<size_t>(orow) * A.n_split + z) * D + c);
+#pragma unroll 8
+  for (int z = g; z < A.n_split; z += NG) {
+    const f32x4_t x = load4(sums + static_cast<size_t>(z) * D);
+    const float w = __shfl(weight, z, kWave);
+    const bool seen = (on >> z) & 1ull;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += seen ? w * x[e] : 0.f;
   }
+#pragma unroll
+  for (int d = LPR; d < kWave; d <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], d, kWave);
+  if (g != 0) return;
   sum *= 1.0f / l;
   const size_t at = static_cast<size_t>(orow) * D + c;
   if constexpr (BF16)
@@ -307,17 +388,20 @@ int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
 
 }  // namespace
 
-int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int nodes, bool bf16) {
+// fp32: four workgroups per CU (that is what fits at d 64 and hides one's
+// softmax behind the others' products: 2048 tokens of 8 heads 134 us with two,
+// 100 us with four, 84 us with eight, where 256 tokens then take 19 us instead
+// of 12).  bf16: two (one or two fit).  No more than the key axis has tiles.
+int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int nodes, bool bf16, int64_t keys) {
   if (bf16 && nodes > 0) return 1;
-  // two workgroups per CU, and at most 64 parts to join
   const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kFlashRows : kGenRows) * Hk;
-  const int64_t want = wgs > 0 ? 512 / wgs : 1;
-  return static_cast<int>(want < 1 ? 1 : (want > 64 ? 64 : want));
+  const int64_t want = wgs > 0 ? (bf16 ? 512 : 1024) / wgs : 1, tiles = (keys + kGenKeys - 1) / kGenKeys;
+  return static_cast<int>(std::max<int64_t>(std::min({want, tiles, static_cast<int64_t>(kMaxSplits)}), 1));
 }
 
 size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
   if (bf16 && nodes > 0) return flash_tree_part_bytes(n_seqs, Hk, G, D, nodes);
-  const int n_split = attn_splits(tokens, n_seqs, Hk, G, nodes, bf16);
+  const int n_split = attn_splits(tokens, n_seqs, Hk, G, nodes, bf16, INT64_MAX - kGenKeys);
   return n_split <= 1 ? 0 : static_cast<size_t>(tokens) * Hk * G * n_split * (D + 2) * sizeof(float);
 }
 
@@ -337,9 +421,8 @@ static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
   }
   int e = static_cast<int>(hipGetLastError());
   if (e == 0 && a.n_split > 1) {
-    const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.Hq, per = 256 / (D / 4);
-    hipLaunchKernelGGL((attn_combine_kernel<D, BF16>), dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256),
-                       0, s, a);
+    const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.Hq;  // few: a call of many rows is not split
+    hipLaunchKernelGGL((attn_combine_kernel<D, BF16>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, s, a);
     e = static_cast<int>(hipGetLastError());
   }
   return e;

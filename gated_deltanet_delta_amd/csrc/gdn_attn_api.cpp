@@ -61,8 +61,11 @@ gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, c
   return GDN_OK;
 }
 
-int attn_split(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes) {
-  return gdn::attn_splits(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, nodes, g->dtype == GDN_BF16);
+// own: the largest number of keys that a sequence has among the call's tokens
+int attn_split(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes, int64_t own, bool cached) {
+  const int64_t keys = own + (cached ? static_cast<int64_t>(g->max_pages) * g->page_tokens : 0);
+  return gdn::attn_splits(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, nodes, g->dtype == GDN_BF16,
+                          keys);
 }
 size_t attn_bytes(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes) {
   return gdn::attn_part_bytes(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head, nodes,
@@ -202,7 +205,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q
   if ((s = check_stride(g, q_stride, g->n_q_heads, "q_stride")) != GDN_OK) return s;
   if ((s = check_stride(g, k_stride, g->n_kv_heads, "k_stride")) != GDN_OK) return s;
   if ((s = check_stride(g, v_stride, g->n_kv_heads, "v_stride")) != GDN_OK) return s;
-  const int n_split = attn_split(g, n_tokens, n_seqs, 0);
+  const int n_split = attn_split(g, n_tokens, n_seqs, 0, n_tokens, ctx_len != nullptr);
   s = check_workspace(workspace, workspace_bytes, attn_bytes(g, n_tokens, n_seqs, 0));
   if (s != GDN_OK) return s;
   GDN_NEED_PTR4(cu_seqlens, "cu_seqlens");
@@ -249,7 +252,7 @@ gdn_status gdn_attn_tree(const gdn_attn_geometry* g, const void* q, int64_t q_st
   if ((s = check_stride(g, k_stride, g->n_kv_heads, "k_stride")) != GDN_OK) return s;
   if ((s = check_stride(g, v_stride, g->n_kv_heads, "v_stride")) != GDN_OK) return s;
   const int64_t rows = static_cast<int64_t>(batch) * n;
-  const int n_split = attn_split(g, rows, batch, n);
+  const int n_split = attn_split(g, rows, batch, n, n, true);
   s = check_workspace(workspace, workspace_bytes, attn_bytes(g, rows, batch, n));
   if (s != GDN_OK) return s;
   GDN_NEED_PTR(q, "q");
