@@ -388,20 +388,27 @@ int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
 
 }  // namespace
 
-// fp32: four workgroups per CU (that is what fits at d 64 and hides one's
-// softmax behind the others' products: 2048 tokens of 8 heads 134 us with two,
-// 100 us with four, 84 us with eight, where 256 tokens then take 19 us instead
-// of 12).  bf16: two (one or two fit).  No more than the key axis has tiles.
-int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int nodes, bool bf16, int64_t keys) {
+// Parts of the key axis that a row tile is split into.  fp32: up to four
+// workgroups per CU (that is what fits at d 64 and hides one's softmax behind the
+// others' products: 2048 tokens of 8 heads 134 us with two, 100 us with four, 84 us
+// with eight, where 256 tokens then take 19 us instead of 12).  bf16: one per CU
+// (LDS holds one at d 128 and 256), none of fewer than 128 keys: parts are written
+// and read once more, and with two per CU 512 tokens of 24 heads on 4, d 256, took
+// 64 us instead of 40, 256 behind 8192 cached ones 102 instead of 77.  At d 64 two
+// workgroups fit and the last part may begin beside others (4096 tokens 88 us in
+// 130 workgroups, 64 us in 260).
+int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16, int64_t keys) {
   if (bf16 && nodes > 0) return 1;
   const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kFlashRows : kGenRows) * Hk;
-  const int64_t want = wgs > 0 ? (bf16 ? 512 : 1024) / wgs : 1, tiles = (keys + kGenKeys - 1) / kGenKeys;
-  return static_cast<int>(std::max<int64_t>(std::min({want, tiles, static_cast<int64_t>(kMaxSplits)}), 1));
+  if (wgs <= 0) return 1;
+  const int64_t want = !bf16 ? 1024 / wgs : (D == 64 ? (255 + wgs) / wgs : 256 / wgs);
+  const int64_t least = bf16 ? 128 : kGenKeys, parts = keys / least + (keys % least != 0);
+  return static_cast<int>(std::max<int64_t>(std::min({want, parts, static_cast<int64_t>(kMaxSplits)}), 1));
 }
 
 size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
   if (bf16 && nodes > 0) return flash_tree_part_bytes(n_seqs, Hk, G, D, nodes);
-  const int n_split = attn_splits(tokens, n_seqs, Hk, G, nodes, bf16, INT64_MAX - kGenKeys);
+  const int n_split = attn_splits(tokens, n_seqs, Hk, G, D, nodes, bf16, INT64_MAX);
   return n_split <= 1 ? 0 : static_cast<size_t>(tokens) * Hk * G * n_split * (D + 2) * sizeof(float);
 }
 

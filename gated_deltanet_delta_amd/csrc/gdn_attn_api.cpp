@@ -64,8 +64,8 @@ gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, c
 // own: the largest number of keys that a sequence has among the call's tokens
 int attn_split(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes, int64_t own, bool cached) {
   const int64_t keys = own + (cached ? static_cast<int64_t>(g->max_pages) * g->page_tokens : 0);
-  return gdn::attn_splits(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, nodes, g->dtype == GDN_BF16,
-                          keys);
+  return gdn::attn_splits(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head, nodes,
+                          g->dtype == GDN_BF16, keys);
 }
 size_t attn_bytes(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes) {
   return gdn::attn_part_bytes(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head, nodes,
