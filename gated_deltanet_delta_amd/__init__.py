@@ -570,6 +570,8 @@ def _same_device(*named):
 
 def _need_rows(t: Optional[torch.Tensor], name: str, shape, dtype) -> int:
     """Rows of heads, any row stride, contiguous within a row; returns the row stride in elements."""
+    if t is not None and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return shape[-2] * shape[-1]
     if t is None:
         raise ValueError(f"{name}: missing")
     if not t.is_cuda:
