@@ -100,6 +100,8 @@ int main(void) {
   CHECK(32, gdn_attn_prefill(&g, P, 6144, P, 1024, P, 1024, PI, 1, 1 << 30, P, P, PI, PI, P, BIG, P, NULL, NULL) == GDN_ERR_RANGE);
   CHECK(33, gdn_attn_prefill(&g, P, 6136, P, 1024, P, 1024, PI, 1, 9, P, P, PI, PI, P, BIG, P, NULL, NULL) == GDN_ERR_RANGE && has("q_stride"));
   size_t w = gdn_attn_prefill_workspace_bytes(&g, 9, 1);
+  CHECK(42, gdn_attn_prefill(&g, P, 1 << 24, P, 1024, P, 1024, PI, 1, 9, P, P, PI, PI, P, BIG, P, NULL, NULL) == GDN_ERR_RANGE && has("q_stride: 16777216"));
+  CHECK(43, gdn_attn_prefill(&g, P, 6144, P, 1024, P, 1LL << 33, PI, 1, 9, P, P, PI, PI, P, BIG, P, NULL, NULL) == GDN_ERR_RANGE && has("v_stride"));
   CHECK(34, w > 0 && gdn_attn_prefill(&g, P, 6144, P, 1024, P, 1024, PI, 1, 9, P, P, PI, PI, P, w - 1, P, NULL, NULL) == GDN_ERR_WORKSPACE);
   CHECK(35, gdn_attn_prefill(&g, P, 6144, P, 1024, P, 1024, PI, 1, 9, P, P, PI, PI, NULL, w, P, NULL, NULL) == GDN_ERR_NULL && has("workspace"));
   CHECK(36, gdn_attn_prefill(&g, P, 6144, P, 1024, P, 1024, NULL, 1, 9, P, P, PI, PI, P, w, P, NULL, NULL) == GDN_ERR_NULL && has("cu_seqlens"));

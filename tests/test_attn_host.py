@@ -105,6 +105,9 @@ class _OnGpu:
     def stride(self):
         return self.t.stride()
 
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
 
 def test_row_strides_of_the_binding(gdn):
     """Parts of a fused row pass with their row's stride; transposed or scattered rows are refused."""

@@ -169,6 +169,81 @@ def test_prefill_refused_sequences():
     assert int(err.item()) == m.DEV_BAD_PAGE and torch.equal(o[:20], good[:20]) and torch.equal(o[50:], good[50:])
 
 
+def _check_sequences(pg, parts, cu, ctx, o, scale, dtype, what):
+    """Every sequence of a packed batch on its own (its keys alone set its bound)."""
+    q, k, v = (AH.host(p) for p in parts)
+    kc, vc = AH.host(pg.k), AH.host(pg.v)
+    Hk, D = k.shape[1:]
+    for i, c in enumerate(ctx):
+        lo, hi = int(cu[i]), int(cu[i + 1])
+        if lo == hi:
+            continue
+        ref, mag = ao.prefill(q[lo:hi], k[lo:hi], v[lo:hi], np.array([0, hi - lo]), kc, vc, pg.table[i:i + 1].numpy(), [c], scale)
+        pages = np.nan_to_num(kc[pg.table[i, :-(-c // kc.shape[2])].numpy()]).transpose(0, 2, 1, 3).reshape(-1, Hk, D)
+        _check(o[lo:hi], ref, mag, q[lo:hi], np.concatenate([k[lo:hi], pages]), scale, c + hi - lo, dtype, f"{what} {i}")
+
+
+@pytest.mark.parametrize("S,Hk,G,D,dtype", [(64, 1, 3, 64, BF16), (65, 2, 2, 128, BF16), (150, 1, 4, 64, BF16), (70, 2, 3, 64, F32)])
+def test_prefill_many_sequences(S, Hk, G, D, dtype):
+    """Up to and past 64 sequences: empty ones, single tokens, several blocks of rows, prefixes of all lengths, two of
+    each length so that blocks of equal lengths meet."""
+    rng = np.random.Generator(np.random.PCG64(S))
+    half = [int(n) for n in rng.integers(0, 120, size=S // 2)]
+    new = (half + half + [300])[:S] if S % 2 == 0 else half + half + [300]
+    ctx = [int(c) for c in rng.integers(0, 90, size=S // 2)]
+    ctx = ctx + ctx + [0] * (S - 2 * (S // 2))
+    new[1], new[2], ctx[2] = 0, 1, 0
+    m, geom, pg, parts, dev, cu, o = _prefill_case(500 + S, new, ctx, Hk, G, D, 16, dtype)
+    err = _err()
+    _run_prefill(m, geom, pg, dev, cu, ctx, o, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    _check_sequences(pg, parts, cu, ctx, o, D ** -0.5, dtype, "sequence")
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, BF16), (128, F32)])
+def test_prefill_few_rows_behind_long_prefixes(D, dtype):
+    """Few rows, many keys: the key axis is split, with parts that hold no key of the shorter rows, and joined; a
+    sequence of its own and the same one in a batch of three differ by their rounding only."""
+    new, ctx = [3, 1, 20], [3000, 0, 517]
+    m, geom, pg, parts, dev, cu, o = _prefill_case(520 + D, new, ctx, 1, 4, D, 16, dtype)
+    assert m.attn_prefill_workspace_bytes(geom, sum(new), 3) > 0
+    err = _err()
+    _run_prefill(m, geom, pg, dev, cu, ctx, o, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    _check_sequences(pg, parts, cu, ctx, o, D ** -0.5, dtype, "sequence")
+
+
+def test_prefill_refused_sequence_among_many():
+    """Blocks are ordered by their keys across sequences: a refused one leaves the others right, wherever it stands."""
+    new, ctx = [40, 90, 40, 7, 200], [0, 64, 0, 300, 16]
+    m, geom, pg, parts, dev, cu, o = _prefill_case(530, new, ctx, 2, 4, 64, 16, BF16)
+    err = _err()
+    for at in range(5):
+        bad = list(ctx)
+        bad[at] = -1
+        err.zero_()
+        o.fill_(7.0)
+        _run_prefill(m, geom, pg, dev, cu, bad, o, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == m.DEV_BAD_LENGTH
+        assert torch.all(o[cu[at]:cu[at + 1]] == 7.0)
+        for i in range(5):
+            if i == at:
+                continue
+            one = slice(int(cu[i]), int(cu[i + 1]))
+            alone = torch.full_like(o[one], 7.0)
+            m.attn_prefill(geom, *(t[one] for t in dev), _cuda([0, new[i]]), alone,
+                           m.alloc_attn_prefill_workspace(geom, new[i], 1), cache=pg.cache(),
+                           block_table=pg.table[i:i + 1].cuda(), ctx_len=_cuda([ctx[i]]), dev_err=_err())
+            torch.cuda.synchronize()
+            # each result's weights are rounded, against its own running maximum (h sum p |v|, |v| < max |v| + 4
+            # in the cache too), and each output (h |o|)
+            off = (alone.float() - o[one].float()).abs()
+            assert (off <= 2 * AH.half_step(BF16) * (alone.float().abs() + float(parts[2].abs().max()) + 4)).all()
+
+
 # ---------------------------------------------------------------------------
 # trees
 # ---------------------------------------------------------------------------

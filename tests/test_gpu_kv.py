@@ -151,6 +151,23 @@ def test_plan_refused_values():
     assert code == m.DEV_BAD_PAGE and np.all(t["slot_map"][5:12] == -1) and np.all(t["slot_map"][:5] >= 0)
 
 
+def test_plan_sums_past_31_bits():
+    """Lengths that are refused still count as tokens: their sum stays at the slot map's size, the served rows before
+    them get theirs, the ones behind none."""
+    m = AH.gdn()
+    kv, new = [10, 20, 20, 20, 30], [5, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 3]
+    n_pages, width, tables, free, n_free = _plan_inputs(6, kv, [5, 7, 7, 7, 3], 16, 4)
+    geom = m.AttnGeometry(n_q_heads=1, n_kv_heads=1, d_head=64, page_tokens=16, n_pages=n_pages, max_pages=width)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t, _ = _plan(geom, kv, new, free, n_free, tables, 700, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) in (m.DEV_BAD_LENGTH, m.DEV_BAD_SEQLENS)  # both hold; the first that lands is kept
+    assert t["cu_new"].tolist() == [0, 5, 700, 700, 700, 700]
+    assert t["kv_len_out"].tolist() == [15, 20, 20, 20, 33]
+    slots = t["slot_map"].cpu().numpy()
+    assert slots[0] == tables[0, 0] * 16 + 10 and np.all(slots[5:] == -1)
+
+
 @pytest.mark.parametrize("N,Hk,D,page,dtype,fused", [
     (1, 1, 64, 16, BF16, False), (5, 4, 256, 16, BF16, True), (530, 2, 128, 528, BF16, False), (100, 8, 64, 32, F32, True),
     (3000, 1, 256, 48, F32, False)])

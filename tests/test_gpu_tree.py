@@ -10,6 +10,7 @@ import attn_harness as AH
 import gdn_inputs as gi
 import harness as H
 from oracle import attn_oracle as ao
+from test_gpu_debug_checks import _debug_library
 
 pytestmark = pytest.mark.gpu
 
@@ -123,6 +124,70 @@ def test_branches_equal_chains_of_their_own_and_commit():
     assert nxt.cpu().tolist() == [int(ss[0, 4]), int(inp["slots"][1])]
 
 
+SHAPES = {
+    "full binary": [-1] + [(j - 1) // 2 for j in range(1, 15)],           # states of three depths wait at once
+    "full binary, two roots": [-1, -1] + [(j - 2) // 2 for j in range(2, 16)],
+    "star": [-1] * 16,
+    "one root, 15 leaves": [-1] + [0] * 15,
+    "comb": [-1, 0, 0, 1, 1, 3, 3, 5, 5, 7, 7, 9, 9, 11, 11, 13],
+    "comb, teeth first": [-1, 0, 0, 2, 2, 4, 4, 6, 6, 8, 8, 10, 10, 12, 12, 14],
+    "chain": list(range(-1, 15)),
+    "forest": [-1, 0, 1, -1, 3, 3, -1, 6, 7, 8, 8, 6, -1, 12, 2, 13],
+}
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("d,W,dtype", [(128, 4, gi.BF16), (32, 0, gi.F32)])
+def test_tree_shapes_against_the_oracle(shape, d, W, dtype):
+    """Trees that branch at every node, at none, at the root only, to one side: each node starts from its own parent's
+    state and window."""
+    par = np.array([SHAPES[shape]], np.int32)
+    k = par.shape[1]
+    g = dataclasses.replace(gi.GEOM_QWEN, n_k_heads=1, n_v_heads=2, d_k=d, d_v=d, n_slots=k + 2, max_draft=k, conv_ring=32,
+                            conv_width=W, l2norm_qk=W > 0, dtype_in=dtype, dtype_out=dtype)
+    inp = gi.verify_inputs(seed=870 + d, geom=g, batch=1, k=k)
+    ss = _snap_slots(g, inp["slots"], k)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pool, o = _run(g, inp, par, ss, k, err)
+    assert int(err.item()) == 0
+    s = inp["slots"][0]
+    o_r, st_r, h_r, depth = ao.verify_tree(g, inp["state"][s], inp["hist"][s], inp["x"][0], inp["a"][0], inp["b"][0],
+                                           inp["conv_w"], par[0])
+    assert H.relerr(H.f64(o[0]), o_r) <= H.tol_for(g)
+    hist, pos = H.read_hist(g, pool), H.positions(pool)
+    for j in range(k):
+        sj = int(ss[0, j])
+        assert H.relerr(pool.state[sj].cpu().numpy(), st_r[j]) <= H.tol_for(g), j
+        if W:
+            assert np.array_equal(hist[sj], h_r[j].astype(np.float32)), j
+            assert pos[sj] == int(inp["pos"][s]) + depth[j]
+
+
+def test_missing_slots_in_a_branching_tree():
+    """A node without a slot that has two subtrees: its own output comes, neither subtree is touched, the walk goes on
+    with the others."""
+    m = AH.gdn()
+    par = np.array([[-1, 0, 0, 1, 1, 2, 2, 3, 4]], np.int32)
+    k = par.shape[1]
+    g = dataclasses.replace(gi.GEOM_QWEN, n_k_heads=1, n_v_heads=2, n_slots=k + 2, max_draft=k, conv_ring=16)
+    inp = gi.verify_inputs(seed=880, geom=g, batch=1, k=k)
+    ss = _snap_slots(g, inp["slots"], k)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good, og = _run(g, inp, par, ss, k, err)
+    bad = ss.copy()
+    bad[0, 1] = -1
+    pool, o = _run(g, inp, par, bad, k, err)
+    before = H.make_pool(g, inp["state"], inp["hist"], inp["pos"])
+    assert int(err.item()) == m.DEV_BAD_SLOT
+    for j in range(k):
+        s = int(ss[0, j])
+        if j in (1, 3, 4, 7, 8):
+            assert torch.equal(pool.state[s], before.state[s])
+            assert torch.equal(o[0, j], og[0, j]) if j == 1 else torch.isnan(o[0, j].float()).all()
+        else:
+            assert torch.equal(pool.state[s], good.state[s]) and torch.equal(o[0, j], og[0, j])
+
+
 def test_refused_rows_and_snapshots():
     m = AH.gdn()
     k, B = 4, 3
@@ -177,6 +242,27 @@ def test_refused_rows_and_snapshots():
     assert torch.equal(pool.state[int(ss[1, 2])], before.state[int(ss[1, 2])])
     assert torch.equal(pool.state[int(ss[1, 1])], before.state[int(ss[1, 1])])
     assert torch.equal(pool.state[int(ss[1, 3])], good.state[int(ss[1, 3])])
+
+
+def test_debug_library_reports_slots_used_twice():
+    """The debug build checks rows' and snapshots' slots before the kernel; entries past a row's count are not used."""
+    m = AH.gdn()
+    g = dataclasses.replace(gi.GEOM_QWEN, n_k_heads=1, n_v_heads=2, n_slots=8)
+    geom, dt = H.to_geom(g), H.in_dtype(g)
+    inp = gi.verify_inputs(seed=890, geom=g, batch=2, k=2)
+    pool = m.SlotPool.zeros(geom)
+    args = [H.dev(inp[n][:, :2], dt) for n in ("x", "a", "b")] + [H.dev(inp["conv_w"]), H.dev(np.array([0, 1], np.int32))]
+    par = H.dev(np.array([[-1, -1], [-1, 0]], np.int32))
+    o = torch.empty(2, 2, 2, 128, dtype=dt, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with _debug_library(m):
+        for ss, k_row, want in (([[2, 3], [4, 5]], None, 0), ([[2, 3], [4, 0]], None, 7), ([[2, 3], [4, 0]], [2, 1], 0),
+                                ([[2, 3], [3, 5]], [2, 1], 7)):
+            err.zero_()
+            m.verify_tree_slots(geom, pool, *args, par, H.dev(np.array(ss, np.int32)), o, dev_err=err,
+                                k_row=None if k_row is None else H.dev(np.array(k_row, np.int32)))
+            torch.cuda.synchronize()
+            assert int(err.item()) == want, (ss, k_row)
 
 
 def test_graph_replays_match_eager():
