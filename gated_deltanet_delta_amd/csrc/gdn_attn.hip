@@ -415,12 +415,12 @@ size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nod
 template <int D, bool BF16>
 static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
   const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, BF16 ? kFlashRows : kGenRows);
-  if (tiles * a.Hk > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
   if constexpr (BF16) {
     if (a.nodes > 0) return launch_flash_tree(a, s);
     const int e = launch_flash_prefill(a, tiles, s);
     if (e != 0) return e;
   } else {
+    if (!grid_fits(tiles, kGenThreads)) return static_cast<int>(hipErrorInvalidValue);
     const dim3 grid(static_cast<unsigned>(tiles), a.Hk, a.n_split);
     const size_t lds = 2 * GenShape<D>::TILE_BYTES + 4 * kGenKeys * 16 * sizeof(float) + 16;
     if (a.nodes > 0) hipLaunchKernelGGL((attn_f32_kernel<D, true>), grid, dim3(kGenThreads), lds, s, a);

@@ -2,9 +2,9 @@
 // gdn_attn.hip): 32x32x16 matrix instructions on key tiles that the waves of a
 // workgroup share through LDS.
 //
-// A wave owns 32 rows.  S^T = K Q^T takes K as the A operand from
-// LDS and Q^T from registers; lane l then holds row l % 32 and keys 8 (i / 4) +
-// 4 (l / 32) + i % 4 of a block of 32.  O^T = V^T P^T contracts 16 keys per
+// A wave owns 32 rows.  S^T = K Q^T takes K as the A operand from LDS and Q^T
+// from registers; lane l then holds row l % 32 and keys 8 (i / 4) + 4 (l / 32) +
+// i % 4 of a block of 32.  O^T = V^T P^T contracts 16 keys per
 // instruction: lane l's eight weights of one instruction are its accumulators
 // 8 ks .. 8 ks + 7 as they are, and V^T's operand is read out of the V tile in
 // the same key order with transposing LDS reads (ds_read_b64_tr_b16).
@@ -15,6 +15,17 @@
 // both kinds of reads hit all banks: K reads take one chunk of 16 consecutive
 // rows (chunk ^ row % 16), transposing reads four chunks of four consecutive
 // rows (chunk ^ 4 (row % 4)).
+//
+// What bounds it.  Prompts: the matrix instructions and the exponentials, sums
+// and conversions between them, which a wave does in turn; eight waves of one
+// workgroup (two per SIMD) overlap them in part.  24 heads on 4, d 256, one
+// prompt of 8192: 790 us, 1.04 PFLOP/s, where a large library product reaches
+// 1.6; ragged prompts behind prefixes of up to 20011 tokens, 32 heads on 8, d 128:
+// 728 us, 0.97 PFLOP/s.  Rows per wave: 64 (four waves, one per SIMD) took 1452 us
+// on the second, for want of a second wave to overlap with, and at d 256 do not
+// fit the registers.  Two groups of waves that alternate products and weights
+// between barriers: 995 and 1166 us against 785 and 896 then.  Trees: the bytes
+// of K and V (below).
 #include "gdn_attn_device.h"
 
 namespace gdn {
@@ -28,9 +39,9 @@ constexpr int kSchedMfma = 0x8, kSchedLds = 0x100;  // instruction classes of sc
 
 // 16 bytes per lane from memory to LDS at `lds` + 16 lane (lds: a byte address,
 // the same in every lane).  Written out because the compiler, which cannot
-// tell the two halves of the double buffer apart, would wait for these loads
+// tell the buffers apart, would wait for these loads
 // before every LDS read.  There is no register to return to; the readers are
-// ordered by tile_ready().
+// ordered by wait_tiles() and a barrier.
 __device__ __forceinline__ void load_lds16(const void* g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
@@ -39,8 +50,7 @@ __device__ __forceinline__ void load_lds16(const char* base, uint32_t off, uint3
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
-// All but this wave's newest LEFT loads have landed; then every wave's have,
-// and every wave is done with what it read before.  The wait is the builtin,
+// All but this wave's newest LEFT loads have landed.  The wait is the builtin,
 // which the compiler takes into account: it then adds no wait of its own, among
 // a tile's products, for loads issued before.
 template <int LEFT>
@@ -48,12 +58,6 @@ __device__ __forceinline__ void wait_loads() {
   static_assert(LEFT >= 0 && LEFT < 64, "vmcnt has six bits");
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | 0x0070);  // vmcnt LEFT, lgkmcnt 0
-  asm volatile("" ::: "memory");
-}
-template <int LEFT>
-__device__ __forceinline__ void tile_ready() {
-  wait_loads<LEFT>();
-  __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 // One 32-bit word per lane from memory to LDS at `lds` + 4 lane.
@@ -617,8 +621,15 @@ __host__ __device__ inline size_t tree_meta_offset(const TreeSplit& t, int D) {
 
 // 32-key tiles in four buffers; waves that have no rows only move tiles.  With
 // few rows a call is bound by memory, and what reaches its rate is many waves
-// with many loads in flight: 256 CUs x 8 waves, 64 - 96 KB per CU.
-constexpr int kTreeKeys = 32, kUnitCost = 4;
+// with many loads in flight: 256 CUs x 8 waves, 64 - 96 KB per CU.  Between two
+// units a workgroup's loads run dry once, so a unit counts as its tiles and
+// kUnitCost more where the line is cut into shares: 64 ragged rows (below) 209 us
+// with 0, 188 with 2, 174 with 4, 153 with 8, 151 with 12, 154 with 16, 161 with 32.
+// 24 heads on 4, d 256: 4 rows of one node at 8K 47 us (134 MB, 2.9 TB/s; the
+// join of the shares 6 of them); 4 rows of 16 nodes at 80 - 120K 356 us (1.64 GB,
+// 4.6 TB/s, the rate of a large copy).  32 heads on 8, d 128, 64 rows of 8 nodes
+// up to 16K, 16-token pages: 151 us (0.67 GB, 4.4 TB/s).
+constexpr int kTreeKeys = 32, kUnitCost = 12;
 template <int D, int RW>
 using TreeFlash = Flash<D, RW, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
 
@@ -821,7 +832,7 @@ static void launch_tree_rows(const AttnArgs& a, const TreeSplit& t, hipStream_t 
 template <int D>
 static int launch_flash_tree_t(const AttnArgs& a, hipStream_t s) {
   const TreeSplit t = tree_split(a.Hk, a.G, D, a.nodes);
-  if (static_cast<int64_t>(a.n_seqs) * t.units_per_row > INT32_MAX) return static_cast<int>(hipErrorInvalidValue);
+  if (!grid_fits(static_cast<int64_t>(a.n_seqs) * t.units_per_row, 256)) return static_cast<int>(hipErrorInvalidValue);
   if (t.rows_per_unit == 32) launch_tree_rows<D, 1>(a, t, s);
   else if (t.rows_per_unit == 64) launch_tree_rows<D, 2>(a, t, s);
   else launch_tree_rows<D, 4>(a, t, s);
@@ -845,6 +856,7 @@ int launch_flash_tree(const AttnArgs& a, void* stream) {
 template <int D>
 static int launch_flash_prefill_t(const AttnArgs& a, int64_t tiles, hipStream_t s) {
   typedef PromptFlash<D> F;
+  if (!grid_fits(tiles * a.Hk, F::THREADS)) return static_cast<int>(hipErrorInvalidValue);
   hipLaunchKernelGGL((flash_prefill_kernel<D>), dim3(static_cast<unsigned>(tiles * a.Hk), a.n_split), dim3(F::THREADS), F::LDS,
                      s, a);
   return static_cast<int>(hipGetLastError());

@@ -155,8 +155,11 @@ int launch_commit_slots(const StepArgs& a, void* stream);
 int launch_verify_tree(const StepArgs& a, bool bf16, void* stream);
 int launch_kv_plan(const KvPlanArgs& a, void* stream);
 int launch_kv_write(const KvWriteArgs& a, void* stream);
-// Splits of the key axis of an attention call (1: none), by its row tiles
-// alone, since only the device knows the lengths; bf16 trees are split on the device.
+// A launch has fewer than 2^32 threads along x.
+inline bool grid_fits(int64_t workgroups, int threads) { return workgroups <= 0xffffffffll / threads; }
+// Splits of the key axis of an attention call (1: none), by its row tiles and
+// `keys`, the most keys that a row can have, since only the device knows the
+// lengths; bf16 trees are split on the device.
 int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16, int64_t keys);
 // Workspace of a call: tokens = rows of q (trees: batch x nodes).
 size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16);
