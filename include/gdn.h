@@ -19,7 +19,9 @@
  * (WY/UT-transform) prefill over variable-length sequences, and a k-draft
  * speculative verify that writes a state snapshot after every draft so that
  * rollback is a copy ("Forge: how I wrote my own inference engine and beat
- * llama.cpp", entry of 27 August).
+ * llama.cpp", entry of 27 August).  The verify also runs over trees of drafts.
+ * For the attention layers of a hybrid stack, at the end of this file: a paged
+ * KV cache and attention over it, for prompts and for trees of drafts.
  *
  * Conventions for every call below
  * --------------------------------
