@@ -6,7 +6,7 @@
 
 #include "gdn.h"
 #include "gdn_host.h"
-#include "gdn_internal.h"
+#include "gdn_ops.h"
 
 namespace {
 
@@ -313,7 +313,7 @@ gdn_status gdn_verify_tree_slots(const gdn_geometry* g, float* state, float* con
   GDN_NEED_PTR4(parent, "parent");
   GDN_NEED_PTR4(snap_slot, "snap_slot");
   GDN_NEED_PTR(o, "o");
-  gdn::StepArgs a{};
+  gdn::TreeArgs a{};
   a.Hk = g->n_k_heads;
   a.Hv = g->n_v_heads;
   a.D = g->d_k;

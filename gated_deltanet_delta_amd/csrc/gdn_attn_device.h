@@ -3,7 +3,7 @@
 #pragma once
 
 #include "gdn_device.h"
-#include "gdn_internal.h"
+#include "gdn_ops.h"
 
 namespace gdn {
 

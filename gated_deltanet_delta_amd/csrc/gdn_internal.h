@@ -55,7 +55,6 @@ struct StepArgs {
   float* snap;              // verify: out; rollback: in
   const int32_t* snap_slot; // verify into pool slots: [batch][k] slots receiving the snapshots (else null)
   const int32_t* k_row;     // verify into pool slots, commit: drafts of each row (null: k for every row)
-  const int32_t* parent;    // tree verify: [batch][k] parent node of each draft, -1 for the committed state
   int32_t* next_slot;       // slot commit: out
   int32_t* dev_err;
   int32_t batch, k;
@@ -90,43 +89,6 @@ struct PrefillArgs {
   int32_t last_seg;        // 1 on the launch that writes the ring positions
 };
 
-// Arguments of the paged-cache kernels (gdn_kv.hip).
-struct KvPlanArgs {
-  const int32_t *kv_len, *new_len, *n_free;
-  int32_t *free_pages, *block_table, *cu_new, *slot_map, *position, *kv_len_out, *n_free_out, *dev_err;
-  int32_t batch, max_tokens, page, n_pages, max_pages;
-};
-struct KvWriteArgs {
-  const void *k, *v;
-  void *k_cache, *v_cache;
-  const int32_t* slot_map;
-  int32_t* dev_err;
-  int64_t k_stride, v_stride;  // bytes between tokens
-  int32_t n_tokens, heads, row_bytes, page, n_pages;  // row_bytes: one head's D elements
-};
-constexpr int kKvPlanMaxBatch = 4096;
-
-// Arguments of the attention kernels (gdn_attn.hip), prefill and tree.  Rows
-// of a sequence are its (token, query head of one KV head's group) pairs, token
-// major; keys are the sequence's cached tokens followed by its own.
-struct AttnArgs {
-  const void *q, *k, *v, *k_cache, *v_cache;
-  int64_t q_stride, k_stride, v_stride;  // elements between tokens
-  const int32_t* block_table;
-  const int32_t* ctx_len;     // null: no cached tokens
-  const int32_t* cu_seqlens;  // prefill
-  const int32_t* parent;      // tree
-  const int32_t* n_row;       // tree, may be null
-  void* o;
-  float* part;                // partial outputs [token][H_q][n_split][D], then (max, sum) [token][H_q][n_split][2]
-  int32_t* dev_err;
-  int32_t n_seqs, n_tokens;   // tree: batch, batch * n
-  int32_t nodes;              // tree: n; prefill: 0
-  int32_t Hq, Hk, G, D, page, n_pages, max_pages;
-  int32_t n_split;
-  float scale_log2;           // scale * log2(e)
-};
-
 // Byte offsets of the prefill workspace.  Its size does not depend on the
 // number of tokens: chunks pass from producer to chain workgroups through a
 // ring of ring_slots chunk slots.
@@ -152,22 +114,6 @@ int launch_verify(const StepArgs& a, bool bf16, void* stream);
 int launch_conv_step(const StepArgs& a, bool bf16, void* stream);
 int launch_rollback(const StepArgs& a, void* stream);
 int launch_commit_slots(const StepArgs& a, void* stream);
-int launch_verify_tree(const StepArgs& a, bool bf16, void* stream);
-int launch_kv_plan(const KvPlanArgs& a, void* stream);
-int launch_kv_write(const KvWriteArgs& a, void* stream);
-// A launch has fewer than 2^32 threads along x.
-inline bool grid_fits(int64_t workgroups, int threads) { return workgroups <= 0xffffffffll / threads; }
-// Splits of the key axis of an attention call (1: none), by its row tiles and
-// `keys`, the most keys that a row can have, since only the device knows the
-// lengths; bf16 trees are split on the device.
-int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16, int64_t keys);
-// Workspace of a call: tokens = rows of q (trees: batch x nodes).
-size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16);
-int launch_attn(const AttnArgs& a, bool bf16, void* stream);
-constexpr int kFlashRows = 256;  // rows of a workgroup of the bf16 prompt attention
-int launch_flash_prefill(const AttnArgs& a, int64_t tiles, void* stream);
-int launch_flash_tree(const AttnArgs& a, void* stream);
-size_t flash_tree_part_bytes(int64_t batch, int Hk, int G, int D, int nodes);
 // Debug builds: one small kernel reporting GDN_DEV_DUP_SLOT to *dev_err when
 // two of a call's slot ids are equal: a[0..na), then, for rows i < nb, the
 // ids b[i kb + j] for j < kb, or j < k_row[i] when k_row is given (rows whose

@@ -17,7 +17,7 @@
 // d 256, bf16 (268 MB read and written) 53 us, 5.1 TB/s, above the rate of a
 // large copy; 4 tokens 2.2 us.
 #include "gdn_device.h"
-#include "gdn_internal.h"
+#include "gdn_ops.h"
 
 namespace gdn {
 

@@ -21,7 +21,7 @@
 // Plain stores 177 us; four waves per SIMD (registers spill) 199 us.  4 rows of
 // 4 nodes, from HBM: 16.8 us.
 #include "gdn_device.h"
-#include "gdn_internal.h"
+#include "gdn_ops.h"
 
 namespace gdn {
 
@@ -33,7 +33,7 @@ __device__ __forceinline__ float tree_dot4(f32x4_t a, float4 b) {
 }
 
 template <int D, bool BF16, int W>
-__global__ __launch_bounds__((StepShape<D, true>::THREADS)) void tree_kernel(StepArgs A) {
+__global__ __launch_bounds__((StepShape<D, true>::THREADS)) void tree_kernel(TreeArgs A) {
   using Sh = StepShape<D, true>;
   constexpr int LPR = Sh::LPR;
   constexpr int NP = Sh::NP;
@@ -299,7 +299,7 @@ __global__ __launch_bounds__((StepShape<D, true>::THREADS)) void tree_kernel(Ste
 }
 
 template <int D, bool BF16>
-static int launch_tree_t(const StepArgs& a, hipStream_t s) {
+static int launch_tree_t(const TreeArgs& a, hipStream_t s) {
   using Sh = StepShape<D, true>;
   dim3 grid(a.Hv * Sh::WG_PER_HEAD, a.batch);
   if (a.W == 4) hipLaunchKernelGGL((tree_kernel<D, BF16, 4>), grid, dim3(Sh::THREADS), 0, s, a);
@@ -308,7 +308,7 @@ static int launch_tree_t(const StepArgs& a, hipStream_t s) {
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_verify_tree(const StepArgs& a, bool bf16, void* stream) {
+int launch_verify_tree(const TreeArgs& a, bool bf16, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   switch (a.D) {
     case 16: return bf16 ? launch_tree_t<16, true>(a, s) : launch_tree_t<16, false>(a, s);
