@@ -194,8 +194,13 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream(torch.cuda.current_device())
+        return ctypes.c_void_p(_current_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+# the current stream's handle without a Stream object around it (0.1 us instead of 1.3), where torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _need(t: Optional[torch.Tensor], name: str, shape, dtype, optional=False):
