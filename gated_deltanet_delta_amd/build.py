@@ -23,7 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 LIB_DEBUG = os.path.join(PKG, "libgdn_debug.so")
 
-HIP_SOURCES = ["gdn_step.hip", "gdn_prefill.hip", "gdn_tree.hip", "gdn_kv.hip", "gdn_attn.hip", "gdn_flash.hip"]
+HIP_SOURCES = ["gdn_step.hip", "gdn_prefill.hip", "gdn_tree.hip", "gdn_kv.hip", "gdn_attn.hip", "gdn_attn_bf16.hip"]
 HOST_SOURCES = ["gdn_api.cpp", "gdn_attn_api.cpp"]
 
 HIPCC_FLAGS = [
@@ -36,7 +36,7 @@ HIPCC_FLAGS = [
 ]
 # MFMA accumulators in VGPRs: the chained products feed them straight to VALU
 # code and the next MFMA, so AGPR<->VGPR copies would only add instructions.  Not
-# for gdn_flash.hip, whose kernels of one wave per SIMD need both register files.
+# for gdn_attn_bf16.hip, whose kernels of one wave per SIMD need both register files.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Wno-unused-parameter"]
 
@@ -70,7 +70,7 @@ def build(verbose: bool = False) -> str:
     for src in HIP_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
-        form = [] if src == "gdn_flash.hip" else VGPR_FORM
+        form = [] if src == "gdn_attn_bf16.hip" else VGPR_FORM
         jobs.append([hipcc, *HIPCC_FLAGS, *form, *incs, "-c", os.path.join(CSRC, src), "-o", obj])
     debug_objs = list(objs)
     for src in HOST_SOURCES:

@@ -47,7 +47,7 @@ __device__ __forceinline__ float quarter_max(float x) {
 // operands are 16 bytes of LDS: instruction 4 s + i of the logits contracts
 // elements 16 s + 4 g + i of K and Q; instruction i of half h of the keys
 // contracts keys 16 h + 4 g + i (where the weights are), and row c of V^T's block
-// dt stands for d = 64 (dt / 4) + 4 c + dt % 4.  (bf16: gdn_flash.hip.)
+// dt stands for d = 64 (dt / 4) + 4 c + dt % 4.  (bf16: gdn_attn_bf16.hip.)
 //
 // Bound by the matrix instructions and, as much again, the vector instructions of
 // softmax, addresses and copies between them: 1024 tokens of 8 heads on 2, d 64,
@@ -399,7 +399,7 @@ int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
 // 130 workgroups, 64 us in 260).
 int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16, int64_t keys) {
   if (bf16 && nodes > 0) return 1;
-  const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kFlashRows : kGenRows) * Hk;
+  const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kPromptRows : kGenRows) * Hk;
   if (wgs <= 0) return 1;
   const int64_t want = !bf16 ? 1024 / wgs : (D == 64 ? (255 + wgs) / wgs : 256 / wgs);
   const int64_t least = bf16 ? 128 : kGenKeys, parts = keys / least + (keys % least != 0);
@@ -407,17 +407,17 @@ int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, boo
 }
 
 size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16) {
-  if (bf16 && nodes > 0) return flash_tree_part_bytes(n_seqs, Hk, G, D, nodes);
+  if (bf16 && nodes > 0) return tree_bf16_part_bytes(n_seqs, Hk, G, D, nodes);
   const int n_split = attn_splits(tokens, n_seqs, Hk, G, D, nodes, bf16, INT64_MAX);
   return n_split <= 1 ? 0 : static_cast<size_t>(tokens) * Hk * G * n_split * (D + 2) * sizeof(float);
 }
 
 template <int D, bool BF16>
 static int launch_attn_t(const AttnArgs& a, hipStream_t s) {
-  const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, BF16 ? kFlashRows : kGenRows);
+  const int64_t tiles = row_tiles(a.n_tokens, a.n_seqs, a.G, a.nodes, BF16 ? kPromptRows : kGenRows);
   if constexpr (BF16) {
-    if (a.nodes > 0) return launch_flash_tree(a, s);
-    const int e = launch_flash_prefill(a, tiles, s);
+    if (a.nodes > 0) return launch_tree_bf16(a, s);
+    const int e = launch_prompt_bf16(a, tiles, s);
     if (e != 0) return e;
   } else {
     if (!grid_fits(tiles, kGenThreads)) return static_cast<int>(hipErrorInvalidValue);

@@ -86,7 +86,7 @@ __device__ __forceinline__ float half_sum(float x) {
 // NW waves move KT-key tiles through NST buffers; the first RW of them compute,
 // 32 rows each.
 template <int D, int RW, int NW, int KT, int NST, bool TREE>
-struct Flash {
+struct Tiles {
   static constexpr int THREADS = 64 * NW, BM = 32 * RW;
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int TILE = KT * ROW_BYTES;            // K or V of a tile
@@ -128,7 +128,7 @@ struct Flash {
   f32x16_t O[NT];
   float m, l;            // running maximum (of unscaled logits), this lane's part of the sum
 
-  __device__ Flash(const AttnArgs& a, char* smem) : A(a), lds(smem) {
+  __device__ Tiles(const AttnArgs& a, char* smem) : A(a), lds(smem) {
     lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -504,7 +504,7 @@ struct Flash {
 template <int D>
 constexpr int prompt_keys() { return D == 256 ? 32 : 64; }
 template <int D>
-using PromptFlash = Flash<D, kFlashRows / 32, kFlashRows / 32, prompt_keys<D>(), 4, false>;
+using PromptTiles = Tiles<D, kPromptRows / 32, kPromptRows / 32, prompt_keys<D>(), 4, false>;
 
 // Sum over the wave's lanes, in every lane.
 __device__ __forceinline__ int32_t wave_sum(int32_t v) {
@@ -565,8 +565,8 @@ __device__ bool ranked_block(const AttnArgs& A, int64_t rank, int* seq, int64_t*
 
 // One workgroup per (block of rows, KV head, split of the key axis).
 template <int D>
-__global__ __launch_bounds__(PromptFlash<D>::THREADS, 2) void flash_prefill_kernel(AttnArgs A) {
-  typedef PromptFlash<D> F;
+__global__ __launch_bounds__(PromptTiles<D>::THREADS, 2) void attn_prompt_kernel(AttnArgs A) {
+  typedef PromptTiles<D> F;
   extern __shared__ __align__(1024) char smem[];
   F f(A, smem);
   int s;
@@ -634,11 +634,11 @@ __host__ __device__ inline size_t tree_meta_offset(const TreeSplit& t, int D) {
 // up to 16K, 16-token pages: 151 us (0.67 GB, 4.4 TB/s).
 constexpr int kTreeKeys = 32, kUnitCost = 12;
 template <int D, int RW>
-using TreeFlash = Flash<D, RW, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
+using TreeTiles = Tiles<D, RW, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
 
 template <int D, int RW>
-__global__ __launch_bounds__((TreeFlash<D, RW>::THREADS), 2) void flash_tree_kernel(AttnArgs A, TreeSplit ts) {
-  typedef TreeFlash<D, RW> F;
+__global__ __launch_bounds__((TreeTiles<D, RW>::THREADS), 2) void attn_tree_kernel(AttnArgs A, TreeSplit ts) {
+  typedef TreeTiles<D, RW> F;
   extern __shared__ __align__(1024) char smem[];
   F f(A, smem);
   const int lane = threadIdx.x & 63;
@@ -821,19 +821,19 @@ TreeSplit tree_split(int Hk, int G, int D, int nodes) {
 
 }  // namespace
 
-size_t flash_tree_part_bytes(int64_t batch, int Hk, int G, int D, int nodes) {
+size_t tree_bf16_part_bytes(int64_t batch, int Hk, int G, int D, int nodes) {
   const TreeSplit t = tree_split(Hk, G, D, nodes);
   return tree_meta_offset(t, D) * sizeof(float) + static_cast<size_t>(batch) * t.units_per_row * sizeof(int2);
 }
 
 template <int D, int RW>
 static void launch_tree_rows(const AttnArgs& a, const TreeSplit& t, hipStream_t s) {
-  typedef TreeFlash<D, RW> F;
-  hipLaunchKernelGGL((flash_tree_kernel<D, RW>), dim3(t.workgroups), dim3(F::THREADS), F::LDS, s, a, t);
+  typedef TreeTiles<D, RW> F;
+  hipLaunchKernelGGL((attn_tree_kernel<D, RW>), dim3(t.workgroups), dim3(F::THREADS), F::LDS, s, a, t);
 }
 
 template <int D>
-static int launch_flash_tree_t(const AttnArgs& a, hipStream_t s) {
+static int launch_tree_bf16_t(const AttnArgs& a, hipStream_t s) {
   const TreeSplit t = tree_split(a.Hk, a.G, D, a.nodes);
   if (!grid_fits(static_cast<int64_t>(a.n_seqs) * t.units_per_row, 256)) return static_cast<int>(hipErrorInvalidValue);
   if (t.rows_per_unit == 32) launch_tree_rows<D, 1>(a, t, s);
@@ -846,31 +846,31 @@ static int launch_flash_tree_t(const AttnArgs& a, hipStream_t s) {
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_flash_tree(const AttnArgs& a, void* stream) {
+int launch_tree_bf16(const AttnArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   switch (a.D) {
-    case 64: return launch_flash_tree_t<64>(a, s);
-    case 128: return launch_flash_tree_t<128>(a, s);
-    case 256: return launch_flash_tree_t<256>(a, s);
+    case 64: return launch_tree_bf16_t<64>(a, s);
+    case 128: return launch_tree_bf16_t<128>(a, s);
+    case 256: return launch_tree_bf16_t<256>(a, s);
     default: return static_cast<int>(hipErrorInvalidValue);
   }
 }
 
 template <int D>
-static int launch_flash_prefill_t(const AttnArgs& a, int64_t tiles, hipStream_t s) {
-  typedef PromptFlash<D> F;
+static int launch_prompt_bf16_t(const AttnArgs& a, int64_t tiles, hipStream_t s) {
+  typedef PromptTiles<D> F;
   if (!grid_fits(tiles * a.Hk, F::THREADS)) return static_cast<int>(hipErrorInvalidValue);
-  hipLaunchKernelGGL((flash_prefill_kernel<D>), dim3(static_cast<unsigned>(tiles * a.Hk), a.n_split), dim3(F::THREADS), F::LDS,
+  hipLaunchKernelGGL((attn_prompt_kernel<D>), dim3(static_cast<unsigned>(tiles * a.Hk), a.n_split), dim3(F::THREADS), F::LDS,
                      s, a);
   return static_cast<int>(hipGetLastError());
 }
 
-int launch_flash_prefill(const AttnArgs& a, int64_t tiles, void* stream) {
+int launch_prompt_bf16(const AttnArgs& a, int64_t tiles, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   switch (a.D) {
-    case 64: return launch_flash_prefill_t<64>(a, tiles, s);
-    case 128: return launch_flash_prefill_t<128>(a, tiles, s);
-    case 256: return launch_flash_prefill_t<256>(a, tiles, s);
+    case 64: return launch_prompt_bf16_t<64>(a, tiles, s);
+    case 128: return launch_prompt_bf16_t<128>(a, tiles, s);
+    case 256: return launch_prompt_bf16_t<256>(a, tiles, s);
     default: return static_cast<int>(hipErrorInvalidValue);
   }
 }

@@ -1,4 +1,4 @@
-// Device helpers shared by the attention kernels (gdn_attn.hip, gdn_flash.hip):
+// Device helpers shared by the attention kernels (gdn_attn.hip, gdn_attn_bf16.hip):
 // the sequences of a call, the rows of its keys, and partial results.
 #pragma once
 

@@ -1,5 +1,5 @@
 // Arguments and launchers of the attention layers' kernels (gdn_kv.hip,
-// gdn_attn.hip, gdn_flash.hip) and of the delta rule over trees (gdn_tree.hip).
+// gdn_attn.hip, gdn_attn_bf16.hip) and of the delta rule over trees (gdn_tree.hip).
 #pragma once
 
 #include "gdn_internal.h"
@@ -61,9 +61,9 @@ int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, boo
 // Workspace of a call: tokens = rows of q (trees: batch x nodes).
 size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16);
 int launch_attn(const AttnArgs& a, bool bf16, void* stream);
-constexpr int kFlashRows = 256;  // rows of a workgroup of the bf16 prompt attention
-int launch_flash_prefill(const AttnArgs& a, int64_t tiles, void* stream);
-int launch_flash_tree(const AttnArgs& a, void* stream);
-size_t flash_tree_part_bytes(int64_t batch, int Hk, int G, int D, int nodes);
+constexpr int kPromptRows = 256;  // rows of a workgroup of the bf16 prompt attention
+int launch_prompt_bf16(const AttnArgs& a, int64_t tiles, void* stream);
+int launch_tree_bf16(const AttnArgs& a, void* stream);
+size_t tree_bf16_part_bytes(int64_t batch, int Hk, int G, int D, int nodes);
 
 }  // namespace gdn
