@@ -354,10 +354,11 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
   const uint64_t on = __ballot(!(mz == -INFINITY && lz == 0.f));
   f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-  for (int z = g; z < A.n_split; z += NG) {
+  for (int z0 = 0; z0 < A.n_split; z0 += NG) {  // the same turns in every lane: the weights come from other lanes
+    const int z = min(z0 + g, A.n_split - 1);
     const f32x4_t x = load4(sums + static_cast<size_t>(z) * D);
     const float w = __shfl(weight, z, kWave);
-    const bool seen = (on >> z) & 1ull;
+    const bool seen = z0 + g < A.n_split && ((on >> z) & 1ull);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] += seen ? w * x[e] : 0.f;
   }

@@ -215,6 +215,20 @@ def test_prefill_few_rows_behind_long_prefixes(D, dtype):
     _check_sequences(pg, parts, cu, ctx, o, D ** -0.5, dtype, "sequence")
 
 
+@pytest.mark.parametrize("S,cut,D,dtype", [(60, 17, 64, F32), (20, 51, 64, F32), (31, 33, 128, F32), (19, 53, 128, F32),
+                                           (31, 33, 256, F32), (5, 51, 128, BF16), (14, 19, 64, BF16), (7, 36, 256, BF16)])
+def test_prefill_odd_numbers_of_parts(S, cut, D, dtype):
+    """Single tokens, one behind a prefix that fills `cut` parts of the key axis, as many as a call of this many
+    sequences makes, mostly no multiple of the parts that a turn of the join takes."""
+    new, ctx = [1] * S, [128 * cut - 1] + [5] * (S - 1)
+    m, geom, pg, parts, dev, cu, o = _prefill_case(540 + S + D, new, ctx, 1, 1, D, 16, dtype)
+    err = _err()
+    _run_prefill(m, geom, pg, dev, cu, ctx, o, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    _check_sequences(pg, parts, cu, ctx, o, D ** -0.5, dtype, "sequence")
+
+
 def test_prefill_refused_sequence_among_many():
     """Blocks are ordered by their keys across sequences: a refused one leaves the others right, wherever it stands."""
     new, ctx = [40, 90, 40, 7, 200], [0, 64, 0, 300, 16]
