@@ -64,6 +64,8 @@ PREFILL = [
     ([1, 0, 33, 70], [3, 0, 64, 0], 2, 3, 64, 16, F32, True, 5),
     ([40, 1], [0, 77], 1, 2, 128, 48, F32, False, 0),
     ([35, 3], [20, 0], 2, 2, 256, 16, F32, False, 0),
+    ([5, 41], [0, 33], 1, 64, 64, 16, BF16, True, 2),
+    ([3, 9], [17, 0], 1, 64, 128, 16, F32, False, 0),
 ]
 
 
@@ -309,6 +311,8 @@ TREE = [
     ([30, 600], 5, 2, 3, 64, 16, F32, True, [2, 5]),
     ([0, 65], 1, 1, 8, 128, 16, F32, False, None),
     ([129], 9, 1, 2, 256, 16, F32, False, None),
+    ([20, 7], 64, 1, 64, 64, 16, BF16, False, [64, 33]),
+    ([31], 17, 1, 64, 128, 16, F32, True, None),
 ]
 
 
@@ -393,6 +397,32 @@ def test_tree_refused_rows():
         torch.cuda.synchronize()
         assert int(err.item()) == code, what
         others(1)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, BF16), (256, BF16), (64, F32)])
+def test_full_tables(D, dtype):
+    """Rows whose cached tokens fill their tables to the last entry, the largest length that is accepted, at lengths
+    where the page ids of 1024 keys end; one token more is refused."""
+    m = AH.gdn()
+    for c in (1024, 2048 + 16):
+        pg = AH.Paged(95, [c, 5], 1, D, 16, dtype, width_extra=0)
+        geom = m.AttnGeometry(n_q_heads=2, n_kv_heads=1, d_head=D, n_pages=pg.n_pages, max_pages=pg.width, max_tree=3,
+                              dtype=dtype)
+        rows, parts = AH.qkv(96, 6, 2, 1, D, dtype, False)
+        dev = tuple(p.cuda() for p in parts)
+        o, err = torch.full((6, 2, D), 7.0, dtype=dtype, device="cuda"), _err()
+        cu = np.array([0, 3, 6], np.int32)
+        _run_prefill(m, geom, pg, dev, cu, [c, 5], o, err)
+        tree = torch.full((2, 3, 2, D), 7.0, dtype=dtype, device="cuda")
+        par = AH.parents(97, 2, 3)
+        _run_tree(m, geom, pg, tuple(t.unflatten(0, (2, 3)) for t in dev), par, [c, 5], tree, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        _check_sequences(pg, parts, cu, [c, 5], o, D ** -0.5, dtype, "sequence")
+        _check_tree(pg, parts, par, [c, 5], tree, None, 2, D, dtype, "full table")
+        _run_prefill(m, geom, pg, dev, cu, [c + 1, 5], o, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == m.DEV_BAD_LENGTH
 
 
 def test_tree_cache_beyond_32_bit_offsets():
