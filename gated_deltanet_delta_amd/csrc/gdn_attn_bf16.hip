@@ -27,6 +27,7 @@
 // between barriers: 995 and 1166 us against 785 and 896 then.  Trees: the bytes
 // of K and V (below).
 #include "gdn_attn_device.h"
+#include "gdn_rank.h"
 
 namespace gdn {
 
@@ -516,50 +517,41 @@ __device__ __forceinline__ int32_t wave_sum(int32_t v) {
          __builtin_amdgcn_readlane(v, 48);
 }
 
-// Row block number `rank` of a batch of at most 64 sequences, in falling order
-// of the keys that blocks attend (equal ones in order of their sequences), so
-// the longest start first, whatever the order of the sequences.  Block b of a
-// sequence attends ctx + min(n, floor(((b + 1) BM - 1) / G) + 1) keys, more with
-// every b; so the number of blocks of at least `keys` keys is a sum over the
-// sequences, one per lane, and a search over `keys` finds the block.  False:
-// there are no more blocks.  Refused sequences are taken as they come, from rank 0.
+// A wave's lanes for ranked_block(), one sequence per lane.
 template <int BM>
-__device__ bool ranked_block(const AttnArgs& A, int64_t rank, int* seq, int64_t* r0) {
+struct WaveLanes {
+  typedef RowBlocks<BM> Blocks;
+  Blocks mine;
+  int lane;
+  template <class F>
+  __device__ int32_t sum(F f) const { return wave_sum(f(mine, lane)); }
+  template <class F>
+  __device__ int32_t max(F f) const {
+    int32_t v = f(mine, lane);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v = ::max(v, __shfl_xor(v, d, 64));
+    return uniform(v);
+  }
+  template <class F>
+  __device__ uint64_t ballot(F f) const { return __ballot(f(mine, lane)); }
+  template <class F>
+  __device__ int32_t at(F f, int l) const { return __builtin_amdgcn_readlane(f(mine, lane), l); }
+};
+
+// Row block number `rank` of a batch of at most 64 sequences (gdn_rank.h).
+// Refused sequences have no blocks, and are reported at rank 0.  False: there are
+// no more blocks.
+template <int BM>
+__device__ bool ranked_block_of(const AttnArgs& A, int64_t rank, int* seq, int64_t* r0) {
   const int lane = threadIdx.x & 63;
   Seq q{0, 0, 0, 0};
   if (lane < A.n_seqs) q = packed_seq(A, lane, rank == 0);
-  const int32_t blocks = static_cast<int32_t>((static_cast<int64_t>(q.n) * A.G + BM - 1) / BM);
-  const int32_t r = static_cast<int32_t>(rank);
-  if (r >= wave_sum(blocks)) return false;
-  // the sequence's first block of at least `keys` keys (blocks: none)
-  auto first = [&](int32_t keys) {
-    const int32_t need = keys - q.ctx;
-    if (need <= 1) return 0;
-    return need > q.n ? blocks : static_cast<int32_t>((static_cast<int64_t>(need - 1) * A.G) / BM);
-  };
-  // the largest number of keys that more than r blocks have at least
-  int32_t lo = 1, hi = 0x7fffffff;  // more than r blocks have lo; hi: not so many
-  {
-    int32_t most = q.n > 0 ? q.ctx + q.n : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d, 64));
-    hi = uniform(most) + 1;
-  }
-  while (hi - lo > 1) {
-    const int32_t mid = lo + (hi - lo) / 2;
-    if (wave_sum(blocks - first(mid)) > r) lo = mid;
-    else hi = mid;
-  }
-  // among the blocks of exactly lo keys, at most one per sequence
-  const int32_t b = first(lo);
-  const uint64_t on = __ballot(b < blocks && b != first(lo + 1));
-  int32_t skip = r - wave_sum(blocks - first(lo + 1));
-  uint64_t left = on;
-  for (; skip > 0 && left != 0; --skip) left &= left - 1;
-  if (left == 0) return false;  // only where cu_seqlens is no partition and the counts wrapped
-  const int s = __builtin_ctzll(left);
+  const WaveLanes<BM> lanes{RowBlocks<BM>(q.n, q.ctx, A.G), lane};
+  int s;
+  int32_t block;
+  if (!ranked_block(lanes, static_cast<int32_t>(rank), &s, &block)) return false;
   *seq = uniform(s);
-  *r0 = static_cast<int64_t>(__builtin_amdgcn_readlane(b, s)) * BM;
+  *r0 = static_cast<int64_t>(block) * BM;
   return true;
 }
 
@@ -572,7 +564,7 @@ __global__ __launch_bounds__(PromptTiles<D>::THREADS, 2) void attn_prompt_kernel
   int s;
   int64_t r0;
   if (A.n_seqs <= 64) {
-    if (!ranked_block<F::BM>(A, blockIdx.x / A.Hk, &s, &r0)) return;
+    if (!ranked_block_of<F::BM>(A, blockIdx.x / A.Hk, &s, &r0)) return;
   } else {  // there are many blocks to even out what their order does not
     const int64_t id = gridDim.x / A.Hk - 1 - blockIdx.x / A.Hk;
     s = uniform(find_seq(A, id, F::BM));

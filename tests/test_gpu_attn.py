@@ -260,6 +260,30 @@ def test_prefill_refused_sequence_among_many():
             assert (off <= 2 * AH.half_step(BF16) * (alone.float().abs() + float(parts[2].abs().max()) + 4)).all()
 
 
+# Row counts n G that end one block of 256 rows inside the heads of the last token: 0 < n G mod 256 < G.
+STRADDLE = [(3, 86), (3, 171), (5, 52), (6, 43), (6, 86), (6, 171), (7, 37), (12, 22)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,n", STRADDLE)
+def test_prefill_last_token_in_two_row_blocks(G, n, D):
+    """The last two row blocks attend the same keys: alone and behind a prefix (few rows: the key axis is split), twice
+    the same beside others, and in so many sequences that it is not split.  No row keeps what the output held."""
+    assert 0 < n * G % 256 < G
+    print(f"last token in two row blocks: G {G} n {n} D {D}", flush=True)
+    for seed, (new, ctx, Hk) in enumerate((([n], [0], 1), ([n], [700], 2), ([n, 5, n, 33, n - 1], [64, 0, 64, 130, 0], 2),
+                                           ([n] * 40, [0, 17] * 20, 4))):
+        m, geom, pg, parts, dev, cu, o = _prefill_case(900 + seed + D + G, new, ctx, Hk, G, D, 16, BF16)
+        split = m.attn_prefill_workspace_bytes(geom, sum(new), len(new)) > 0
+        assert split == (len(new) < 40)
+        o.fill_(float("nan"))
+        err = _err()
+        _run_prefill(m, geom, pg, dev, cu, ctx, o, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and torch.isfinite(o).all()
+        _check_sequences(pg, parts, cu, ctx[:5], o, D ** -0.5, BF16, f"G {G} n {n} D {D} batch {seed} sequence")
+
+
 # ---------------------------------------------------------------------------
 # trees
 # ---------------------------------------------------------------------------
