@@ -331,12 +331,8 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
     const int s = tok / A.nodes;
     if (tok - s * A.nodes >= tree_seq(A, s, false, &path).n) return;
   } else {
-    int s = 0;  // the last sequence that does not begin after the token
-    for (int base = 0; base < A.n_seqs; base += kWave) {
-      const uint64_t on = __ballot(base + lane < A.n_seqs && A.cu_seqlens[min(base + lane, A.n_seqs - 1)] <= tok);
-      if (on == 0) break;
-      s = base + 63 - __builtin_clzll(on);
-    }
+    // the last sequence that does not begin after the token
+    const int s = last_seq(A, [&](int32_t t0, int) { return t0 <= tok; });
     const Seq q = packed_seq(A, s, false);
     if (q.n == 0 || tok < q.row0 || tok >= q.row0 + q.n) return;
   }

@@ -545,7 +545,11 @@ template <int BM>
 __device__ bool ranked_block_of(const AttnArgs& A, int64_t rank, int* seq, int64_t* r0) {
   const int lane = threadIdx.x & 63;
   Seq q{0, 0, 0, 0};
-  if (lane < A.n_seqs) q = packed_seq(A, lane, rank == 0);
+  const bool in = lane < A.n_seqs;
+  if (in) q = packed_seq(A, lane, rank == 0);
+  // sequences behind one that ends before it begins are refused with it (last_seq)
+  const uint64_t back = __ballot(in && A.cu_seqlens[lane + 1] < A.cu_seqlens[lane]);
+  if (((back ^ (back - 1)) >> lane & 1ull) == 0) q.n = 0;
   const WaveLanes<BM> lanes{RowBlocks<BM>(q.n, q.ctx, A.G), lane};
   int s;
   int32_t block;

@@ -85,6 +85,26 @@ __device__ __forceinline__ Seq tree_seq(const AttnArgs& A, int s, bool report, u
   return q;
 }
 
+// Last sequence s with begins(cu_seqlens[s], s), a condition that no sequence
+// meets after one that does not, of those up to the first that ends before it
+// begins (which is refused, and so are those behind it: their bounds are in no
+// order); 0 if none meets it.  All lanes of a wave together.
+template <class F>
+__device__ __forceinline__ int last_seq(const AttnArgs& A, F begins) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int s = 0;
+  for (int base = 0; base < A.n_seqs; base += kWave) {
+    const int i = min(base + lane, A.n_seqs - 1);
+    const bool in = base + lane < A.n_seqs;
+    const int32_t t0 = A.cu_seqlens[i], t1 = A.cu_seqlens[i + 1];
+    const uint64_t back = __ballot(in && t1 < t0);
+    const uint64_t on = __ballot(in && begins(t0, i)) & (back ^ (back - 1));  // all lanes if none goes back
+    if (on != 0) s = base + 63 - __builtin_clzll(on);
+    if (on == 0 || back != 0) break;
+  }
+  return s;
+}
+
 // Row tiles of a packed batch: sequence s owns the tile ids from
 // floor(cu[s] G / BM) + s on, at least ceil(n_s G / BM) of them, so a tile id
 // finds its sequence without sums over the sequences before it.  Finds the
@@ -94,15 +114,7 @@ __device__ __forceinline__ int64_t tile_start(const AttnArgs& A, int s, int bm) 
   return (t > 0 ? t : 0) * A.G / bm + s;
 }
 __device__ __forceinline__ int find_seq(const AttnArgs& A, int64_t id, int bm) {
-  const int lane = threadIdx.x & (kWave - 1);
-  int s = 0;
-  for (int base = 0; base < A.n_seqs; base += kWave) {
-    const int i = base + lane;
-    const uint64_t m = __ballot(i < A.n_seqs && tile_start(A, i, bm) <= id);
-    if (m == 0) break;
-    s = base + 63 - __builtin_clzll(m);
-  }
-  return s;
+  return last_seq(A, [&](int32_t t0, int i) { return (t0 > 0 ? static_cast<int64_t>(t0) : 0) * A.G / bm + i <= id; });
 }
 
 // The address of the K (or V) row of key j: in its page, or among the call's rows.

@@ -528,9 +528,10 @@ gdn_status gdn_kv_write(const gdn_attn_geometry* g, void* k_cache, void* v_cache
  *   workspace: device, >= gdn_attn_prefill_workspace_bytes() (0 where no
  *   workspace is needed; then it may be NULL).  Calls that share a workspace
  *   must be ordered on one stream.
- * Device errors: GDN_DEV_BAD_SEQLENS (cu_seqlens[0] != 0, decreasing, or the
- * last > n_tokens) and GDN_DEV_BAD_LENGTH (ctx_len outside [0, max_pages * P])
- * skip the sequence; GDN_DEV_BAD_PAGE: a page id outside the cache, the
+ * Device errors: GDN_DEV_BAD_SEQLENS skips every sequence where cu_seqlens[0]
+ * != 0, the sequences that end past n_tokens, and a sequence that ends before it
+ * begins with all that follow it; GDN_DEV_BAD_LENGTH (ctx_len outside
+ * [0, max_pages * P]) skips the sequence; GDN_DEV_BAD_PAGE: a page id outside the cache, the
  * sequence's outputs are then not valid.
  */
 gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q_stride, const void* k,

@@ -284,6 +284,26 @@ def test_prefill_last_token_in_two_row_blocks(G, n, D):
         _check_sequences(pg, parts, cu, ctx[:5], o, D ** -0.5, BF16, f"G {G} n {n} D {D} batch {seed} sequence")
 
 
+@pytest.mark.parametrize("S,at,back,N,G,D,dtype", [
+    (3, 1, 2, 150, 1, 64, F32), (5, 3, 40, 400, 3, 128, F32), (130, 70, 90, 3900, 2, 64, F32),
+    (70, 65, 300, 2100, 3, 64, BF16), (150, 20, 5, 4500, 1, 128, BF16), (64, 40, 700, 6400, 4, 256, BF16), (4, 2, 60, 320, 6, 64, BF16)])
+def test_prefill_a_sequence_that_ends_before_it_begins(S, at, back, N, G, D, dtype):
+    """Bounds that go back: reported in every form of the call, the sequences before are right, that one and those
+    behind it stay as they were."""
+    new = [N // S] * S
+    m, geom, pg, parts, dev, cu, o = _prefill_case(940 + S + at, new, [0] * S, 1, G, D, 16, dtype)
+    cu = cu.copy()
+    cu[at + 1:] -= new[at] + back  # sequence `at` ends `back` tokens before it begins, the others follow on
+    assert cu[at + 1] == cu[at] - back
+    err = _err()
+    _run_prefill(m, geom, pg, dev, cu, None, o, err, paged=False)
+    torch.cuda.synchronize()
+    assert int(err.item()) == m.DEV_BAD_SEQLENS
+    ok = int(cu[at])
+    _check_sequences(pg, parts, cu, [0] * at, o, D ** -0.5, dtype, "sequence")
+    assert torch.all(o[ok:] == 7.0)
+
+
 # ---------------------------------------------------------------------------
 # trees
 # ---------------------------------------------------------------------------
