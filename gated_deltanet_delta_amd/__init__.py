@@ -203,8 +203,26 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _need(t: Optional[torch.Tensor], name: str, shape, dtype, optional=False):
-    if t is not None and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+def _index(t: torch.Tensor) -> Optional[int]:
+    """The GPU that a call's tensors are to be on, that of its first one (None: it is not on a GPU, which _need refuses)."""
+    return t.get_device() if t.is_cuda else None
+
+
+def _here(device: int, stream) -> ctypes.c_void_p:
+    """The stream of a call whose tensors are on `device`, which has to be the current one (the call launches there)."""
+    cur = torch.cuda.current_device()
+    if device != cur:
+        raise ValueError(f"tensors on cuda:{device}, required: the current device cuda:{cur}")
+    if stream is None:
+        return ctypes.c_void_p(_current_stream(cur))
+    if getattr(stream, "device_index", cur) != cur:
+        raise ValueError(f"stream: of cuda:{stream.device_index}, required: of the current device cuda:{cur}")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _need(t: Optional[torch.Tensor], name: str, shape, dtype, optional=False, device: Optional[int] = None):
+    if (t is not None and (t.is_cuda if device is None else t.get_device() == device) and t.dtype == dtype
+            and t.shape == shape and t.is_contiguous()):
         return
     if t is None:
         if optional:
@@ -218,6 +236,12 @@ def _need(t: Optional[torch.Tensor], name: str, shape, dtype, optional=False):
         raise ValueError(f"{name}: dtype {t.dtype}, required {dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, required {tuple(shape)}")
+    _need_device(t, name, device)
+
+
+def _need_device(t: torch.Tensor, name: str, device: Optional[int]):
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, required: cuda:{device}, as the call's other tensors")
 
 
 @dataclass
@@ -237,11 +261,11 @@ class SlotPool:
             torch.zeros(geom.n_slots, POS_STRIDE, dtype=torch.int32, device=device))
 
 
-def _check_pool(geom: Geometry, pool: SlotPool):
-    _need(pool.state, "state", (geom.n_slots, geom.n_v_heads, geom.d_v, geom.d_k), torch.float32)
+def _check_pool(geom: Geometry, pool: SlotPool, device: Optional[int] = None):
+    _need(pool.state, "state", (geom.n_slots, geom.n_v_heads, geom.d_v, geom.d_k), torch.float32, device=device)
     if geom.conv_width > 0:
-        _need(pool.conv_state, "conv_state", (geom.n_slots, geom.conv_ring, geom.conv_channels), torch.float32)
-        _need(pool.conv_pos, "conv_pos", (geom.n_slots, POS_STRIDE), torch.int32)
+        _need(pool.conv_state, "conv_state", (geom.n_slots, geom.conv_ring, geom.conv_channels), torch.float32, device=device)
+        _need(pool.conv_pos, "conv_pos", (geom.n_slots, POS_STRIDE), torch.int32, device=device)
 
 
 # --------------------------------------------------------------------------
@@ -493,26 +517,27 @@ def verify_tree_slots(geom: Geometry, pool: SlotPool, x, a, b, conv_w, slot, par
     """gdn_verify_tree_slots: as verify_k_slots, but draft j of row i continues from draft parent[i][j]
     (device int32 [batch][k]; -1: from the row's committed state); commit with commit_slots, accepted =
     1 + the last accepted node.  Without a dev_err, device errors go to ``device_error``'s word."""
-    B, k = x.shape[0], x.shape[1]
+    B, k, dev = x.shape[0], x.shape[1], _index(x)
     C, Hv, dv = geom.conv_channels, geom.n_v_heads, geom.d_v
-    _check_pool(geom, pool)
-    _need(x, "x", (B, k, C), geom.dtype)
-    _need(a, "a", (B, k, Hv), geom.dtype)
-    _need(b, "b", (B, k, Hv), geom.dtype)
-    _need(conv_w, "conv_w", (C, geom.conv_width), torch.float32, optional=geom.conv_width == 0)
-    _need(slot, "slot", (B,), torch.int32)
-    _need(parent, "parent", (B, k), torch.int32)
-    _need(snap_slot, "snap_slot", (B, k), torch.int32)
-    _need(k_row, "k_row", (B,), torch.int32, optional=True)
-    _need(o, "o", (B, k, Hv, dv), geom.dtype)
-    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
+    _check_pool(geom, pool, dev)
+    _need(x, "x", (B, k, C), geom.dtype, device=dev)
+    _need(a, "a", (B, k, Hv), geom.dtype, device=dev)
+    _need(b, "b", (B, k, Hv), geom.dtype, device=dev)
+    _need(conv_w, "conv_w", (C, geom.conv_width), torch.float32, optional=geom.conv_width == 0, device=dev)
+    _need(slot, "slot", (B,), torch.int32, device=dev)
+    _need(parent, "parent", (B, k), torch.int32, device=dev)
+    _need(snap_slot, "snap_slot", (B, k), torch.int32, device=dev)
+    _need(k_row, "k_row", (B,), torch.int32, optional=True, device=dev)
+    _need(o, "o", (B, k, Hv, dv), geom.dtype, device=dev)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
+    st = _here(dev, stream)
     if dev_err is None:
         dev_err = _default_err(x.device)
     g = geom.c_struct()
     _check(lib().gdn_verify_tree_slots(ctypes.byref(g), _ptr(pool.state), _ptr(pool.conv_state),
                                        _ptr(pool.conv_pos), _ptr(x), _ptr(a), _ptr(b), _ptr(conv_w), _ptr(slot), B,
                                        k, _ptr(k_row), _ptr(parent), _ptr(snap_slot), _ptr(o), _ptr(dev_err),
-                                       _stream(stream)))
+                                       st))
 
 
 # --------------------------------------------------------------------------
@@ -565,17 +590,10 @@ class KVCache:
                        torch.zeros(shape, dtype=geom.dtype, device=device))
 
 
-def _same_device(*named):
-    """Every tensor on the current device (the calls launch there): refused otherwise."""
-    cur = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"{name}: on {t.device}, required: the current device cuda:{cur}")
-
-
-def _need_rows(t: Optional[torch.Tensor], name: str, shape, dtype) -> int:
+def _need_rows(t: Optional[torch.Tensor], name: str, shape, dtype, device: Optional[int] = None) -> int:
     """Rows of heads, any row stride, contiguous within a row; returns the row stride in elements."""
-    if t is not None and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+    if (t is not None and (t.is_cuda if device is None else t.get_device() == device) and t.dtype == dtype
+            and t.shape == shape and t.is_contiguous()):
         return shape[-2] * shape[-1]
     if t is None:
         raise ValueError(f"{name}: missing")
@@ -593,20 +611,22 @@ def _need_rows(t: Optional[torch.Tensor], name: str, shape, dtype) -> int:
     if (st[-1] != 1 or (st[-2] != D and shape[-2] > 1) or (len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * row)
             or row < 0):
         raise ValueError(f"{name}: strides {tuple(st)}, required: heads contiguous, rows one stride apart")
+    _need_device(t, name, device)
     return row
 
 
-def _check_cache(geom: AttnGeometry, cache: KVCache):
+def _check_cache(geom: AttnGeometry, cache: KVCache, device: Optional[int]):
     shape = (geom.n_pages, geom.n_kv_heads, geom.page_tokens, geom.d_head)
-    _need(cache.k, "cache.k", shape, geom.dtype)
-    _need(cache.v, "cache.v", shape, geom.dtype)
+    _need(cache.k, "cache.k", shape, geom.dtype, device=device)
+    _need(cache.v, "cache.v", shape, geom.dtype, device=device)
 
 
-def _workspace(workspace):
+def _workspace(workspace, device: Optional[int]):
     if workspace is None:
         return None, 0
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous device tensor")
+    _need_device(workspace, "workspace", device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -614,42 +634,42 @@ def kv_plan(geom: AttnGeometry, kv_len, new_len, free_pages, n_free, block_table
             kv_len_out, n_free_out, dev_err=None, stream=None):
     """gdn_kv_plan: block tables, slot map and positions of the new tokens from the rows' lengths (new_len -1: the
     row leaves and gives its pages back); slot_map and position may be longer than the new tokens (padding)."""
-    B, N = kv_len.shape[0], slot_map.shape[0]
+    B, N, dev = kv_len.shape[0], slot_map.shape[0], _index(kv_len)
     i32 = torch.int32
-    _need(kv_len, "kv_len", (B,), i32)
-    _need(new_len, "new_len", (B,), i32)
-    _need(free_pages, "free_pages", (geom.n_pages,), i32)
-    _need(n_free, "n_free", (1,), i32)
-    _need(block_table, "block_table", (B, geom.max_pages), i32)
-    _need(cu_new, "cu_new", (B + 1,), i32)
-    _need(slot_map, "slot_map", (N,), i32)
-    _need(position, "position", (N,), i32)
-    _need(kv_len_out, "kv_len_out", (B,), i32)
-    _need(n_free_out, "n_free_out", (1,), i32)
-    _need(dev_err, "dev_err", (1,), i32, optional=True)
-    _same_device(("kv_len", kv_len), ("block_table", block_table), ("slot_map", slot_map))
+    _need(kv_len, "kv_len", (B,), i32, device=dev)
+    _need(new_len, "new_len", (B,), i32, device=dev)
+    _need(free_pages, "free_pages", (geom.n_pages,), i32, device=dev)
+    _need(n_free, "n_free", (1,), i32, device=dev)
+    _need(block_table, "block_table", (B, geom.max_pages), i32, device=dev)
+    _need(cu_new, "cu_new", (B + 1,), i32, device=dev)
+    _need(slot_map, "slot_map", (N,), i32, device=dev)
+    _need(position, "position", (N,), i32, device=dev)
+    _need(kv_len_out, "kv_len_out", (B,), i32, device=dev)
+    _need(n_free_out, "n_free_out", (1,), i32, device=dev)
+    _need(dev_err, "dev_err", (1,), i32, optional=True, device=dev)
+    st = _here(dev, stream)
     if dev_err is None:
         dev_err = _default_err(kv_len.device)
     _check(lib().gdn_kv_plan(geom._ref(), kv_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
                              n_free.data_ptr(), block_table.data_ptr(), B, N, cu_new.data_ptr(), slot_map.data_ptr(),
                              position.data_ptr(), kv_len_out.data_ptr(), n_free_out.data_ptr(), dev_err.data_ptr(),
-                             _stream(stream)))
+                             st))
 
 
 def kv_write(geom: AttnGeometry, cache: KVCache, k, v, slot_map, dev_err=None, stream=None):
     """gdn_kv_write: k and v rows [n_tokens][H_kv][d_head] (any row stride) into their cache slots; slot -1 skips."""
-    N = slot_map.shape[0]
+    N, dev = slot_map.shape[0], _index(cache.k)
     shape = (N, geom.n_kv_heads, geom.d_head)
-    _check_cache(geom, cache)
-    ks = _need_rows(k, "k", shape, geom.dtype)
-    vs = _need_rows(v, "v", shape, geom.dtype)
-    _need(slot_map, "slot_map", (N,), torch.int32)
-    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
-    _same_device(("cache.k", cache.k), ("k", k), ("v", v), ("slot_map", slot_map))
+    _check_cache(geom, cache, dev)
+    ks = _need_rows(k, "k", shape, geom.dtype, dev)
+    vs = _need_rows(v, "v", shape, geom.dtype, dev)
+    _need(slot_map, "slot_map", (N,), torch.int32, device=dev)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
+    st = _here(dev, stream)
     if dev_err is None:
         dev_err = _default_err(k.device)
     _check(lib().gdn_kv_write(geom._ref(), cache.k.data_ptr(), cache.v.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs,
-                              slot_map.data_ptr(), N, dev_err.data_ptr(), _stream(stream)))
+                              slot_map.data_ptr(), N, dev_err.data_ptr(), st))
 
 
 def attn_prefill_workspace_bytes(geom: AttnGeometry, n_tokens: int, n_seqs: int) -> int:
@@ -666,31 +686,30 @@ def attn_prefill(geom: AttnGeometry, q, k, v, cu_seqlens, o, workspace=None, cac
     """gdn_attn_prefill: causal attention of packed prompts, q [n_tokens][H_q][d_head], k and v
     [n_tokens][H_kv][d_head] (any row strides), sequence s after ctx_len[s] tokens that are in the cache already
     (block table row s); ctx_len None: none.  Without a dev_err, device errors go to ``device_error``'s word."""
-    N, S = q.shape[0], cu_seqlens.shape[0] - 1
+    N, S, dev = q.shape[0], cu_seqlens.shape[0] - 1, _index(q)
     if S < 1:
         raise ValueError("cu_seqlens: needs at least two entries")
-    qs = _need_rows(q, "q", (N, geom.n_q_heads, geom.d_head), geom.dtype)
-    ks = _need_rows(k, "k", (N, geom.n_kv_heads, geom.d_head), geom.dtype)
-    vs = _need_rows(v, "v", (N, geom.n_kv_heads, geom.d_head), geom.dtype)
-    _need(cu_seqlens, "cu_seqlens", (S + 1,), torch.int32)
-    _need(o, "o", (N, geom.n_q_heads, geom.d_head), geom.dtype)
-    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
+    qs = _need_rows(q, "q", (N, geom.n_q_heads, geom.d_head), geom.dtype, dev)
+    ks = _need_rows(k, "k", (N, geom.n_kv_heads, geom.d_head), geom.dtype, dev)
+    vs = _need_rows(v, "v", (N, geom.n_kv_heads, geom.d_head), geom.dtype, dev)
+    _need(cu_seqlens, "cu_seqlens", (S + 1,), torch.int32, device=dev)
+    _need(o, "o", (N, geom.n_q_heads, geom.d_head), geom.dtype, device=dev)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
     kc = vc = bt = cl = None
     if ctx_len is not None:
         if cache is None:
             raise ValueError("cache: missing (ctx_len is given)")
-        _check_cache(geom, cache)
-        _need(block_table, "block_table", (S, geom.max_pages), torch.int32)
-        _need(ctx_len, "ctx_len", (S,), torch.int32)
-        _same_device(("cache.k", cache.k), ("block_table", block_table))
+        _check_cache(geom, cache, dev)
+        _need(block_table, "block_table", (S, geom.max_pages), torch.int32, device=dev)
+        _need(ctx_len, "ctx_len", (S,), torch.int32, device=dev)
         kc, vc, bt, cl = cache.k.data_ptr(), cache.v.data_ptr(), block_table.data_ptr(), ctx_len.data_ptr()
-    _same_device(("q", q), ("k", k), ("v", v), ("o", o), ("workspace", workspace))
-    ws, nbytes = _workspace(workspace)
+    st = _here(dev, stream)
+    ws, nbytes = _workspace(workspace, dev)
     if dev_err is None:
         dev_err = _default_err(q.device)
     _check(lib().gdn_attn_prefill(geom._ref(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                                   cu_seqlens.data_ptr(), S, N, kc, vc, bt, cl, ws, nbytes, o.data_ptr(),
-                                  dev_err.data_ptr(), _stream(stream)))
+                                  dev_err.data_ptr(), st))
 
 
 def attn_tree_workspace_bytes(geom: AttnGeometry, batch: int, n: int) -> int:
@@ -707,25 +726,25 @@ def attn_tree(geom: AttnGeometry, cache: KVCache, block_table, ctx_len, q, k, v,
     """gdn_attn_tree: each row's n drafted nodes attend its ctx_len cached tokens, their ancestors among the drafts
     (parent [batch][n], -1: the cached tokens) and themselves; q [batch][n][H_q][d_head], k and v
     [batch][n][H_kv][d_head].  n = 1 with parent -1 is the decode step."""
-    B, n = q.shape[0], q.shape[1]
-    _check_cache(geom, cache)
-    qs = _need_rows(q, "q", (B, n, geom.n_q_heads, geom.d_head), geom.dtype)
-    ks = _need_rows(k, "k", (B, n, geom.n_kv_heads, geom.d_head), geom.dtype)
-    vs = _need_rows(v, "v", (B, n, geom.n_kv_heads, geom.d_head), geom.dtype)
-    _need(block_table, "block_table", (B, geom.max_pages), torch.int32)
-    _need(ctx_len, "ctx_len", (B,), torch.int32)
-    _need(parent, "parent", (B, n), torch.int32)
-    _need(n_row, "n_row", (B,), torch.int32, optional=True)
-    _need(o, "o", (B, n, geom.n_q_heads, geom.d_head), geom.dtype)
-    _need(dev_err, "dev_err", (1,), torch.int32, optional=True)
-    _same_device(("cache.k", cache.k), ("q", q), ("k", k), ("v", v), ("o", o), ("workspace", workspace))
-    ws, nbytes = _workspace(workspace)
+    B, n, dev = q.shape[0], q.shape[1], _index(cache.k)
+    _check_cache(geom, cache, dev)
+    qs = _need_rows(q, "q", (B, n, geom.n_q_heads, geom.d_head), geom.dtype, dev)
+    ks = _need_rows(k, "k", (B, n, geom.n_kv_heads, geom.d_head), geom.dtype, dev)
+    vs = _need_rows(v, "v", (B, n, geom.n_kv_heads, geom.d_head), geom.dtype, dev)
+    _need(block_table, "block_table", (B, geom.max_pages), torch.int32, device=dev)
+    _need(ctx_len, "ctx_len", (B,), torch.int32, device=dev)
+    _need(parent, "parent", (B, n), torch.int32, device=dev)
+    _need(n_row, "n_row", (B,), torch.int32, optional=True, device=dev)
+    _need(o, "o", (B, n, geom.n_q_heads, geom.d_head), geom.dtype, device=dev)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
+    st = _here(dev, stream)
+    ws, nbytes = _workspace(workspace, dev)
     if dev_err is None:
         dev_err = _default_err(q.device)
     _check(lib().gdn_attn_tree(geom._ref(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, parent.data_ptr(),
                                None if n_row is None else n_row.data_ptr(), B, n, cache.k.data_ptr(),
                                cache.v.data_ptr(), block_table.data_ptr(), ctx_len.data_ptr(), ws, nbytes,
-                               o.data_ptr(), dev_err.data_ptr(), _stream(stream)))
+                               o.data_ptr(), dev_err.data_ptr(), st))
 
 
 __all__ = [
