@@ -575,6 +575,10 @@ class AttnGeometry:
             object.__setattr__(self, "_c_ref", r)
         return r
 
+    def __getstate__(self):
+        """What copies and pickles carry: the fields, not this object's C struct."""
+        return {k: v for k, v in self.__dict__.items() if k != "_c_ref"}
+
 
 @dataclass
 class KVCache:

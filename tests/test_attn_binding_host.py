@@ -1,6 +1,9 @@
 """The binding of the paged-cache, attention and tree entry points on the host (no GPU): which device a call's tensors
-and stream are on."""
+and stream are on, copies of the geometry."""
+import copy
+import dataclasses
 import os
+import pickle
 
 import pytest
 import torch
@@ -121,3 +124,17 @@ def test_every_tensor_is_on_the_current_device(gdn, on_gpu_0, name):
 def test_the_stream_is_of_the_current_device(gdn, on_gpu_0, name):
     with pytest.raises(ValueError, match="stream: of cuda:1, required: of the current device cuda:0"):
         _call(gdn, name, _calls(gdn)[name][2], _Stream(1))
+
+
+def test_a_geometry_that_was_used_can_be_copied(gdn):
+    """Copies and pickles of a geometry carry its fields; each has a C struct of its own."""
+    g = gdn.AttnGeometry(n_q_heads=6, n_kv_heads=2, d_head=128, n_pages=7, scale=0.25)
+    g.check()  # makes its C struct
+    for c in (copy.copy(g), copy.deepcopy(g), pickle.loads(pickle.dumps(g)), dataclasses.replace(g)):
+        assert c == g and c is not g and hash(c) == hash(g)
+        assert "_c_ref" not in c.__dict__
+        c.check()
+        assert gdn.attn_prefill_workspace_bytes(c, 9, 1) == gdn.attn_prefill_workspace_bytes(g, 9, 1) > 0
+    other = dataclasses.replace(g, n_q_heads=5)
+    with pytest.raises(gdn.GdnError, match="n_q_heads: 5"):
+        other.check()
