@@ -26,7 +26,7 @@ POS_ONE = 65536
 POS_STRIDE = 32  # int32 words per slot in conv_pos: slot s's position is conv_pos[s, 0]
 CHUNK = 64
 
-ABI_VERSION = 8  # GDN_ABI_VERSION of include/gdn.h that these signatures follow
+ABI_VERSION = 9  # GDN_ABI_VERSION of include/gdn.h that these signatures follow
 DEV_OK = 0
 DEV_BAD_SLOT = 1
 DEV_BAD_ACCEPTED = 2
@@ -116,8 +116,10 @@ _SIGS = {
     "gdn_kv_write": (ctypes.c_int, [_P, _P, _P, _P, _L, _P, _L, _P, _I, _P, _P]),
     "gdn_attn_prefill": (ctypes.c_int, [_P, _P, _L, _P, _L, _P, _L, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P, _P, _P]),
     "gdn_attn_prefill_workspace_bytes": (_Z, [_P, _I, _I]),
+    "gdn_attn_prefill_workspace_max_bytes": (_Z, [_P, _I, _I]),
     "gdn_attn_tree": (ctypes.c_int, [_P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P, _P, _P]),
     "gdn_attn_tree_workspace_bytes": (_Z, [_P, _I, _I]),
+    "gdn_attn_tree_workspace_max_bytes": (_Z, [_P, _I, _I]),
 }
 
 _lib = None
@@ -676,13 +678,17 @@ def kv_write(geom: AttnGeometry, cache: KVCache, k, v, slot_map, dev_err=None, s
                               slot_map.data_ptr(), N, dev_err.data_ptr(), st))
 
 
-def attn_prefill_workspace_bytes(geom: AttnGeometry, n_tokens: int, n_seqs: int) -> int:
-    return int(lib().gdn_attn_prefill_workspace_bytes(geom._ref(), n_tokens, n_seqs))
+def attn_prefill_workspace_bytes(geom: AttnGeometry, n_tokens: int, n_seqs: int, up_to: bool = False) -> int:
+    """What a call of these sizes needs; up_to: the most that any call of up to these sizes needs (a shorter one may
+    need more than a longer one)."""
+    f = lib().gdn_attn_prefill_workspace_max_bytes if up_to else lib().gdn_attn_prefill_workspace_bytes
+    return int(f(geom._ref(), n_tokens, n_seqs))
 
 
-def alloc_attn_prefill_workspace(geom: AttnGeometry, n_tokens: int, n_seqs: int, device="cuda") -> torch.Tensor:
-    """A caller-owned workspace of the size gdn_attn_prefill_workspace_bytes reports (may be empty)."""
-    return torch.empty(attn_prefill_workspace_bytes(geom, n_tokens, n_seqs), dtype=torch.uint8, device=device)
+def alloc_attn_prefill_workspace(geom: AttnGeometry, n_tokens: int, n_seqs: int, device="cuda",
+                                 up_to: bool = False) -> torch.Tensor:
+    """A caller-owned workspace of the size attn_prefill_workspace_bytes reports (may be empty)."""
+    return torch.empty(attn_prefill_workspace_bytes(geom, n_tokens, n_seqs, up_to), dtype=torch.uint8, device=device)
 
 
 def attn_prefill(geom: AttnGeometry, q, k, v, cu_seqlens, o, workspace=None, cache: Optional[KVCache] = None,
@@ -716,13 +722,15 @@ def attn_prefill(geom: AttnGeometry, q, k, v, cu_seqlens, o, workspace=None, cac
                                   dev_err.data_ptr(), st))
 
 
-def attn_tree_workspace_bytes(geom: AttnGeometry, batch: int, n: int) -> int:
-    return int(lib().gdn_attn_tree_workspace_bytes(geom._ref(), batch, n))
+def attn_tree_workspace_bytes(geom: AttnGeometry, batch: int, n: int, up_to: bool = False) -> int:
+    """What a call of these sizes needs; up_to: the most that any call of up to these sizes needs."""
+    f = lib().gdn_attn_tree_workspace_max_bytes if up_to else lib().gdn_attn_tree_workspace_bytes
+    return int(f(geom._ref(), batch, n))
 
 
-def alloc_attn_tree_workspace(geom: AttnGeometry, batch: int, n: int, device="cuda") -> torch.Tensor:
-    """A caller-owned workspace of the size gdn_attn_tree_workspace_bytes reports (may be empty)."""
-    return torch.empty(attn_tree_workspace_bytes(geom, batch, n), dtype=torch.uint8, device=device)
+def alloc_attn_tree_workspace(geom: AttnGeometry, batch: int, n: int, device="cuda", up_to: bool = False) -> torch.Tensor:
+    """A caller-owned workspace of the size attn_tree_workspace_bytes reports (may be empty)."""
+    return torch.empty(attn_tree_workspace_bytes(geom, batch, n, up_to), dtype=torch.uint8, device=device)
 
 
 def attn_tree(geom: AttnGeometry, cache: KVCache, block_table, ctx_len, q, k, v, parent, o, workspace=None,

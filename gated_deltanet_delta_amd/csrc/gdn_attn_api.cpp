@@ -1,6 +1,7 @@
 // C ABI of the paged KV cache, the attention over it, and the verify over a
 // tree of drafts: argument validation and dispatch, as gdn_api.cpp does for
 // the layer's other entry points.  Host code only.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -70,6 +71,26 @@ int attn_split(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes
 size_t attn_bytes(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes) {
   return gdn::attn_part_bytes(tokens, n_seqs, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head, nodes,
                               g->dtype == GDN_BF16);
+}
+
+// The most that attn_bytes() gives for 1 .. most rows (or batch rows), whose calls
+// take splits_of() parts: fewer with more rows.  Among calls of as many parts the
+// one of the most rows needs the most.
+template <class Splits, class Bytes>
+size_t most_bytes(int64_t most, Splits splits_of, Bytes bytes_of) {
+  size_t best = 0;
+  for (int64_t n = most; n >= 1;) {
+    best = std::max(best, bytes_of(n));
+    const int parts = splits_of(n);
+    int64_t lo = 0, hi = n;  // the largest below n with more parts: lo has more (or is 0), hi has not
+    while (hi - lo > 1) {
+      const int64_t mid = lo + (hi - lo) / 2;
+      if (splits_of(mid) > parts) lo = mid;
+      else hi = mid;
+    }
+    n = lo;
+  }
+  return best;
 }
 
 gdn::AttnArgs attn_args(const gdn_attn_geometry* g, int32_t n_split, void* workspace, int64_t tokens) {
@@ -190,6 +211,25 @@ size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_geometry* g, int32_t n_to
 size_t gdn_attn_tree_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n) {
   if (check_attn(g) != GDN_OK || batch < 1 || n < 1 || n > g->max_tree) return 0;
   return attn_bytes(g, static_cast<int64_t>(batch) * n, batch, n);
+}
+
+size_t gdn_attn_prefill_workspace_max_bytes(const gdn_attn_geometry* g, int32_t max_tokens, int32_t max_seqs) {
+  if (check_attn(g) != GDN_OK || max_tokens < 0 || max_seqs < 1) return 0;
+  // one sequence has the fewest row tiles, so the most parts
+  return most_bytes(
+      max_tokens, [&](int64_t n) { return attn_split(g, n, 1, 0, INT64_MAX / 2, false); },
+      [&](int64_t n) { return attn_bytes(g, n, 1, 0); });
+}
+
+size_t gdn_attn_tree_workspace_max_bytes(const gdn_attn_geometry* g, int32_t max_batch, int32_t max_n) {
+  if (check_attn(g) != GDN_OK || max_batch < 1 || max_n < 1 || max_n > g->max_tree) return 0;
+  size_t best = 0;
+  for (int n = 1; n <= max_n; ++n)
+    best = std::max(best, most_bytes(
+                              max_batch,
+                              [&](int64_t b) { return attn_split(g, b * n, static_cast<int>(b), n, INT64_MAX / 2, false); },
+                              [&](int64_t b) { return attn_bytes(g, b * n, static_cast<int>(b), n); }));
+  return best;
 }
 
 gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q_stride, const void* k,

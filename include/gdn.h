@@ -87,12 +87,13 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 8  /* 4: prefill on the caller's stream alone, workspace independent of n_tokens,
+#define GDN_ABI_VERSION 9  /* 4: prefill on the caller's stream alone, workspace independent of n_tokens,
                               checkpoints at any block size, GDN_DEV_INCOMPLETE;
                               5: gdn_prefill_chunked_static;
                               6: gdn_prefill_timing_events;
                               7: GDN_DEV_DUP_SLOT (debug builds);
-                              8: the paged KV cache and the attention over it, verify over a tree of drafts */
+                              8: the paged KV cache and the attention over it, verify over a tree of drafts;
+                              9: gdn_attn_prefill_workspace_max_bytes, gdn_attn_tree_workspace_max_bytes */
 /* bytes of the library's own prefill workspace, one per GPU (gdn_prefill_chunked_static) */
 #define GDN_PREFILL_STATIC_WORKSPACE_BYTES ((size_t)64 << 20)
 #define GDN_POS_ONE 65536
@@ -525,9 +526,12 @@ gdn_status gdn_kv_write(const gdn_attn_geometry* g, void* k_cache, void* v_cache
  * Sequences may be empty; rows of o behind cu_seqlens[n_seqs] <= n_tokens are
  * left as they are.
  *   0 <= n_tokens < 2^30.
- *   workspace: device, >= gdn_attn_prefill_workspace_bytes() (0 where no
- *   workspace is needed; then it may be NULL).  Calls that share a workspace
- *   must be ordered on one stream.
+ *   workspace: device, >= gdn_attn_prefill_workspace_bytes() of this n_tokens
+ *   and n_seqs (0 where no workspace is needed; then it may be NULL).  Calls of
+ *   few rows split the key axis and need one, longer ones do not, so a buffer
+ *   for calls of many sizes is of gdn_attn_prefill_workspace_max_bytes(), the
+ *   most that any call of up to max_tokens tokens and max_seqs sequences needs.
+ *   Calls that share a workspace must be ordered on one stream.
  * Device errors: GDN_DEV_BAD_SEQLENS skips every sequence where cu_seqlens[0]
  * != 0, the sequences that end past n_tokens, and a sequence that ends before it
  * begins with all that follow it; GDN_DEV_BAD_LENGTH (ctx_len outside
@@ -540,6 +544,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q
                             const int32_t* block_table, const int32_t* ctx_len, void* workspace,
                             size_t workspace_bytes, void* o, int32_t* dev_err, void* stream);
 size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_geometry* g, int32_t n_tokens, int32_t n_seqs);
+size_t gdn_attn_prefill_workspace_max_bytes(const gdn_attn_geometry* g, int32_t max_tokens, int32_t max_seqs);
 
 /*
  * Attention of a tree of n drafted tokens per row over the cache: node j of row
@@ -552,7 +557,9 @@ size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_geometry* g, int32_t n_to
  * accepted is written there, afterwards (gdn_kv_write with slot -1 for the
  * other nodes).  n_row (int32 [batch], or NULL for n): row i's own node count
  * in 1..n; later nodes are neither read nor written.
- *   workspace: device, >= gdn_attn_tree_workspace_bytes(); calls that share a
+ *   workspace: device, >= gdn_attn_tree_workspace_bytes() of this batch and n (a
+ *   smaller call may need more: gdn_attn_tree_workspace_max_bytes() is the most
+ *   that any of up to max_batch rows and max_n nodes needs); calls that share a
  *   workspace must be ordered on one stream.
  *   1 <= batch, 1 <= n <= max_tree.
  * Device errors: GDN_DEV_BAD_K (n_row), GDN_DEV_BAD_PARENT and
@@ -565,6 +572,7 @@ gdn_status gdn_attn_tree(const gdn_attn_geometry* g, const void* q, int64_t q_st
                          const int32_t* block_table, const int32_t* ctx_len, void* workspace,
                          size_t workspace_bytes, void* o, int32_t* dev_err, void* stream);
 size_t gdn_attn_tree_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n);
+size_t gdn_attn_tree_workspace_max_bytes(const gdn_attn_geometry* g, int32_t max_batch, int32_t max_n);
 
 #ifdef __cplusplus
 }

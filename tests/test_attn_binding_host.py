@@ -1,5 +1,5 @@
 """The binding of the paged-cache, attention and tree entry points on the host (no GPU): which device a call's tensors
-and stream are on, copies of the geometry."""
+and stream are on, copies of the geometry, workspaces for calls of many sizes."""
 import copy
 import dataclasses
 import os
@@ -138,3 +138,24 @@ def test_a_geometry_that_was_used_can_be_copied(gdn):
     other = dataclasses.replace(g, n_q_heads=5)
     with pytest.raises(gdn.GdnError, match="n_q_heads: 5"):
         other.check()
+
+
+@pytest.mark.parametrize("Hk,G,D,dtype", [(4, 6, 256, BF16), (1, 1, 64, BF16), (2, 7, 128, BF16), (4, 6, 256, F32), (1, 3, 64, F32)])
+def test_a_workspace_for_all_sizes(gdn, Hk, G, D, dtype):
+    """The size for calls of up to n is the largest of theirs: a shorter call may need more than a longer one."""
+    g = gdn.AttnGeometry(n_q_heads=Hk * G, n_kv_heads=Hk, d_head=D, n_pages=64, max_pages=64, max_tree=20, dtype=dtype)
+    for most in (1, 9, 43, 256, 2048, 5000):
+        for seqs in (1, 5):
+            each = [gdn.attn_prefill_workspace_bytes(g, n, s) for n in range(1, most + 1) for s in range(1, seqs + 1)]
+            assert gdn.attn_prefill_workspace_bytes(g, most, seqs, up_to=True) == max(each)
+    assert gdn.attn_prefill_workspace_bytes(g, 100000, 1) == 0  # and the largest among them need none
+    assert gdn.attn_prefill_workspace_bytes(g, (1 << 30) - 1, 1, up_to=True) == \
+        gdn.attn_prefill_workspace_bytes(g, 100000, 3, up_to=True) > 0
+    for batch, n in ((1, 1), (7, 20), (300, 3), (1500, 20)):
+        each = [gdn.attn_tree_workspace_bytes(g, b, k) for b in range(1, batch + 1) for k in range(1, n + 1)]
+        assert gdn.attn_tree_workspace_bytes(g, batch, n, up_to=True) == max(each)
+    assert gdn.attn_prefill_workspace_bytes(g, 0, 1, up_to=True) == 0
+    for bad in ((-1, 1), (9, 0)):
+        assert gdn.attn_prefill_workspace_bytes(g, *bad, up_to=True) == 0
+    for bad in ((0, 1), (1, 0), (1, 21)):
+        assert gdn.attn_tree_workspace_bytes(g, *bad, up_to=True) == 0

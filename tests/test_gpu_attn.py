@@ -533,3 +533,30 @@ def test_streams_and_graph_replays():
         torch.cuda.synchronize()
         assert int(err.item()) == 0
         assert torch.equal(o, eager) and torch.equal(o2, eager2) and torch.equal(outs[0], eager)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 256), (F32, 64)])
+def test_one_workspace_for_calls_of_many_sizes(dtype, D):
+    """A workspace for up to 2048 tokens serves every shorter prompt, and one for up to 40 rows every smaller batch of
+    trees: results as with a workspace of the call's own, bit for bit."""
+    m = AH.gdn()
+    ws = None
+    for n in (2048, 700, 256, 43, 1):
+        mm, geom, pg, parts, dev, cu, o = _prefill_case(980, [n], [0], 1, 6, D, 16, dtype)
+        if ws is None:
+            ws = m.alloc_attn_prefill_workspace(geom, 2048, 3, up_to=True)
+        err, own = _err(), o.clone()
+        m.attn_prefill(geom, *dev, _cuda(cu), o, ws, dev_err=err)
+        m.attn_prefill(geom, *dev, _cuda(cu), own, m.alloc_attn_prefill_workspace(geom, n, 1), dev_err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and torch.isfinite(o).all() and torch.equal(o, own)
+    ws = None
+    for b, n in ((40, 5), (8, 5), (3, 1), (1, 4)):
+        mm, geom, pg, parts, dev, par, o = _tree_case(990, [100] * b, n, 1, 6, D, 16, dtype, max_tree=5)
+        if ws is None:
+            ws = m.alloc_attn_tree_workspace(geom, 40, 5, up_to=True)
+        err, own = _err(), o.clone()
+        _run_tree(m, geom, pg, dev, par, [100] * b, o, err, ws=ws)
+        _run_tree(m, geom, pg, dev, par, [100] * b, own, err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and torch.isfinite(o).all() and torch.equal(o, own)
