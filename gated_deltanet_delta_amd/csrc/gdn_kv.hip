@@ -142,6 +142,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs A) {
   };
 
   const int gtid = blockIdx.x * kPlanThreads + tid, gsize = gridDim.x * kPlanThreads;
+  const uint32_t n_slots = A.max_tokens;  // up to 2^31 - 1, so its index has no sign: the step past the last entry takes 32 bits
   // ---- rows: lengths, offsets ----
   for (int i = gtid; i < B; i += gsize) {
     const int32_t c = A.kv_len[i], n = A.new_len[i];
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs A) {
     *A.n_free_out = stack_ok ? static_cast<int32_t>(top - used) : f0;
   }
   if (!stack_ok) {
-    for (int t = gtid; t < A.max_tokens; t += gsize) {
+    for (uint32_t t = gtid; t < n_slots; t += gsize) {
       A.slot_map[t] = -1;
       A.position[t] = 0;
     }
@@ -183,7 +184,8 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(KvPlanArgs A) {
   }
   // ---- slots and positions of the new tokens ----
   const int32_t total = min(tok0[B], A.max_tokens);
-  for (int t = gtid; t < A.max_tokens; t += gsize) {
+  for (uint32_t at = gtid; at < n_slots; at += gsize) {
+    const int32_t t = static_cast<int32_t>(at);
     int32_t slot = -1, pos = 0;
     if (t < total) {
       const int i = row_of(tok0, B, t);

@@ -307,3 +307,28 @@ def test_operators_together():
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     assert int(n_free.item()) == before + -(-len(held[0][0]) // page) and kv_len.cpu().tolist()[0] == 0
+
+
+@pytest.mark.parametrize("bad_stack", [False, True])
+def test_plan_with_the_longest_slot_map(bad_stack):
+    """max_tokens of 2^31 - 1: every padding entry is written, up to the last, and none outside the tables."""
+    m = AH.gdn()
+    kv, new = [10, 0], [5, 3]
+    n_pages, width, tables, free, n_free = _plan_inputs(8, kv, new, 16, 2)
+    geom = m.AttnGeometry(n_q_heads=1, n_kv_heads=1, d_head=64, page_tokens=16, n_pages=n_pages, max_pages=width)
+    N, edge = 2 ** 31 - 1, 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    both = torch.full((2, N + 2 * edge), -3, **i32)  # 17 GB
+    slot_map, position = both[0, edge:edge + N], both[1, edge:edge + N]
+    out = [torch.full((n,), -3, **i32) for n in (3, 2, 1)]
+    err = torch.zeros(1, **i32)
+    m.kv_plan(geom, _cuda(kv), _cuda(new), _cuda(free), _cuda([n_pages + 1 if bad_stack else n_free]), _cuda(tables), out[0],
+              slot_map, position, out[1], out[2], dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == (m.DEV_BAD_PAGE if bad_stack else 0)
+    used = 0 if bad_stack else 8
+    if not bad_stack:
+        ref = ao.kv_plan(16, n_pages, width, kv, new, free, n_free, tables, 8)
+        assert slot_map[:8].tolist() == ref["slot_map"].tolist() and position[:8].tolist() == ref["position"].tolist()
+    assert bool((slot_map[used:] == -1).all()) and bool((position[used:] == 0).all())
+    assert bool((both[:, :edge] == -3).all()) and bool((both[:, edge + N:] == -3).all())
