@@ -15,7 +15,10 @@ using gdn::fail;
 using gdn::launched;
 using gdn::ok;
 
-constexpr int32_t kMaxLen = (1 << 30) - 1;  // tokens of a sequence: cached plus new ones fit 31 bits
+constexpr int32_t kMaxLen = (1 << 30) - 1;  // cached tokens of a sequence
+// rows of a packed call: a sequence's cached plus new tokens fit 31 bits, rounded
+// up to whole tiles and with the tiles that are requested ahead of the last
+constexpr int32_t kMaxTokens = (1 << 30) - 4096;
 
 gdn_status check_attn(const gdn_attn_geometry* g) {
   if (!g) return fail(GDN_ERR_NULL, "attention geometry: NULL, required: a gdn_attn_geometry");
@@ -240,8 +243,8 @@ gdn_status gdn_attn_prefill(const gdn_attn_geometry* g, const void* q, int64_t q
   gdn_status s = check_attn(g);
   if (s != GDN_OK) return s;
   if (n_seqs < 1) return fail(GDN_ERR_RANGE, "n_seqs: %d, required: >= 1", n_seqs);
-  if (n_tokens < 0 || n_tokens > kMaxLen)
-    return fail(GDN_ERR_RANGE, "n_tokens: %d, required: 0..%d", n_tokens, kMaxLen);
+  if (n_tokens < 0 || n_tokens > kMaxTokens)
+    return fail(GDN_ERR_RANGE, "n_tokens: %d, required: 0..%d", n_tokens, kMaxTokens);
   if ((s = check_stride(g, q_stride, g->n_q_heads, "q_stride")) != GDN_OK) return s;
   if ((s = check_stride(g, k_stride, g->n_kv_heads, "k_stride")) != GDN_OK) return s;
   if ((s = check_stride(g, v_stride, g->n_kv_heads, "v_stride")) != GDN_OK) return s;

@@ -525,7 +525,7 @@ gdn_status gdn_kv_write(const gdn_attn_geometry* g, void* k_cache, void* v_cache
  * read from k and v, whether or not they are in the cache already.
  * Sequences may be empty; rows of o behind cu_seqlens[n_seqs] <= n_tokens are
  * left as they are.
- *   0 <= n_tokens < 2^30.
+ *   0 <= n_tokens <= 2^30 - 4096.
  *   workspace: device, >= gdn_attn_prefill_workspace_bytes() of this n_tokens
  *   and n_seqs (0 where no workspace is needed; then it may be NULL).  Calls of
  *   few rows split the key axis and need one, longer ones do not, so a buffer

@@ -1,5 +1,6 @@
 """The binding of the paged-cache, attention and tree entry points on the host (no GPU): which device a call's tensors
-and stream are on, copies of the geometry, workspaces for calls of many sizes."""
+and stream are on, copies of the geometry, workspaces for calls of many
+sizes, limits."""
 import copy
 import dataclasses
 import os
@@ -159,3 +160,24 @@ def test_a_workspace_for_all_sizes(gdn, Hk, G, D, dtype):
         assert gdn.attn_prefill_workspace_bytes(g, *bad, up_to=True) == 0
     for bad in ((0, 1), (1, 0), (1, 21)):
         assert gdn.attn_tree_workspace_bytes(g, *bad, up_to=True) == 0
+
+
+def _prefill_status(m, g, n_tokens):
+    """The status of a packed call that is refused for its missing cu_seqlens if for nothing else."""
+    p, row = 0x10000, g.n_kv_heads * g.d_head
+    st = m.lib().gdn_attn_prefill(g._ref(), p, g.n_q_heads * g.d_head, p, row, p, row, None, 1, n_tokens, p, p, p, p, p, 1 << 50, p,
+                                  None, None)
+    return m.lib().gdn_status_string(st).decode(), m.lib().gdn_last_error().decode()
+
+
+def test_lengths_leave_room_for_whole_tiles(gdn):
+    """The most cached and new tokens together, rounded up to tiles with the ones requested ahead, fit 31 bits."""
+    g = gdn.AttnGeometry(n_q_heads=1, n_kv_heads=1, d_head=64, max_pages=(1 << 26) - 1)
+    g.check()
+    most = (1 << 30) - 4096
+    assert g.max_pages * g.page_tokens + most + 4 * 64 < 1 << 31
+    name, message = _prefill_status(gdn, g, most)
+    assert name == "GDN_ERR_NULL" and "cu_seqlens" in message
+    for n in (most + 1, (1 << 30) - 1):
+        name, message = _prefill_status(gdn, g, n)
+        assert name == "GDN_ERR_RANGE" and f"n_tokens: {n}, required: 0..{most}" in message
