@@ -42,6 +42,8 @@ gdn_status check_attn(const gdn_attn_geometry* g) {
     return fail(GDN_ERR_GEOMETRY, "dtype: %d, required: GDN_F32 (0) or GDN_BF16 (1)", g->dtype);
   if (!std::isfinite(g->scale) || g->scale <= 0.f)
     return fail(GDN_ERR_GEOMETRY, "scale: %g, required: finite and > 0", g->scale);
+  if (g->scale > 0x1p127f)  // the kernels take scale log2(e), which has to be finite
+    return fail(GDN_ERR_UNSUPPORTED, "scale: %g, supported by this library: <= 2^127", g->scale);
   if (g->d_head != 64 && g->d_head != 128 && g->d_head != 256)
     return fail(GDN_ERR_UNSUPPORTED, "d_head: %d, supported by this library: 64, 128 or 256", g->d_head);
   if (g->page_tokens % 16 != 0)

@@ -464,7 +464,7 @@ typedef struct gdn_attn_geometry {
   int32_t max_pages;   /* entries of a block-table row; max_pages * P < 2^30 */
   int32_t max_tree;    /* largest node count accepted by gdn_attn_tree (1..64) */
   int32_t dtype;       /* gdn_dtype of q, k, v, o and of the cache */
-  float scale;         /* logits are scale * q.k; finite and > 0 */
+  float scale;         /* logits are scale * q.k; > 0 and <= 2^127 */
 } gdn_attn_geometry;
 
 /* gdn_check_geometry for the attention geometry. */

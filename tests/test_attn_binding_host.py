@@ -181,3 +181,13 @@ def test_lengths_leave_room_for_whole_tiles(gdn):
     for n in (most + 1, (1 << 30) - 1):
         name, message = _prefill_status(gdn, g, n)
         assert name == "GDN_ERR_RANGE" and f"n_tokens: {n}, required: 0..{most}" in message
+
+
+def test_scales_whose_base_2_form_is_not_finite_are_refused(gdn):
+    for scale in (2.0 ** 127, 1e-45):
+        gdn.AttnGeometry(scale=scale).check()
+    for scale in (2.0 ** 127 * (1 + 2.0 ** -23), 3.4e38):
+        with pytest.raises(gdn.GdnError, match="scale: .*supported by this library: <= 2\\^127"):
+            gdn.AttnGeometry(scale=scale).check()
+    with pytest.raises(gdn.GdnError, match="scale: inf, required: finite and > 0"):
+        gdn.AttnGeometry(scale=float("inf")).check()
