@@ -33,11 +33,10 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
     "-Wno-inline-asm",  # m0 in a clobber list
+    # MFMA accumulators in VGPRs: the chained products feed them straight to VALU
+    # code and the next MFMA, so AGPR<->VGPR copies would only add instructions
+    "-mllvm", "-amdgpu-mfma-vgpr-form",
 ]
-# MFMA accumulators in VGPRs: the chained products feed them straight to VALU
-# code and the next MFMA, so AGPR<->VGPR copies would only add instructions.  Not
-# for gdn_attn_bf16.hip, whose kernels of one wave per SIMD need both register files.
-VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Wno-unused-parameter"]
 
 
@@ -70,8 +69,7 @@ def build(verbose: bool = False) -> str:
     for src in HIP_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
-        form = [] if src == "gdn_attn_bf16.hip" else VGPR_FORM
-        jobs.append([hipcc, *HIPCC_FLAGS, *form, *incs, "-c", os.path.join(CSRC, src), "-o", obj])
+        jobs.append([hipcc, *HIPCC_FLAGS, *incs, "-c", os.path.join(CSRC, src), "-o", obj])
     debug_objs = list(objs)
     for src in HOST_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
