@@ -52,7 +52,11 @@ __device__ __forceinline__ float quarter_max(float x) {
 // Bound by the matrix instructions and, as much again, the vector instructions of
 // softmax, addresses and copies between them: 1024 tokens of 8 heads on 2, d 64,
 // behind 4096 cached ones 132 us (73 TFLOP/s; a large fp32 product reaches 154); short prompts (301, 1 and
-// 777 tokens) 30 us, of which the join of the splits is 4.
+// 777 tokens) 30 us, of which the join of the splits is 6.  One of the two arrays
+// of rows in flight lies in private memory (48, 80 and 144 bytes per lane at d 64,
+// 128 and 256), so these rows make a way through it at every step.  Trees: 4 rows of
+// one node at 8K, 24 heads on 4, d 256, 227 us (267 MB, 1.2 TB/s), of 16 nodes 437 us;
+// 64 rows of 8 nodes up to 16K, 32 heads on 8, d 128, 2680 us.
 // ---------------------------------------------------------------------------
 constexpr int kGenRows = 64, kGenKeys = 32, kGenThreads = 256;
 constexpr int kMaxSplits = 64;  // parts of a row
@@ -393,7 +397,9 @@ int64_t row_tiles(int64_t tokens, int n_seqs, int G, int nodes, int bm) {
 // and read once more, and with two per CU 512 tokens of 24 heads on 4, d 256, took
 // 64 us instead of 40, 256 behind 8192 cached ones 102 instead of 77.  At d 64 two
 // workgroups fit and the last part may begin beside others (4096 tokens 88 us in
-// 130 workgroups, 64 us in 260).
+// 130 workgroups, 64 us in 260).  The parts are those of rows that fill their block
+// table: shorter ones leave parts empty.  fp32 trees take the prompts' rule, which
+// was measured on prompts alone.
 int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16, int64_t keys) {
   if (bf16 && nodes > 0) return 1;
   const int64_t wgs = row_tiles(tokens, n_seqs, G, nodes, bf16 && nodes == 0 ? kPromptRows : kGenRows) * Hk;

@@ -19,11 +19,11 @@
 // What bounds it.  Prompts: the matrix instructions and the exponentials, sums
 // and conversions between them, which a wave does in turn; eight waves of one
 // workgroup (two per SIMD) overlap them in part.  24 heads on 4, d 256, one
-// prompt of 8192: 790 us, 1.04 PFLOP/s, where a large library product reaches
-// 1.6; ragged prompts behind prefixes of up to 20011 tokens, 32 heads on 8, d 128:
-// 728 us, 0.97 PFLOP/s.  Rows per wave: 64 (four waves, one per SIMD) took 1452 us
-// on the second, for want of a second wave to overlap with, and at d 256 do not
-// fit the registers.  Two groups of waves that alternate products and weights
+// prompt of 8192: 784 - 846 us by the card, 0.98 - 1.05 PFLOP/s, where a large library
+// product reaches 1.6; ragged prompts behind prefixes of up to 20011 tokens, 32 heads
+// on 8, d 128: 717 - 779 us, 0.91 - 0.98 PFLOP/s.  Rows per wave: 64 (four waves, one
+// per SIMD) took 1452 us on the second, for want of a second wave to overlap with,
+// and at d 256 do not fit the registers.  Two groups of waves that alternate products and weights
 // between barriers: 995 and 1166 us against 785 and 896 then.  Trees: the bytes
 // of K and V (below).
 #include "gdn_attn_device.h"
@@ -334,9 +334,12 @@ struct Tiles {
     }
     __builtin_amdgcn_sched_barrier(0);
   }
-  // Weights of a tile from its logits: rounded to bf16 for the product, each is
-  // off by at most 2^-8 of itself, below the output's own rounding on average
-  // over keys.  The sum takes the rounded weights too, two to an instruction.
+  // Weights of a tile from its logits: rounded to bf16 for the product (what the
+  // matrix instruction takes; fp32 operands run at a sixteenth of its rate), each
+  // off by at most 2^-8 of itself.  Over the keys of a row that stays below the
+  // output's own rounding: outputs are 0.0020 - 0.0023 of their size from the exact
+  // ones, 0.0015 - 0.0017 where the outputs alone are rounded.  The sum takes the
+  // rounded weights too, two to an instruction.
   // MASKED: some row does not attend every key of the tile; S then keeps the
   // unrounded weights.
   template <bool MASKED>
@@ -627,7 +630,10 @@ __host__ __device__ inline size_t tree_meta_offset(const TreeSplit& t, int D) {
 // 24 heads on 4, d 256: 4 rows of one node at 8K 47 us (134 MB, 2.9 TB/s; the
 // join of the shares 6 of them); 4 rows of 16 nodes at 80 - 120K 356 us (1.64 GB,
 // 4.6 TB/s, the rate of a large copy).  32 heads on 8, d 128, 64 rows of 8 nodes
-// up to 16K, 16-token pages: 151 us (0.67 GB, 4.4 TB/s).
+// up to 16K, 16-token pages: 149 us (0.67 GB, 4.5 TB/s).  At d 256 25 - 27 registers
+// of the addresses and row descriptions are spilled: stored once per workgroup,
+// read back between units, and one of them within the tiles, where new page ids are
+// taken (every 1024 keys).
 constexpr int kTreeKeys = 32, kUnitCost = 12;
 template <int D, int RW>
 using TreeTiles = Tiles<D, RW, (RW > 2048 / 256 * D / 256 ? RW : 2048 / 256 * D / 256), kTreeKeys, 4, true>;
