@@ -23,9 +23,9 @@
 // product reaches 1.6; ragged prompts behind prefixes of up to 20011 tokens, 32 heads
 // on 8, d 128: 717 - 779 us, 0.91 - 0.98 PFLOP/s.  Rows per wave: 64 (four waves, one
 // per SIMD) took 1452 us on the second, for want of a second wave to overlap with,
-// and at d 256 do not fit the registers.  Two groups of waves that alternate products and weights
-// between barriers: 995 and 1166 us against 785 and 896 then.  Trees: the bytes
-// of K and V (below).
+// and at d 256 do not fit the registers.  Two groups of waves that alternate
+// products and weights between barriers: 995 and 1166 us against 785 and 896 then.
+// Trees: the bytes of K and V (below).
 #include "gdn_attn_device.h"
 #include "gdn_rank.h"
 

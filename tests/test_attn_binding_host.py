@@ -1,6 +1,5 @@
 """The binding of the paged-cache, attention and tree entry points on the host (no GPU): which device a call's tensors
-and stream are on, copies of the geometry, workspaces for calls of many
-sizes, limits."""
+and stream are on, copies of the geometry, workspaces for calls of many sizes, limits."""
 import copy
 import dataclasses
 import os

@@ -560,3 +560,35 @@ def test_one_workspace_for_calls_of_many_sizes(dtype, D):
         _run_tree(m, geom, pg, dev, par, [100] * b, own, err)
         torch.cuda.synchronize()
         assert int(err.item()) == 0 and torch.isfinite(o).all() and torch.equal(o, own)
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Calls that name a stream run in its order: inputs that arrive on it late are those that they read, and results
+    equal those of the current stream, bit for bit."""
+    ctx, n, new = [70, 33], 3, [50, 90]
+    m, geom, pg, _, dev, par, o = _tree_case(74, ctx, n, 2, 4, 128, 16, BF16)
+    table, c, p = pg.table.cuda(), _cuda(ctx), _cuda(par)
+    _, _, _, _, pdev, cu, po = _prefill_case(75, new, ctx, 2, 4, 128, 16, BF16)
+    cu, slots = _cuda(cu), _cuda(np.arange(geom.n_pages * 16 - 140, geom.n_pages * 16))
+    err, cache = _err(), pg.cache()
+    ws = m.alloc_attn_tree_workspace(geom, 2, n), m.alloc_attn_prefill_workspace(geom, 140, 2)
+
+    def calls(q, pq, out, pout, stream):
+        written = m.KVCache(cache.k.clone(), cache.v.clone())
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+                q.copy_(dev[0], non_blocking=True)
+                pq.copy_(pdev[0], non_blocking=True)
+        m.attn_tree(geom, cache, table, c, q, *dev[1:], p, out, ws[0], dev_err=err, stream=stream)
+        m.attn_prefill(geom, pq, *pdev[1:], cu, pout, ws[1], cache=cache, block_table=table, ctx_len=c, dev_err=err, stream=stream)
+        m.kv_write(geom, written, pout[:, :2], pout[:, 2:4], slots, dev_err=err, stream=stream)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return out, pout, written.k.view(torch.int16), written.v.view(torch.int16)
+
+    here = calls(dev[0], pdev[0], o.clone(), po.clone(), None)
+    late = calls(torch.zeros_like(dev[0]), torch.zeros_like(pdev[0]), o.clone(), po.clone(), torch.cuda.Stream())
+    for a, b in zip(here, late):
+        assert torch.equal(a, b)
