@@ -26,7 +26,7 @@ POS_ONE = 65536
 POS_STRIDE = 32  # int32 words per slot in conv_pos: slot s's position is conv_pos[s, 0]
 CHUNK = 64
 
-ABI_VERSION = 9  # GDN_ABI_VERSION of include/gdn.h that these signatures follow
+ABI_VERSION = 10  # GDN_ABI_VERSION of include/gdn.h that these signatures follow
 DEV_OK = 0
 DEV_BAD_SLOT = 1
 DEV_BAD_ACCEPTED = 2
@@ -71,6 +71,21 @@ class GdnAttnGeometry(ctypes.Structure):
         ("max_tree", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
         ("scale", ctypes.c_float),
+    ]
+
+
+class GdnRope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dims", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("context", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("amplitude", ctypes.c_float),
     ]
 
 
@@ -120,6 +135,13 @@ _SIGS = {
     "gdn_attn_tree": (ctypes.c_int, [_P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P, _P, _P]),
     "gdn_attn_tree_workspace_bytes": (_Z, [_P, _I, _I]),
     "gdn_attn_tree_workspace_max_bytes": (_Z, [_P, _I, _I]),
+    "gdn_check_rope": (ctypes.c_int, [_P, ctypes.c_char_p, _Z]),
+    "gdn_rope_turns": (ctypes.c_int, [_P, _P, _P]),
+    "gdn_rope_rotate": (ctypes.c_int, [_P, _P, _P, _P, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P]),
+    "gdn_attn_weights": (ctypes.c_int, [_P, _P, _L, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _Z, _P, _P]),
+    "gdn_attn_weights_workspace_bytes": (_Z, [_P, _I, _I, _I]),
+    "gdn_evict_plan": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "gdn_kv_move": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I, _I, _P, _P]),
 }
 
 _lib = None
@@ -759,6 +781,214 @@ def attn_tree(geom: AttnGeometry, cache: KVCache, block_table, ctx_len, q, k, v,
                                o.data_ptr(), dev_err.data_ptr(), st))
 
 
+# --------------------------------------------------------------------------
+# rotary positions, and a cache within a budget
+# --------------------------------------------------------------------------
+
+_ROPE_LAYOUTS = {"half": 0, "pairs": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+GDN_ROPE_INVERSE = 1
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Python mirror of gdn_rope (see include/gdn.h for every field); layout "half" or "pairs", scaling "none",
+    "linear", "base" or "parts"."""
+
+    rot_dims: int = 64
+    layout: str = "half"
+    base: float = 1e4
+    scaling: str = "none"
+    factor: float = 1.0
+    context: float = 8192.0
+    low: float = 1.0
+    high: float = 32.0
+    amplitude: float = 1.0
+    inverse: bool = False
+
+    def c_struct(self) -> GdnRope:
+        for name, known in (("layout", _ROPE_LAYOUTS), ("scaling", _ROPE_SCALINGS)):
+            if getattr(self, name) not in known:
+                raise ValueError(f"{name}: {getattr(self, name)!r}, required: one of {', '.join(known)}")
+        return GdnRope(self.rot_dims, _ROPE_LAYOUTS[self.layout], _ROPE_SCALINGS[self.scaling],
+                       GDN_ROPE_INVERSE if self.inverse else 0, self.base, self.factor, self.context, self.low, self.high,
+                       self.amplitude)
+
+    def check(self):
+        _check(lib().gdn_check_rope(self._ref(), None, 0))
+
+    def _ref(self):
+        """The C struct by reference, made once per object (it is frozen)."""
+        r = self.__dict__.get("_c_ref")
+        if r is None:
+            r = ctypes.byref(self.c_struct())
+            object.__setattr__(self, "_c_ref", r)
+        return r
+
+    def __getstate__(self):
+        """What copies and pickles carry: the fields, not this object's C struct."""
+        return {k: v for k, v in self.__dict__.items() if k != "_c_ref"}
+
+
+def _rope_tables(rope: Rope):
+    half = max(rope.rot_dims, 0) // 2
+    freq, turns = (ctypes.c_double * half)(), (ctypes.c_uint64 * half)()
+    _check(lib().gdn_rope_turns(rope._ref(), freq, turns))
+    return freq, turns
+
+
+def rope_frequencies(rope: Rope) -> list:
+    """The scaled frequencies of the pairs, radians per position (gdn_rope_turns)."""
+    return list(_rope_tables(rope)[0])
+
+
+def rope_turns(rope: Rope, device="cuda") -> torch.Tensor:
+    """gdn_rope_turns: the frequencies as 64-bit fractions of a turn (int64 [rot_dims / 2], the bits of uint64), made
+    once and kept by the caller for rope_rotate."""
+    signed = [t - (1 << 64) if t >> 63 else t for t in _rope_tables(rope)[1]]
+    return torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+def rope_rotate(geom: AttnGeometry, rope: Rope, turns, position, q=None, k=None, q_out=None, k_out=None, v=None,
+                cache: Optional[KVCache] = None, slot_map=None, dev_err=None, stream=None):
+    """gdn_rope_rotate: rotary positions of q [n_tokens][H_q][d_head] and/or k [n_tokens][H_kv][d_head] (any row strides);
+    q_out or k_out None: in place.  With a cache, the rotated k and v [n_tokens][H_kv][d_head] also go to the cache slots
+    slot_map (-1 skips).  Without a dev_err, device errors go to ``device_error``'s word."""
+    N, dev = position.shape[0], _index(position)
+    _need(position, "position", (N,), torch.int32, device=dev)
+    _need(turns, "turns", (rope.rot_dims // 2,), torch.int64, device=dev)
+    qp = kp = vp = qo = ko = kc = vc = sm = None
+    qs = ks = vs = qos = kos = 0
+    if q is None and k is None:
+        raise ValueError("q, k: both missing")
+    if q is not None:
+        shape = (N, geom.n_q_heads, geom.d_head)
+        qs = qos = _need_rows(q, "q", shape, geom.dtype, dev)
+        qp = qo = q.data_ptr()
+        if q_out is not None:
+            qos, qo = _need_rows(q_out, "q_out", shape, geom.dtype, dev), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    if k is not None:
+        shape = (N, geom.n_kv_heads, geom.d_head)
+        ks = kos = _need_rows(k, "k", shape, geom.dtype, dev)
+        kp = ko = k.data_ptr()
+        if k_out is not None:
+            kos, ko = _need_rows(k_out, "k_out", shape, geom.dtype, dev), k_out.data_ptr()
+        if cache is not None:
+            _check_cache(geom, cache, dev)
+            vs = _need_rows(v, "v", shape, geom.dtype, dev)
+            _need(slot_map, "slot_map", (N,), torch.int32, device=dev)
+            vp, kc, vc, sm = v.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), slot_map.data_ptr()
+    elif k_out is not None or cache is not None:
+        raise ValueError("k: missing (k_out or cache is given)")
+    if cache is None and (v is not None or slot_map is not None):
+        raise ValueError("cache: missing (v or slot_map is given)")
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
+    st = _here(dev, stream)
+    if dev_err is None:
+        dev_err = _default_err(position.device)
+    _check(lib().gdn_rope_rotate(geom._ref(), rope._ref(), turns.data_ptr(), position.data_ptr(), N, qp, qs, qo, qos, kp, ks,
+                                 ko, kos, vp, vs, kc, vc, sm, dev_err.data_ptr(), st))
+
+
+def attn_weights_workspace_bytes(geom: AttnGeometry, batch: int, n: int, width: int) -> int:
+    """What a call of these sizes needs; it grows with each of them."""
+    return int(lib().gdn_attn_weights_workspace_bytes(geom._ref(), batch, n, width))
+
+
+def alloc_attn_weights_workspace(geom: AttnGeometry, batch: int, n: int, width: int, device="cuda") -> torch.Tensor:
+    """A caller-owned workspace of the size attn_weights_workspace_bytes reports."""
+    return torch.empty(attn_weights_workspace_bytes(geom, batch, n, width), dtype=torch.uint8, device=device)
+
+
+def attn_weights(geom: AttnGeometry, k_cache, block_table, kv_len, q, score_out, workspace, score_in=None, have_len=None,
+                 n_row=None, dev_err=None, stream=None):
+    """gdn_attn_weights: the attention weight that the last n tokens of each row (their queries q
+    [batch][n][H_q][d_head], keys already in k_cache, a KVCache's k) give to its kv_len cached tokens, added to score_in (None:
+    nothing; may be score_out) from 0 to have_len, into score_out [batch][width].  n_row: each row's own n, 0..n.  Without
+    a dev_err, device errors go to ``device_error``'s word."""
+    B, n, dev = q.shape[0], q.shape[1], _index(k_cache)
+    _need(k_cache, "k_cache", (geom.n_pages, geom.n_kv_heads, geom.page_tokens, geom.d_head), geom.dtype, device=dev)
+    _need(block_table, "block_table", (B, geom.max_pages), torch.int32, device=dev)
+    _need(kv_len, "kv_len", (B,), torch.int32, device=dev)
+    qs = _need_rows(q, "q", (B, n, geom.n_q_heads, geom.d_head), geom.dtype, dev)
+    if score_out is None or len(score_out.shape) != 2:
+        raise ValueError("score_out: required: [batch][width]")
+    W = score_out.shape[1]
+    _need(score_out, "score_out", (B, W), torch.float32, device=dev)
+    _need(score_in, "score_in", (B, W), torch.float32, optional=True, device=dev)
+    _need(have_len, "have_len", (B,), torch.int32, optional=True, device=dev)
+    _need(n_row, "n_row", (B,), torch.int32, optional=True, device=dev)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
+    st = _here(dev, stream)
+    ws, nbytes = _workspace(workspace, dev)
+    if dev_err is None:
+        dev_err = _default_err(q.device)
+    _check(lib().gdn_attn_weights(geom._ref(), q.data_ptr(), qs, None if n_row is None else n_row.data_ptr(), B, n,
+                                  k_cache.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(),
+                                  None if have_len is None else have_len.data_ptr(),
+                                  None if score_in is None else score_in.data_ptr(), score_out.data_ptr(), W, ws, nbytes,
+                                  dev_err.data_ptr(), st))
+
+
+def evict_plan(geom: AttnGeometry, kv_len, budget, score, token_pos, row_state, block_table, free_pages, n_free, score_out,
+               token_pos_out, kv_len_out, row_state_out, n_free_out, move_src, move_dst, n_moves, sink: int = 0,
+               recent: int = 0, dev_err=None, stream=None):
+    """gdn_evict_plan: which of each row's kv_len cached tokens stay within its budget (by falling score, the first `sink`
+    positions and the last `recent` tokens before all others), the moves that close the gaps (move_src, move_dst
+    [batch][max_moves] cache slots, n_moves, for kv_move in every layer), the rows' state after them, and the pages that
+    come free.  score_out and token_pos_out may be score and token_pos.  Without a dev_err, device errors go to
+    ``device_error``'s word."""
+    B, dev, i32 = kv_len.shape[0], _index(kv_len), torch.int32
+    if score is None or len(score.shape) != 2 or move_src is None or len(move_src.shape) != 2:
+        raise ValueError("score, move_src: required: [batch][width], [batch][max_moves]")
+    W, M = score.shape[1], move_src.shape[1]
+    _need(kv_len, "kv_len", (B,), i32, device=dev)
+    _need(budget, "budget", (B,), i32, device=dev)
+    _need(score, "score", (B, W), torch.float32, device=dev)
+    _need(token_pos, "token_pos", (B, W), i32, device=dev)
+    _need(row_state, "row_state", (B, 2), i32, device=dev)
+    _need(block_table, "block_table", (B, geom.max_pages), i32, device=dev)
+    _need(free_pages, "free_pages", (geom.n_pages,), i32, device=dev)
+    _need(n_free, "n_free", (1,), i32, device=dev)
+    _need(score_out, "score_out", (B, W), torch.float32, device=dev)
+    _need(token_pos_out, "token_pos_out", (B, W), i32, device=dev)
+    _need(kv_len_out, "kv_len_out", (B,), i32, device=dev)
+    _need(row_state_out, "row_state_out", (B, 2), i32, device=dev)
+    _need(n_free_out, "n_free_out", (1,), i32, device=dev)
+    _need(move_src, "move_src", (B, M), i32, device=dev)
+    _need(move_dst, "move_dst", (B, M), i32, device=dev)
+    _need(n_moves, "n_moves", (B,), i32, device=dev)
+    _need(dev_err, "dev_err", (1,), i32, optional=True, device=dev)
+    st = _here(dev, stream)
+    if dev_err is None:
+        dev_err = _default_err(kv_len.device)
+    _check(lib().gdn_evict_plan(geom._ref(), kv_len.data_ptr(), budget.data_ptr(), score.data_ptr(), token_pos.data_ptr(),
+                                row_state.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), B, W,
+                                sink, recent, score_out.data_ptr(), token_pos_out.data_ptr(), kv_len_out.data_ptr(),
+                                row_state_out.data_ptr(), n_free_out.data_ptr(), move_src.data_ptr(), move_dst.data_ptr(),
+                                n_moves.data_ptr(), M, dev_err.data_ptr(), st))
+
+
+def kv_move(geom: AttnGeometry, cache: KVCache, move_src, move_dst, n_moves, dev_err=None, stream=None):
+    """gdn_kv_move: the K and V rows of evict_plan's moves, in one layer's cache."""
+    dev = _index(cache.k)
+    _check_cache(geom, cache, dev)
+    if move_src is None or len(move_src.shape) != 2:
+        raise ValueError("move_src: required: [batch][max_moves]")
+    B, M = move_src.shape
+    _need(move_src, "move_src", (B, M), torch.int32, device=dev)
+    _need(move_dst, "move_dst", (B, M), torch.int32, device=dev)
+    _need(n_moves, "n_moves", (B,), torch.int32, device=dev)
+    _need(dev_err, "dev_err", (1,), torch.int32, optional=True, device=dev)
+    st = _here(dev, stream)
+    if dev_err is None:
+        dev_err = _default_err(cache.k.device)
+    _check(lib().gdn_kv_move(geom._ref(), cache.k.data_ptr(), cache.v.data_ptr(), move_src.data_ptr(), move_dst.data_ptr(),
+                             n_moves.data_ptr(), B, M, dev_err.data_ptr(), st))
+
+
 __all__ = [
     "Geometry", "GdnGeometry", "GdnError", "SlotPool", "lib", "conv_state_step", "decode_step", "verify_k",
     "rollback", "verify_k_slots", "commit_slots", "prefill_chunked", "prefill_chunked_static", "prefill_workspace_bytes", "alloc_prefill_workspace",
@@ -767,5 +997,6 @@ __all__ = [
     "DEV_INCOMPLETE", "device_error",
     "verify_tree_slots", "AttnGeometry", "GdnAttnGeometry", "KVCache", "kv_plan", "kv_write", "attn_prefill",
     "attn_prefill_workspace_bytes", "alloc_attn_prefill_workspace", "attn_tree", "attn_tree_workspace_bytes",
-    "alloc_attn_tree_workspace", "DEV_BAD_PAGE", "DEV_NO_PAGES", "DEV_BAD_LENGTH", "DEV_BAD_PARENT",
+    "alloc_attn_tree_workspace", "Rope", "GdnRope", "rope_frequencies", "rope_turns", "rope_rotate", "attn_weights",
+    "attn_weights_workspace_bytes", "alloc_attn_weights_workspace", "evict_plan", "kv_move", "DEV_BAD_PAGE", "DEV_NO_PAGES", "DEV_BAD_LENGTH", "DEV_BAD_PARENT",
 ]

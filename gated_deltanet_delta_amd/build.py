@@ -23,8 +23,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 LIB_DEBUG = os.path.join(PKG, "libgdn_debug.so")
 
-HIP_SOURCES = ["gdn_step.hip", "gdn_prefill.hip", "gdn_tree.hip", "gdn_kv.hip", "gdn_attn.hip", "gdn_attn_bf16.hip"]
-HOST_SOURCES = ["gdn_api.cpp", "gdn_attn_api.cpp"]
+HIP_SOURCES = ["gdn_step.hip", "gdn_prefill.hip", "gdn_tree.hip", "gdn_kv.hip", "gdn_attn.hip", "gdn_attn_bf16.hip",
+               "gdn_rope.hip", "gdn_weights.hip", "gdn_evict.hip"]
+HOST_SOURCES = ["gdn_api.cpp", "gdn_attn_api.cpp", "gdn_cache_api.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

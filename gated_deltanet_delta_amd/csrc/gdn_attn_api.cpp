@@ -11,6 +11,10 @@
 
 namespace {
 
+using gdn::check_attn;
+using gdn::check_stride;
+using gdn::check_workspace;
+using gdn::elem;
 using gdn::fail;
 using gdn::launched;
 using gdn::ok;
@@ -19,53 +23,6 @@ constexpr int32_t kMaxLen = (1 << 30) - 1;  // cached tokens of a sequence
 // rows of a packed call: a sequence's cached plus new tokens fit 31 bits, rounded
 // up to whole tiles and with the tiles that are requested ahead of the last
 constexpr int32_t kMaxTokens = (1 << 30) - 4096;
-
-gdn_status check_attn(const gdn_attn_geometry* g) {
-  if (!g) return fail(GDN_ERR_NULL, "attention geometry: NULL, required: a gdn_attn_geometry");
-  if (g->n_kv_heads < 1) return fail(GDN_ERR_GEOMETRY, "n_kv_heads: %d, required: >= 1", g->n_kv_heads);
-  if (g->n_q_heads < 1 || g->n_q_heads % g->n_kv_heads != 0)
-    return fail(GDN_ERR_GEOMETRY, "n_q_heads: %d, required: a multiple of n_kv_heads = %d", g->n_q_heads,
-                g->n_kv_heads);
-  if (g->d_head < 1) return fail(GDN_ERR_GEOMETRY, "d_head: %d, required: >= 1", g->d_head);
-  if (g->page_tokens < 1) return fail(GDN_ERR_GEOMETRY, "page_tokens: %d, required: >= 1", g->page_tokens);
-  if (g->n_pages < 1) return fail(GDN_ERR_GEOMETRY, "n_pages: %d, required: >= 1", g->n_pages);
-  if (g->max_pages < 1) return fail(GDN_ERR_GEOMETRY, "max_pages: %d, required: >= 1", g->max_pages);
-  if (static_cast<int64_t>(g->n_pages) * g->page_tokens > INT32_MAX)
-    return fail(GDN_ERR_GEOMETRY, "n_pages * page_tokens: %lld, required: <= %d",
-                static_cast<long long>(g->n_pages) * g->page_tokens, INT32_MAX);
-  if (static_cast<int64_t>(g->max_pages) * g->page_tokens > kMaxLen)
-    return fail(GDN_ERR_GEOMETRY, "max_pages * page_tokens: %lld, required: <= %d",
-                static_cast<long long>(g->max_pages) * g->page_tokens, kMaxLen);
-  if (g->max_tree < 1 || g->max_tree > 64)
-    return fail(GDN_ERR_GEOMETRY, "max_tree: %d, required: 1..64", g->max_tree);
-  if (g->dtype != GDN_F32 && g->dtype != GDN_BF16)
-    return fail(GDN_ERR_GEOMETRY, "dtype: %d, required: GDN_F32 (0) or GDN_BF16 (1)", g->dtype);
-  if (!std::isfinite(g->scale) || g->scale <= 0.f)
-    return fail(GDN_ERR_GEOMETRY, "scale: %g, required: finite and > 0", g->scale);
-  if (g->scale > 0x1p127f)  // the kernels take scale log2(e), which has to be finite
-    return fail(GDN_ERR_UNSUPPORTED, "scale: %g, supported by this library: <= 2^127", g->scale);
-  if (g->d_head != 64 && g->d_head != 128 && g->d_head != 256)
-    return fail(GDN_ERR_UNSUPPORTED, "d_head: %d, supported by this library: 64, 128 or 256", g->d_head);
-  if (g->page_tokens % 16 != 0)
-    return fail(GDN_ERR_UNSUPPORTED, "page_tokens: %d, supported by this library: a multiple of 16", g->page_tokens);
-  if (g->n_kv_heads > 1024)
-    return fail(GDN_ERR_UNSUPPORTED, "n_kv_heads: %d, supported by this library: <= 1024", g->n_kv_heads);
-  if (g->n_q_heads / g->n_kv_heads > 64)
-    return fail(GDN_ERR_UNSUPPORTED, "n_q_heads/n_kv_heads: %d, supported by this library: <= 64",
-                g->n_q_heads / g->n_kv_heads);
-  return ok();
-}
-
-int elem(const gdn_attn_geometry* g) { return g->dtype == GDN_BF16 ? 2 : 4; }
-
-// A row stride: at least the row, and whole 16-byte vectors.
-gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, const char* name) {
-  const int64_t row = static_cast<int64_t>(heads) * g->d_head;
-  if (stride < row || stride * elem(g) % 16 != 0 || stride >= (1 << 24))
-    return fail(GDN_ERR_RANGE, "%s: %lld, required: >= %lld and < 2^24 elements, and a multiple of 16 bytes", name,
-                static_cast<long long>(stride), static_cast<long long>(row));
-  return GDN_OK;
-}
 
 // own: the largest number of keys that a sequence has among the call's tokens
 int attn_split(const gdn_attn_geometry* g, int64_t tokens, int n_seqs, int nodes, int64_t own, bool cached) {
@@ -114,6 +71,54 @@ gdn::AttnArgs attn_args(const gdn_attn_geometry* g, int32_t n_split, void* works
   return a;
 }
 
+}  // namespace
+
+namespace gdn {
+
+gdn_status check_attn(const gdn_attn_geometry* g) {
+  if (!g) return fail(GDN_ERR_NULL, "attention geometry: NULL, required: a gdn_attn_geometry");
+  if (g->n_kv_heads < 1) return fail(GDN_ERR_GEOMETRY, "n_kv_heads: %d, required: >= 1", g->n_kv_heads);
+  if (g->n_q_heads < 1 || g->n_q_heads % g->n_kv_heads != 0)
+    return fail(GDN_ERR_GEOMETRY, "n_q_heads: %d, required: a multiple of n_kv_heads = %d", g->n_q_heads,
+                g->n_kv_heads);
+  if (g->d_head < 1) return fail(GDN_ERR_GEOMETRY, "d_head: %d, required: >= 1", g->d_head);
+  if (g->page_tokens < 1) return fail(GDN_ERR_GEOMETRY, "page_tokens: %d, required: >= 1", g->page_tokens);
+  if (g->n_pages < 1) return fail(GDN_ERR_GEOMETRY, "n_pages: %d, required: >= 1", g->n_pages);
+  if (g->max_pages < 1) return fail(GDN_ERR_GEOMETRY, "max_pages: %d, required: >= 1", g->max_pages);
+  if (static_cast<int64_t>(g->n_pages) * g->page_tokens > INT32_MAX)
+    return fail(GDN_ERR_GEOMETRY, "n_pages * page_tokens: %lld, required: <= %d",
+                static_cast<long long>(g->n_pages) * g->page_tokens, INT32_MAX);
+  if (static_cast<int64_t>(g->max_pages) * g->page_tokens > kMaxLen)
+    return fail(GDN_ERR_GEOMETRY, "max_pages * page_tokens: %lld, required: <= %d",
+                static_cast<long long>(g->max_pages) * g->page_tokens, kMaxLen);
+  if (g->max_tree < 1 || g->max_tree > 64)
+    return fail(GDN_ERR_GEOMETRY, "max_tree: %d, required: 1..64", g->max_tree);
+  if (g->dtype != GDN_F32 && g->dtype != GDN_BF16)
+    return fail(GDN_ERR_GEOMETRY, "dtype: %d, required: GDN_F32 (0) or GDN_BF16 (1)", g->dtype);
+  if (!std::isfinite(g->scale) || g->scale <= 0.f)
+    return fail(GDN_ERR_GEOMETRY, "scale: %g, required: finite and > 0", g->scale);
+  if (g->scale > 0x1p127f)  // the kernels take scale log2(e), which has to be finite
+    return fail(GDN_ERR_UNSUPPORTED, "scale: %g, supported by this library: <= 2^127", g->scale);
+  if (g->d_head != 64 && g->d_head != 128 && g->d_head != 256)
+    return fail(GDN_ERR_UNSUPPORTED, "d_head: %d, supported by this library: 64, 128 or 256", g->d_head);
+  if (g->page_tokens % 16 != 0)
+    return fail(GDN_ERR_UNSUPPORTED, "page_tokens: %d, supported by this library: a multiple of 16", g->page_tokens);
+  if (g->n_kv_heads > 1024)
+    return fail(GDN_ERR_UNSUPPORTED, "n_kv_heads: %d, supported by this library: <= 1024", g->n_kv_heads);
+  if (g->n_q_heads / g->n_kv_heads > 64)
+    return fail(GDN_ERR_UNSUPPORTED, "n_q_heads/n_kv_heads: %d, supported by this library: <= 64",
+                g->n_q_heads / g->n_kv_heads);
+  return ok();
+}
+
+gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, const char* name) {
+  const int64_t row = static_cast<int64_t>(heads) * g->d_head;
+  if (stride < row || stride * elem(g) % 16 != 0 || stride >= (1 << 24))
+    return fail(GDN_ERR_RANGE, "%s: %lld, required: >= %lld and < 2^24 elements, and a multiple of 16 bytes", name,
+                static_cast<long long>(stride), static_cast<long long>(row));
+  return GDN_OK;
+}
+
 gdn_status check_workspace(const void* workspace, size_t workspace_bytes, size_t need) {
   if (workspace_bytes < need)
     return fail(GDN_ERR_WORKSPACE, "workspace_bytes: %zu, required: >= %zu", workspace_bytes, need);
@@ -121,7 +126,7 @@ gdn_status check_workspace(const void* workspace, size_t workspace_bytes, size_t
   return GDN_OK;
 }
 
-}  // namespace
+}  // namespace gdn
 
 extern "C" {
 

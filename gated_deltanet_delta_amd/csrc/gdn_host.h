@@ -16,6 +16,15 @@ gdn_status ok();
 // GDN_OK for a launch the runtime took (err 0), else GDN_ERR_LAUNCH naming `what`.
 gdn_status launched(int err, const char* what);
 
+// Checks of the attention layers' entry points (defined in gdn_attn_api.cpp): the
+// geometry; a row stride of `heads` heads, at least the row and whole 16-byte
+// vectors; a workspace of `need` bytes.
+gdn_status check_attn(const gdn_attn_geometry* g);
+gdn_status check_stride(const gdn_attn_geometry* g, int64_t stride, int heads, const char* name);
+gdn_status check_workspace(const void* workspace, size_t workspace_bytes, size_t need);
+// Bytes of an element of q, k, v and o.
+inline int elem(const gdn_attn_geometry* g) { return g->dtype == GDN_BF16 ? 2 : 4; }
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace gdn

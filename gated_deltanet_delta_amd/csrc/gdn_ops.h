@@ -1,5 +1,6 @@
 // Arguments and launchers of the attention layers' kernels (gdn_kv.hip,
-// gdn_attn.hip, gdn_attn_bf16.hip) and of the delta rule over trees (gdn_tree.hip).
+// gdn_attn.hip, gdn_attn_bf16.hip, gdn_rope.hip, gdn_weights.hip, gdn_evict.hip) and
+// of the delta rule over trees (gdn_tree.hip).
 #pragma once
 
 #include "gdn_internal.h"
@@ -48,6 +49,50 @@ struct AttnArgs {
   float scale_log2;           // scale * log2(e)
 };
 
+// Rotary positions (gdn_rope.hip).  Strides in bytes.
+struct RopeArgs {
+  const void *q, *k, *v;
+  void *q_out, *k_out, *k_cache, *v_cache;
+  int64_t q_stride, q_out_stride, k_stride, k_out_stride, v_stride;
+  const uint64_t* turns;
+  const int32_t *position, *slot_map;
+  int32_t* dev_err;
+  int32_t n_tokens, Hq, Hk, D, R, page, n_pages;
+  bool inverse;
+  float amplitude;
+};
+
+// Attention weights of cached tokens (gdn_weights.hip).
+struct WeightArgs {
+  const void *q, *k_cache;
+  int64_t q_stride;  // elements between tokens
+  const int32_t *block_table, *kv_len, *have_len, *n_row;
+  const float* score_in;
+  float* score_out;
+  void* workspace;
+  int32_t* dev_err;
+  int32_t batch, n, width;
+  int32_t Hk, G, D, page, n_pages, max_pages;
+  float scale_log2;
+};
+
+// Eviction (gdn_evict.hip).
+struct EvictArgs {
+  const int32_t *kv_len, *budget, *token_pos, *row_state, *block_table, *n_free;
+  const float* score;
+  int32_t* free_pages;
+  float* score_out;
+  int32_t *token_pos_out, *kv_len_out, *row_state_out, *n_free_out, *move_src, *move_dst, *n_moves, *dev_err;
+  int32_t batch, width, sink, recent, max_moves, page, n_pages, max_pages;
+};
+struct MoveArgs {
+  void *k_cache, *v_cache;
+  const int32_t *move_src, *move_dst, *n_moves;
+  int32_t* dev_err;
+  int32_t batch, max_moves, heads, row_bytes, page, n_pages;
+};
+constexpr int kEvictMaxBatch = 4096;
+
 // Launchers: return 0 on success, else the hipError_t value.
 int launch_verify_tree(const TreeArgs& a, bool bf16, void* stream);
 int launch_kv_plan(const KvPlanArgs& a, void* stream);
@@ -61,6 +106,11 @@ int attn_splits(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, boo
 // Workspace of a call: tokens = rows of q (trees: batch x nodes).
 size_t attn_part_bytes(int64_t tokens, int n_seqs, int Hk, int G, int D, int nodes, bool bf16);
 int launch_attn(const AttnArgs& a, bool bf16, void* stream);
+int launch_rope(const RopeArgs& a, bool bf16, bool pairs, void* stream);
+size_t weights_workspace_bytes(int32_t batch, int32_t n, int32_t width, int Hk, int G, int D, bool bf16);
+int launch_weights(const WeightArgs& a, bool bf16, void* stream);
+int launch_evict_plan(const EvictArgs& a, void* stream);
+int launch_kv_move(const MoveArgs& a, void* stream);
 constexpr int kPromptRows = 256;  // rows of a workgroup of the bf16 prompt attention
 int launch_prompt_bf16(const AttnArgs& a, int64_t tiles, void* stream);
 int launch_tree_bf16(const AttnArgs& a, void* stream);

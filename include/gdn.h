@@ -21,7 +21,8 @@
  * rollback is a copy ("Forge: how I wrote my own inference engine and beat
  * llama.cpp", entry of 27 August).  The verify also runs over trees of drafts.
  * For the attention layers of a hybrid stack, at the end of this file: a paged
- * KV cache and attention over it, for prompts and for trees of drafts.
+ * KV cache and attention over it, for prompts and for trees of drafts; rotary
+ * positions; and eviction from the cache by accumulated attention weight.
  *
  * Conventions for every call below
  * --------------------------------
@@ -87,13 +88,14 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 9  /* 4: prefill on the caller's stream alone, workspace independent of n_tokens,
+#define GDN_ABI_VERSION 10 /* 4: prefill on the caller's stream alone, workspace independent of n_tokens,
                               checkpoints at any block size, GDN_DEV_INCOMPLETE;
                               5: gdn_prefill_chunked_static;
                               6: gdn_prefill_timing_events;
                               7: GDN_DEV_DUP_SLOT (debug builds);
                               8: the paged KV cache and the attention over it, verify over a tree of drafts;
-                              9: gdn_attn_prefill_workspace_max_bytes, gdn_attn_tree_workspace_max_bytes */
+                              9: gdn_attn_prefill_workspace_max_bytes, gdn_attn_tree_workspace_max_bytes;
+                              10: rotary positions, attention weights of cached tokens, eviction from the paged KV cache */
 /* bytes of the library's own prefill workspace, one per GPU (gdn_prefill_chunked_static) */
 #define GDN_PREFILL_STATIC_WORKSPACE_BYTES ((size_t)64 << 20)
 #define GDN_POS_ONE 65536
@@ -116,13 +118,13 @@ typedef enum gdn_status {
 #define GDN_DEV_BAD_ACCEPTED 2   /* accepted length outside [0, k] */
 #define GDN_DEV_BAD_SEQLENS 3    /* cu_seqlens[0] != 0, decreasing, or last != n_tokens */
 #define GDN_DEV_WAIT_TIMEOUT 4   /* prefill: a hand-off between its workgroups stalled (bounded wait); outputs invalid */
-#define GDN_DEV_BAD_K 5          /* a row's draft count outside [1, k] */
+#define GDN_DEV_BAD_K 5          /* a row's draft or query count outside its range */
 #define GDN_DEV_INCOMPLETE 6     /* prefill: part of the work was never picked up by a workgroup; outputs invalid */
 #define GDN_DEV_DUP_SLOT 7       /* two rows of one call name the same slot; written only by a library built with
                                     GDN_DEBUG_CHECKS (libgdn_debug.so), which checks this before each call's kernels */
 #define GDN_DEV_BAD_PAGE 8       /* a page id, cache slot or free-page count outside the cache */
 #define GDN_DEV_NO_PAGES 9       /* gdn_kv_plan: the free pages do not suffice for every row */
-#define GDN_DEV_BAD_LENGTH 10    /* a cached or new length that is negative or does not fit the row's block table */
+#define GDN_DEV_BAD_LENGTH 10    /* a length that is negative or does not fit the row's tables, or a budget that cannot be kept */
 #define GDN_DEV_BAD_PARENT 11    /* a tree node's parent outside [-1, node) */
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -573,6 +575,156 @@ gdn_status gdn_attn_tree(const gdn_attn_geometry* g, const void* q, int64_t q_st
                          size_t workspace_bytes, void* o, int32_t* dev_err, void* stream);
 size_t gdn_attn_tree_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n);
 size_t gdn_attn_tree_workspace_max_bytes(const gdn_attn_geometry* g, int32_t max_batch, int32_t max_n);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions of q and k, before attention and before the cache.
+ *
+ * A token at position p turns pair i of the first R dimensions of each head,
+ * i = 0 .. R/2 - 1, by the angle p f_i:
+ *   y_a = A (x_a cos(p f_i) - x_b sin(p f_i)),  y_b = A (x_a sin(p f_i) + x_b cos(p f_i)),
+ * (a, b) = (i, i + R/2) in the half layout and (2i, 2i + 1) in the pairs layout;
+ * dimensions R .. D-1 are copied.  With GDN_ROPE_INVERSE the angle is -p f_i: the
+ * transposed map, which takes a gradient of y to that of x (and undoes a
+ * rotation where A = 1).
+ * Frequencies (radians per position), f_i = base^(-2i/R), scaled for contexts
+ * `factor` = s times as long as trained:
+ *   GDN_ROPE_LINEAR  f_i / s;
+ *   GDN_ROPE_BASE    base replaced by base s^(R/(R-2));
+ *   GDN_ROPE_PARTS   f_i ((1 - g) / s + g), g = (n_i - low) / (high - low) limited to
+ *                    [0, 1], n_i = context f_i / (2 pi) the turns within `context`
+ *                    trained tokens (interpolation by parts, arXiv:2309.00071, section 3.2).
+ * Angles are exact: a frequency is held as a 64-bit fraction of a turn, its
+ * product with the position wraps at whole turns, and what reaches fp32 is at
+ * most an eighth of a turn; so a position's angle is as good at 10^6 as at 1.
+ * ------------------------------------------------------------------------ */
+typedef enum gdn_rope_layout { GDN_ROPE_HALF = 0, GDN_ROPE_PAIRS = 1 } gdn_rope_layout;
+typedef enum gdn_rope_scaling { GDN_ROPE_NONE = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_BASE = 2, GDN_ROPE_PARTS = 3 } gdn_rope_scaling;
+#define GDN_ROPE_INVERSE 1u
+
+typedef struct gdn_rope {
+  int32_t rot_dims;  /* R: a multiple of 16, at most d_head */
+  int32_t layout;    /* gdn_rope_layout */
+  int32_t scaling;   /* gdn_rope_scaling */
+  uint32_t flags;    /* GDN_ROPE_INVERSE */
+  double base;       /* > 1 */
+  double factor;     /* s >= 1 (ignored with GDN_ROPE_NONE) */
+  double context;    /* GDN_ROPE_PARTS: trained tokens, >= 1 */
+  double low, high;  /* GDN_ROPE_PARTS: turns, 0 <= low < high */
+  float amplitude;   /* A: finite, > 0 (1 for a plain rotation) */
+} gdn_rope;
+
+/* gdn_check_geometry for rotary positions (without the head size, which the call brings). */
+gdn_status gdn_check_rope(const gdn_rope* r, char* msg, size_t msg_len);
+
+/*
+ * The frequencies, on the host: freq[i] = f_i (may be NULL), turns[i] = f_i /
+ * (2 pi) of a turn in units of 2^-64, rounded; i < R/2 (both HOST pointers).
+ * The caller copies turns to the device once.  A caller with frequencies of its
+ * own (f_i < 2 pi) makes the table itself.
+ */
+gdn_status gdn_rope_turns(const gdn_rope* r, double* freq, uint64_t* turns);
+
+/*
+ * Rotary positions of n_tokens tokens, and with k_cache != NULL the write of
+ * their rotated k and their v into the cache slots slot_map, as gdn_kv_write
+ * does it (slot -1 is skipped, k_out is written all the same).
+ *   turns uint64 [R/2] (device), position int32 [n_tokens] (device; a negative
+ *   position turns the other way).
+ *   q, q_out rows [H_q][D], k, k_out and v rows [H_kv][D] of g's dtype, each its own row
+ *   stride in elements (limits as above).  q NULL: no q (q_out is then not used); k NULL: no k.
+ *   In place: q_out = q with the same stride, k_out = k likewise; then only the rotated
+ *   dimensions move.  Apart from that no output overlaps an input or another output.
+ *   k_cache NULL: no cache (v_cache, v, slot_map are not used).
+ * All arithmetic is fp32, rounded once; the copied dimensions keep their bits.
+ * A slot outside the cache sets GDN_DEV_BAD_PAGE and is skipped.  Equal slots in one call race.
+ */
+gdn_status gdn_rope_rotate(const gdn_attn_geometry* g, const gdn_rope* r, const uint64_t* turns, const int32_t* position,
+                           int32_t n_tokens, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                           const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, const void* v,
+                           int64_t v_stride, void* k_cache, void* v_cache, const int32_t* slot_map, int32_t* dev_err,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * A cache within a budget: the attention weight that cached tokens receive,
+ * which of them stay, and the moves that close the gaps.  One plan serves all
+ * layers that share block tables: their weights add up in one score array, and
+ * each layer's cache makes the same moves.
+ *
+ *  score      fp32  [batch][width]     weight received so far by the row's cached token j
+ *  token_pos  int32 [batch][width]     position of the row's cached token j, for j < settled
+ *  row_state  int32 [batch][2]         (settled, evicted): tokens j < settled have their position in
+ *                                      token_pos; every other one is at position j + evicted, since tokens
+ *                                      appended after an eviction follow one another.  Zeros for a new request.
+ *
+ * So a row that has evicted e tokens gets its next one at cache index kv_len and
+ * position kv_len + e (gdn_kv_plan's position + e).  Attention does not depend on
+ * the order of cached keys, so what stays is not brought back into order.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Attention weight of cached tokens.  The last n_i of row i's kv_len[i] cached
+ * tokens (n_row[i] in 0..n, or n with n_row NULL) attend as they do in gdn_attn_prefill,
+ * each the tokens up to itself:
+ *   w[j] = sum over t < n_i, heads h of softmax over j' <= kv_len[i] - n_i + t of (scale q[i][t][h] . k[j'])  at j,
+ *   score_out[i][j] = old + w[j],  j < kv_len[i];  old = score_in[i][j] for j < have_len[i], else 0.
+ * score_in NULL: old = 0; have_len NULL: kv_len.  score_out may be score_in.
+ * Rows with n_i = 0 and entries from kv_len[i] on are left as they are.
+ *   q [batch][n][H_q][D] (consecutive tokens one row stride apart, row i starting at
+ *   token i n; only the first n_i of a row are read); 1 <= n <= max_tree; 1 <= batch <= 65535.
+ *   workspace: device, >= gdn_attn_weights_workspace_bytes() of this batch, n and width (it
+ *   grows with each of them); calls that share a workspace must be ordered on one stream.
+ * Logits, weights and sums are fp32, each sum in a fixed order.  Masked keys do not enter, whatever
+ * they hold.  A query whose logits hold a NaN or +inf, or are all -inf, gives NaN to every token it attends.
+ * Device errors: GDN_DEV_BAD_K (n_row) and GDN_DEV_BAD_LENGTH (kv_len outside
+ * [n_i, min(width, max_pages P)], have_len outside [0, kv_len]) leave the row as it is;
+ * GDN_DEV_BAD_PAGE: a page id outside the cache, the row's scores are then not valid.
+ */
+gdn_status gdn_attn_weights(const gdn_attn_geometry* g, const void* q, int64_t q_stride, const int32_t* n_row,
+                            int32_t batch, int32_t n, const void* k_cache, const int32_t* block_table,
+                            const int32_t* kv_len, const int32_t* have_len, const float* score_in, float* score_out,
+                            int32_t width, void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream);
+size_t gdn_attn_weights_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n, int32_t width);
+
+/*
+ * Eviction plan.  A row of c = kv_len[i] cached tokens and budget b = budget[i],
+ * 0 <= b < c, keeps b of them (b < 0 or b >= c: all).  Order of keeping: first tokens whose
+ * position is below `sink` or among the last `recent` (>= c + evicted - recent), then by falling score
+ * (NaN below all, -0 = 0); equals by rising index j.  The kept tokens of index >= b, in order
+ * of their index, move into the indexes below b that are not kept, in order:
+ *   move_src, move_dst int32 [batch][max_moves]: their cache slots before and after, for
+ *     gdn_kv_move; -1 behind the last.  n_moves int32 [batch].
+ *   score_out, token_pos_out [batch][width]: scores and positions at the tokens' indexes after the
+ *     moves, j < kv_len_out[i]; other entries are left as they are.  May be score and token_pos.
+ *   kv_len_out [batch], row_state_out [batch][2] ((b, evicted + c - b) where tokens left, else as before).
+ *   free_pages, n_free, n_free_out: the pages from ceil(b / P) on are pushed, rows in order
+ *     (the stack of gdn_kv_plan).  They hold rows that are still to be moved: gdn_kv_move of every layer comes before
+ *     the next gdn_kv_write.  block_table is not modified; its entries behind ceil(b / P) are no longer the row's.
+ * Pages below a budget must not be shared with another row, since tokens move into them.
+ * Inputs other than free_pages are not modified where the outputs are other buffers (kv_len_out,
+ * row_state_out and n_free_out have to be), so a call can be repeated.
+ * A row with c outside [0, min(width, max_pages P)], settled outside [0, c], evicted < 0 or c + evicted beyond 2^31 - 1
+ * sets GDN_DEV_BAD_LENGTH; it is left as it is, nothing of its score_out and token_pos_out written.  A row to be cut with
+ * b < sink + recent or min(b, c - b) > max_moves sets GDN_DEV_BAD_LENGTH and keeps all its tokens.
+ * GDN_DEV_BAD_PAGE: n_free outside [0, n_pages], or more pages on the stack than the cache has (all rows then keep
+ * all their tokens), or a page id outside the cache (the slots are then -1 and the token is not moved).
+ * 1 <= batch <= 4096, width >= 1, max_moves >= 1, sink, recent >= 0.
+ */
+gdn_status gdn_evict_plan(const gdn_attn_geometry* g, const int32_t* kv_len, const int32_t* budget, const float* score,
+                          const int32_t* token_pos, const int32_t* row_state, const int32_t* block_table,
+                          int32_t* free_pages, const int32_t* n_free, int32_t batch, int32_t width, int32_t sink,
+                          int32_t recent, float* score_out, int32_t* token_pos_out, int32_t* kv_len_out,
+                          int32_t* row_state_out, int32_t* n_free_out, int32_t* move_src, int32_t* move_dst,
+                          int32_t* n_moves, int32_t max_moves, int32_t* dev_err, void* stream);
+
+/*
+ * K and V rows of the moves of gdn_evict_plan, in one layer's cache: for every row i and m <
+ * n_moves[i], all heads of slot move_src[i][m] to slot move_dst[i][m].  A pair with a slot -1 is skipped; a slot
+ * outside the cache sets GDN_DEV_BAD_PAGE and the pair is skipped; n_moves outside [0, max_moves] sets
+ * GDN_DEV_BAD_LENGTH and the row is skipped.  Sources and destinations of one call must all be different slots.
+ */
+gdn_status gdn_kv_move(const gdn_attn_geometry* g, void* k_cache, void* v_cache, const int32_t* move_src,
+                       const int32_t* move_dst, const int32_t* n_moves, int32_t batch, int32_t max_moves,
+                       int32_t* dev_err, void* stream);
 
 #ifdef __cplusplus
 }
