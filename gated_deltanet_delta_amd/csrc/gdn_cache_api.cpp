@@ -57,8 +57,8 @@ gdn_status check_in_place(const void* in, int64_t stride, const void* out, int64
   return GDN_OK;
 }
 
-gdn_status check_width(int32_t width) {
-  if (width < 1 || width > kMaxWidth) return fail(GDN_ERR_RANGE, "width: %d, required: 1..%d", width, kMaxWidth);
+gdn_status check_width(int32_t width, int32_t most) {
+  if (width < 1 || width > most) return fail(GDN_ERR_RANGE, "width: %d, required: 1..%d", width, most);
   return GDN_OK;
 }
 
@@ -168,7 +168,7 @@ gdn_status gdn_rope_rotate(const gdn_attn_geometry* g, const gdn_rope* r, const 
 }
 
 size_t gdn_attn_weights_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n, int32_t width) {
-  if (check_attn(g) != GDN_OK || batch < 1 || batch > 65535 || n < 1 || n > g->max_tree || check_width(width) != GDN_OK)
+  if (check_attn(g) != GDN_OK || batch < 1 || batch > 65535 || n < 1 || n > g->max_tree || check_width(width, kMaxWidth) != GDN_OK)
     return 0;
   return gdn::weights_workspace_bytes(batch, n, width, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head,
                                       g->dtype == GDN_BF16);
@@ -182,7 +182,7 @@ gdn_status gdn_attn_weights(const gdn_attn_geometry* g, const void* q, int64_t q
   if (s != GDN_OK) return s;
   if (n < 1 || n > g->max_tree) return fail(GDN_ERR_RANGE, "n: %d, required: 1..max_tree = %d", n, g->max_tree);
   if (batch < 1 || batch > 65535) return fail(GDN_ERR_RANGE, "batch: %d, required: 1..65535", batch);
-  if ((s = check_width(width)) != GDN_OK) return s;
+  if ((s = check_width(width, kMaxWidth)) != GDN_OK) return s;
   if ((s = check_stride(g, q_stride, g->n_q_heads, "q_stride")) != GDN_OK) return s;
   s = check_workspace(workspace, workspace_bytes, gdn_attn_weights_workspace_bytes(g, batch, n, width));
   if (s != GDN_OK) return s;
@@ -229,7 +229,7 @@ gdn_status gdn_evict_plan(const gdn_attn_geometry* g, const int32_t* kv_len, con
   if (s != GDN_OK) return s;
   if (batch < 1 || batch > gdn::kEvictMaxBatch)
     return fail(GDN_ERR_RANGE, "batch: %d, required: 1..%d", batch, gdn::kEvictMaxBatch);
-  if ((s = check_width(width)) != GDN_OK) return s;
+  if ((s = check_width(width, gdn::kEvictMaxWidth)) != GDN_OK) return s;
   if (max_moves < 1 || max_moves > kMaxWidth)
     return fail(GDN_ERR_RANGE, "max_moves: %d, required: 1..%d", max_moves, kMaxWidth);
   if (sink < 0) return fail(GDN_ERR_RANGE, "sink: %d, required: >= 0", sink);

@@ -2,16 +2,25 @@
 // moves that close the gaps.
 //
 // Plan.  Each token j of a row has a key, its score as an unsigned integer of the same
-// order, the largest for protected tokens; the b that stay are those above the b-th
-// largest key T and, among the tokens with key T, the first by index.  T comes from
-// counts of the keys' upper 11, middle 11 and lower 10 bits, each of the tokens that
-// agree with T in the bits before.  The kept tokens behind the budget fill the gaps
-// below it, both in order, so their numbers are ranks within two ballots: a row that
-// loses e tokens moves min(b, e) at most, whatever its length.
+// order, the largest for protected tokens.  The b tokens that stay are the b largest
+// (key, ~j), found digit by digit from the top: of the tokens that agree with the b-th
+// largest in the digits known, how many have which next digit.  Counts are kept in eight
+// copies, lane l taking copy l % 8, since scores crowd into few digits.  After one digit the
+// tokens left are few and move to a list in LDS; where they do not fit (many equal scores)
+// the row is gone over again.  What stays is a bit per token in LDS; the kept tokens behind
+// the budget fill the gaps below it, both in order, so a pair's number is a rank among bits.
+// A row that loses e tokens moves min(b, e) at most, whatever its length.
 //
-// A workgroup plans one row.  Its keys stay in LDS up to 32768 tokens; the rest are made
-// again from the scores in each of the five passes.  Bound by those passes: scores and
-// positions are read once or from the L2.
+// One workgroup plans one row and needs no memory beside its LDS and the outputs.  A CU
+// issues one vector instruction a cycle for 64 tokens, so what bounds long rows is the
+// number of instructions per token and pass: no branches and no addresses per token, one
+// form of the loads for all steps.  Short rows are bound by latency: chains of loads,
+// barriers between the digits, and the kernel's own instructions, which a launch fetches
+// anew, so all passes take the same code.  us: 4 rows of 8192 20, 64 rows of 500 - 16384
+// 34, 3 rows of 120000 cut to 16384 72.  (Keys of a row gone over in dependent steps, 2048
+// counters in one copy: 27, 39 and 351; a branch per token and counter: 49, 45, 303; loads
+// in a form per kind of step, whose results meet in copies of registers and are waited for
+// there: 22, 34, 104.)
 #include "gdn_attn_device.h"
 
 namespace gdn {
@@ -19,14 +28,22 @@ namespace gdn {
 namespace {
 
 constexpr int kEvictThreads = 1024, kEvictWaves = kEvictThreads / kWave;
-constexpr int kLdsKeys = 32768;
-constexpr uint32_t kZeroKey = 0x80000000u, kProtected = 0xffffffffu;
+constexpr int kKeys = 8;                          // tokens of a thread and step
+constexpr int kStep = kEvictThreads * kKeys;
+constexpr int kWaveTokens = kWave * kKeys;        // a wave's of a step follow one another
+constexpr int kGroupWords = 4;                    // words of the bits whose ranks share one base
+constexpr int kDigits = 2048, kCopies = 8;        // counters: values of a digit, copies of each
+constexpr int kMaxCandidates = 8192;
+constexpr int kFewCandidates = 256;               // ranked by comparing all pairs
+constexpr size_t kEvictLds = 156 << 10;
+// Tokens behind a row's last count as kPast, below every token's key: a row keeps fewer than it has, so none of them stays.
+constexpr uint32_t kPast = 0, kNan = 1, kProtected = 0xffffffffu;
 
-// A score as an unsigned integer of the same order: NaN lowest, -0 = 0.
+// A score as an unsigned integer of the same order: NaN lowest, -0 = 0 (-0 + 0 is 0).
 __device__ __forceinline__ uint32_t score_key(float s) {
-  const uint32_t bits = s == 0.f ? 0u : __float_as_uint(s);
-  if (s != s) return 0;
-  return bits >> 31 ? ~bits : bits | 0x80000000u;
+  const uint32_t bits = __float_as_uint(s + 0.f);
+  const uint32_t key = bits ^ (static_cast<uint32_t>(static_cast<int32_t>(bits) >> 31) | 0x80000000u);
+  return s != s ? kNan : key;
 }
 
 struct EvictRow {
@@ -44,220 +61,472 @@ __device__ __forceinline__ EvictRow evict_row(const EvictArgs& A, int i, bool re
   r.cut = r.cut && !bad;
   return r;
 }
-__device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t page) {
-  return static_cast<int32_t>((static_cast<uint32_t>(tokens) + page - 1) / page);
+__device__ __forceinline__ uint32_t pages_of(int32_t tokens, int32_t page) {
+  return (static_cast<uint32_t>(tokens) + page - 1) / page;
+}
+
+// Digits of (key, n), n = ~j in `n_bits` bits: 11, 11 and 10 bits of the key, 11 of n and the rest.
+constexpr int kAllDigits = 5;
+__device__ __forceinline__ int digit_shift(int d, int n_bits) {
+  return d < 3 ? (d == 0 ? 21 : (d == 1 ? 10 : 0)) : (d == 3 ? (n_bits > 11 ? n_bits - 11 : 0) : 0);
+}
+__device__ __forceinline__ uint32_t digit_mask(int d, int n_bits) {
+  return d < 2 ? 2047 : (d == 2 ? 1023 : (d == 3 ? 2047 : (1u << (n_bits > 11 ? n_bits - 11 : 0)) - 1));
+}
+
+// Inclusive sums over the wave's lanes, which stay at 2^32 - 1 (DPP: shifts within 16 lanes, then the last lane of a
+// row to the next ones).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
+  return __builtin_elementwise_add_sat(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false)));
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = dpp_add<0x111, 0xf>(v);
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);
+  return dpp_add<0x143, 0xc>(v);
+}
+// Bits that any lane has, in every lane.
+__device__ __forceinline__ uint32_t wave_or(uint32_t v) {
+  v |= __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);   // lane ^ 1
+  v |= __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);   // lane ^ 2
+  v |= __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);  // 7 - i within 8 lanes
+  v |= __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);  // 15 - i within 16 lanes
+  return __builtin_amdgcn_readlane(v, 0) | __builtin_amdgcn_readlane(v, 16) | __builtin_amdgcn_readlane(v, 32) |
+         __builtin_amdgcn_readlane(v, 48);
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) { return __builtin_amdgcn_readlane(v, kWave - 1); }
+
+// A buffer of n 32-bit words: words past its end read as 0, without a memory access.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bounded(const void* p, int32_t n) {
+  const uint64_t a = static_cast<uint64_t>(uniform(static_cast<int64_t>(reinterpret_cast<uint64_t>(p))));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a), static_cast<short>(0), uniform(n) * 4, 0x00020000);
+}
+template <class V>
+__device__ __forceinline__ V load_bounded(__amdgpu_buffer_rsrc_t r, int32_t byte) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b32(r, byte, 0, 0));
+}
+
+// The lowest n bits, n of any sign and size.
+__device__ __forceinline__ uint64_t low_bits(int32_t n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
+__device__ __forceinline__ uint64_t uniform_word(uint64_t v) { return static_cast<uint64_t>(uniform(static_cast<int64_t>(v))); }
+// Number of bits of m below this lane's, plus `base`.
+__device__ __forceinline__ uint32_t rank_in(uint64_t m, uint32_t base) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), base));
 }
 
 }  // namespace
 
-__global__ __launch_bounds__(kEvictThreads) void evict_plan_kernel(EvictArgs A) {
-  extern __shared__ uint32_t lds_keys[];
-  __shared__ uint32_t hist[2048];
-  __shared__ int64_t sums[kEvictWaves][2];
-  __shared__ uint32_t waves[kEvictWaves][2];
-  __shared__ uint32_t found[2];
+// LDS of a plan: the bits of `words` 64-token words, a rank per group of them, counters, candidates and one more.
+// page_m: e / page = (2 (e / 16) page_m) >> 32.
+struct EvictPlan {
+  int32_t words, candidates;
+  uint32_t page_m;
+};
+
+__global__ __launch_bounds__(kEvictThreads) void evict_plan_kernel(EvictArgs A, EvictPlan L) {
+  extern __shared__ __align__(16) uint64_t kept[];
+  uint32_t* rank0 = reinterpret_cast<uint32_t*>(kept + L.words);
+  uint32_t* counts = rank0 + L.words / kGroupWords;
+  uint2* candidates = reinterpret_cast<uint2*>(counts + kDigits * kCopies);
+  __shared__ uint32_t sums[3][kEvictWaves], found[3], n_candidates, some_bits, all_bits;
   const int i = blockIdx.x, tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = uniform(tid / kWave);
-  const uint64_t below = (1ull << lane) - 1;
 
   // ---- freed pages of the rows before this one, and of all ----
-  int64_t before = 0, total = 0;
-  for (int r = tid; r < A.batch; r += kEvictThreads) {
-    const EvictRow w = evict_row(A, r, false);
-    const int64_t pages = w.cut ? pages_of(w.c, A.page) - pages_of(w.b, A.page) : 0;
-    total += pages;
-    before += r < i ? pages : 0;
-  }
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    total += __shfl_xor(total, d, kWave);
-    before += __shfl_xor(before, d, kWave);
-  }
-  if (lane == 0) {
-    sums[wave][0] = total;
-    sums[wave][1] = before;
-  }
-  __syncthreads();
-  total = before = 0;
-#pragma unroll
-  for (int w = 0; w < kEvictWaves; ++w) {
-    total += sums[w][0];
-    before += sums[w][1];
-  }
   const int32_t nf = *A.n_free;
-  const bool stack_ok = nf >= 0 && nf + total <= A.n_pages;
-  EvictRow row = evict_row(A, i, tid == 0);
+  uint32_t mine = 0, all = 0;
+#pragma unroll 1
+  for (int r = tid; r < A.batch; r += kEvictThreads) {
+    const EvictRow w = evict_row(A, r, i == 0);
+    const uint32_t pages = w.cut ? pages_of(w.c, A.page) - pages_of(w.b, A.page) : 0;
+    all = __builtin_elementwise_add_sat(all, pages);
+    mine += r < i ? pages : 0;  // of use only if `all` is exact
+  }
+  EvictRow row = evict_row(A, i, false);
+  all = wave_scan(all);
+  mine = wave_scan(mine);
+  if (lane == kWave - 1) {
+    sums[0][wave] = all;
+    sums[1][wave] = mine;
+  }
+  if (tid == 0) {
+    n_candidates = some_bits = 0;
+    all_bits = ~0u;
+  }
+#pragma unroll 1
+  for (int e = tid; e < kDigits * kCopies / 4; e += kEvictThreads) reinterpret_cast<uint4*>(counts)[e] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const uint32_t total = last_lane(wave_scan(lane < kEvictWaves ? sums[0][lane] : 0));
+  const uint32_t before = last_lane(wave_scan(lane < kEvictWaves ? sums[1][lane] : 0));
+  const bool stack_ok = nf >= 0 && static_cast<int64_t>(nf) + total <= A.n_pages;
   if (!stack_ok) row.cut = false;
   const int32_t c = row.c, b = row.cut ? row.b : c;
+  const size_t at = static_cast<size_t>(i) * A.width, list = static_cast<size_t>(i) * A.max_moves;
+  const float* score = A.score + at;
+  const int32_t* token_pos = A.token_pos + at;
+  int32_t moves = 0;
+
+  if (row.cut) {
+    // ---- the threshold, digit by digit ----
+    // protected: positions below `sink` or from `recent` on, that is, outside [sink, recent)
+    const int64_t recent64 = static_cast<int64_t>(c) + row.gone - A.recent;
+    const int32_t recent = static_cast<int32_t>(recent64 > A.sink ? recent64 : A.sink);
+    const uint32_t free_span = static_cast<uint32_t>(recent - A.sink);
+    uint32_t T = 0, N = 0, need = b, knownT = 0, knownN = 0, among = 0;
+    int32_t listed = -1;  // candidates in LDS, -1: they are not
+    const int n_bits = 32 - __builtin_clz(c);  // c >= 1
+    const __amdgpu_buffer_rsrc_t scores = bounded(score, c), positions = bounded(token_pos, row.settled);
+    const uint32_t n_mask = (1u << n_bits) - 1;
+    // Passes over all tokens of the row (or, with the candidates listed, over those).  kCount: counted by their
+    // next digit; kClassify: those above the threshold's known digits stay, those that agree become candidates;
+    // kBits: those from the threshold up stay.
+    enum Pass { kCount, kClassify, kBits };
+    Pass what = b > 0 ? kCount : kBits;
+    if (b == 0) T = N = ~0u;  // above every (key, n)
+    // words of the last group behind the row's
+    if (tid < kGroupWords && (c + 63) / 64 + tid < L.words) kept[(c + 63) / 64 + tid] = 0;
+#pragma unroll 1
+    for (int d = 0;;) {
+      const int shift = digit_shift(d, n_bits);
+      const uint32_t mask = digit_mask(d, n_bits);
+      if (listed >= 0) {
+        const uint32_t of_key = d < 3 ? ~0u : 0u;
+#pragma unroll 1
+        for (int32_t e0 = wave * kWave; e0 < listed; e0 += kEvictThreads) {
+          const uint2 x = candidates[min(e0 + lane, listed - 1)];
+          const uint32_t other = ((x.x ^ T) & knownT) | ((x.y ^ N) & knownN), digit = ((x.x & of_key) | (x.y & ~of_key)) >> shift & mask;
+          atomicAdd(&counts[digit * kCopies + lane % kCopies], e0 + lane < listed && other == 0 ? 1u : 0u);
+        }
+      } else {
+        float s[kKeys];
+        int32_t p[kKeys];
+        // each step's loads are under way while the one before is worked on
+#pragma unroll 1
+        for (int32_t j0 = -kStep; j0 < c; j0 += kStep) {
+          uint32_t key[kKeys];
+          const int32_t first = j0 + wave * kWaveTokens, j = first + lane;  // this wave's first token of the step, this lane's
+          // no token of a plain step is protected, by its index alone
+          auto plain = [&](int32_t f) { return f >= row.settled && f + row.gone >= A.sink && static_cast<uint32_t>(f + row.gone) + kWaveTokens <= static_cast<uint32_t>(recent); };
+          if (j0 >= 0) {
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k) key[k] = score_key(s[k]);
+            if (first + kWaveTokens <= row.settled) {
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k) key[k] = static_cast<uint32_t>(p[k] - A.sink) >= free_span ? kProtected : key[k];
+            } else if (!plain(first)) {
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k) {
+                const int32_t e = j + k * kWave;
+                const uint32_t pos = e < row.settled ? p[k] : static_cast<uint32_t>(e) + row.gone;
+                key[k] = pos - A.sink >= free_span ? kProtected : key[k];
+                key[k] = e < c ? key[k] : kPast;
+              }
+            }
+          }
+          // one form of the loads for all steps: other forms meet in copies of registers, which wait for the loads
+          const int32_t next = (j + kStep) * 4;
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k) s[k] = load_bounded<float>(scores, next + k * kWave * 4);
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k) p[k] = load_bounded<int32_t>(positions, next + k * kWave * 4);
+          if (j0 < 0 || first >= c) continue;
+          const int32_t word = first / 64 + lane;  // lane k stores the bits of tokens first + 64 k on
+          if (what == kCount && d == 0) {
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k) atomicAdd(&counts[(key[k] >> 21) * kCopies + lane % kCopies], 1u);
+          } else if (what == kCount) {
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k) {
+              const uint32_t n = ~(j + k * kWave) & n_mask, other = ((key[k] ^ T) & knownT) | ((n ^ N) & knownN);
+              if (other == 0) atomicAdd(&counts[((d < 3 ? key[k] : n) >> shift & mask) * kCopies + lane % kCopies], 1u);
+            }
+          } else if (what == kClassify) {
+            uint64_t stay = 0, same[kKeys];
+            uint32_t count = 0;
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k) {
+              const uint64_t w = __ballot(key[k] > (T | ~knownT));
+              stay = lane == k ? w : stay;
+              same[k] = __ballot(key[k] - T <= ~knownT);
+              count += __popcll(same[k]);
+            }
+            if (lane < kKeys && word < L.words) kept[word] = stay;
+            if (count != 0) {
+              uint32_t to = 0;
+              if (lane == 0) to = atomicAdd(&n_candidates, count);
+              to = __builtin_amdgcn_readfirstlane(to);
+              // every lane writes, those without a candidate behind the list's end
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k) {
+                const uint32_t rank = rank_in(same[k], to);
+                candidates[__builtin_amdgcn_inverse_ballot_w64(same[k]) && rank < among ? rank : static_cast<uint32_t>(L.candidates)] =
+                    make_uint2(key[k], ~(j + k * kWave) & n_mask);
+                to += __popcll(same[k]);
+              }
+            }
+          } else {
+            uint64_t stay = 0;
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k) {
+              const uint64_t w = __ballot(key[k] > T || (key[k] == T && (~(j + k * kWave) & n_mask) >= N && key[k] != kPast));
+              stay = lane == k ? w : stay;
+            }
+            if (lane < kKeys && word < L.words) kept[word] = stay;
+          }
+        }
+      }
+      __syncthreads();
+      if (what == kBits) break;
+      if (what == kClassify) {
+        listed = among;
+        if (listed <= kFewCandidates) break;
+        uint32_t some = 0, every = ~0u;  // bits that one of the candidates has, that all have
+#pragma unroll 1
+        for (int32_t e = tid; e < listed; e += kEvictThreads) {
+          some |= candidates[e].x;
+          every &= candidates[e].x;
+        }
+        some = wave_or(some);
+        every = ~wave_or(~every);
+        if (lane == 0) {
+          atomicOr(&some_bits, some);
+          atomicAnd(&all_bits, every);
+        }
+        __syncthreads();
+        // digits that all candidates share (equal scores) need no pass
+        const uint32_t varies = some_bits & ~all_bits, shared = varies == 0 ? 0u : ~0u >> __builtin_clz(varies);
+        T |= all_bits & ~shared;
+        while (d < 2 && (~shared >> digit_shift(d + 1, n_bits) & digit_mask(d + 1, n_bits)) == digit_mask(d + 1, n_bits)) {
+          ++d;
+          knownT |= digit_mask(d, n_bits) << digit_shift(d, n_bits);
+        }
+        T &= knownT;
+      } else {
+        // from the highest digit down, two to a thread, which reads and clears their copies: four
+        // times 16 bytes, in an order by lane that spreads them over the banks
+        static_assert(kDigits == 2 * kEvictThreads && kCopies == 8, "two digits to a thread");
+        const int top = kDigits - 1 - 2 * tid;
+        uint4 part[4];
+        uint32_t h[2] = {0, 0};  // of top - 1, top
+        auto copies = [&](int q) -> uint4& { return reinterpret_cast<uint4*>(counts)[(top - 1) * (kCopies / 4) + q]; };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[q] = copies((q + tid / 4) % 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int of = (q + tid / 4) % 4;
+          const uint32_t sum = part[q].x + part[q].y + part[q].z + part[q].w;
+          h[0] += of < 2 ? sum : 0;
+          h[1] += of < 2 ? 0 : sum;
+          copies(of) = make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t inc = wave_scan(h[0] + h[1]);
+        if (lane == kWave - 1) sums[2][wave] = inc;
+        __syncthreads();
+        const uint32_t others = wave_scan(lane < kEvictWaves ? sums[2][lane] : 0);
+        const uint32_t start = wave > 0 ? __builtin_amdgcn_readlane(others, wave - 1) : 0;
+        const uint32_t begin = start + inc - h[0] - h[1], middle = begin + h[1], end = middle + h[0];
+        if (begin < need && need <= end) {
+          const bool high = need <= middle;
+          found[0] = high ? top : top - 1;
+          found[1] = need - (high ? begin : middle);
+          found[2] = high ? h[1] : h[0];
+        }
+        __syncthreads();
+        need = found[1];
+        among = found[2];
+        const uint32_t bits = found[0] << shift, known = mask << shift;
+        if (d < 3) {
+          T |= bits;
+          knownT |= known;
+        } else {
+          N |= bits;
+          knownN |= known;
+        }
+      }
+      if (need == among || d == kAllDigits - 1) {  // the threshold is there, or all of these stay: the digits left are zeros
+        if (listed >= 0) break;
+        what = kBits;
+      } else if (listed < 0 && d < 2 && among <= static_cast<uint32_t>(L.candidates)) {
+        what = kClassify;
+      } else {
+        ++d;
+        what = kCount;
+      }
+    }
+
+    // ---- which of the candidates stay ----
+    if (listed >= 0) {
+#pragma unroll 1
+      for (int32_t e = tid; e < listed; e += kEvictThreads) {
+        const uint2 x = candidates[e];
+        bool stays = x.x > T || (x.x == T && x.y >= N);
+        if (listed <= kFewCandidates) {  // no digits after the list
+          uint32_t above = 0;
+#pragma unroll 4
+          for (int32_t o = 0; o < listed; ++o) {
+            const uint2 y = candidates[o];
+            above += y.x > x.x || (y.x == x.x && y.y > x.y);
+          }
+          stays = above < need;
+        }
+        const uint32_t j = ~x.y & n_mask;
+        if (stays) atomicOr(reinterpret_cast<uint32_t*>(kept) + j / 32, 1u << (j % 32));
+      }
+      __syncthreads();
+    }
+
+    // ---- ranks: gaps below the budget and kept tokens behind it ----
+    const int32_t words = (c + 63) / 64, groups = (words + kGroupWords - 1) / kGroupWords;
+    auto gaps_of = [&](int32_t w) { return ~kept[w] & low_bits(b - 64 * w); };
+    auto movers_of = [&](int32_t w) { return kept[w] & ~low_bits(b - 64 * w); };
+    static_assert((1 << 18) / (64 * kGroupWords) <= kEvictThreads && kEvictMaxWidth <= 1 << 18, "a thread to a group");
+    uint32_t gaps = 0, movers = 0;
+#pragma unroll
+    for (int e = 0; e < kGroupWords; ++e) {
+      const int32_t w = min(tid * kGroupWords + e, words - 1);
+      const bool on = tid * kGroupWords + e < words;
+      gaps += on ? __popcll(gaps_of(w)) : 0;
+      movers += on ? __popcll(movers_of(w)) : 0;
+    }
+    const uint32_t gap_end = wave_scan(gaps), mover_end = wave_scan(movers);
+    if (lane == kWave - 1) {
+      sums[0][wave] = gap_end;
+      sums[1][wave] = mover_end;
+    }
+    __syncthreads();
+    const uint32_t gap_sums = wave_scan(lane < kEvictWaves ? sums[0][lane] : 0);
+    const uint32_t mover_sums = wave_scan(lane < kEvictWaves ? sums[1][lane] : 0);
+    const uint32_t gap0 = gap_end - gaps + (wave > 0 ? __builtin_amdgcn_readlane(gap_sums, wave - 1) : 0);
+    const uint32_t mover0 = mover_end - movers + (wave > 0 ? __builtin_amdgcn_readlane(mover_sums, wave - 1) : 0);
+    // both sums are the same, and fit the lists; the least, so that every entry read below has been written
+    moves = static_cast<int32_t>(min(static_cast<uint32_t>(A.max_moves), min(last_lane(gap_sums), last_lane(mover_sums))));
+    // a group's base: of its gaps where it lies below the budget or holds it (no kept token lies
+    // behind the budget before it), else of its movers
+    const int32_t middle = b / (64 * kGroupWords);
+    if (tid < groups) rank0[tid] = tid <= middle ? gap0 : mover0;
+    __syncthreads();
+
+    // ---- the lists, of indexes for now: a wave takes a group, its tokens in order ----
+    int32_t* src = A.move_src + list;
+    int32_t* dst = A.move_dst + list;
+    const uint32_t last = static_cast<uint32_t>(A.max_moves) - 1;  // (scores that another stream changes meanwhile could make more)
+#pragma unroll 1
+    for (int32_t g = wave; g < groups; g += kEvictWaves) {
+      uint64_t word[kGroupWords];
+#pragma unroll
+      for (int e = 0; e < kGroupWords; ++e) word[e] = uniform_word(kept[g * kGroupWords + e]);
+      uint32_t base = uniform(static_cast<int32_t>(rank0[g]));
+      auto write = [&](int32_t* to, uint64_t marks, int32_t w) {
+        if (__builtin_amdgcn_inverse_ballot_w64(marks)) to[min(rank_in(marks, base), last)] = w * 64 + lane;
+        base += __popcll(marks);
+      };
+      if (g <= middle) {
+#pragma unroll
+        for (int e = 0; e < kGroupWords; ++e) {
+          const int32_t w = g * kGroupWords + e;
+          write(dst, ~word[e] & (g < middle ? ~0ull : low_bits(b - 64 * w)), w);
+        }
+        base = 0;  // of the movers in the group that holds the budget
+      }
+      if (g >= middle) {
+#pragma unroll
+        for (int e = 0; e < kGroupWords; ++e) {
+          const int32_t w = g * kGroupWords + e;
+          write(src, word[e] & (g > middle ? ~0ull : ~low_bits(b - 64 * w)), w);
+        }
+      }
+    }
+  }
+
+  // ---- scores and positions of the tokens that stay where they are ----
+  const int32_t n = row.ok ? b : 0;
+  constexpr int N = kKeys / 2;
+#pragma unroll 1
+  for (int32_t j0 = 0; j0 < n; j0 += N * kEvictThreads) {
+    float s[N];
+    int32_t p[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = score[min(j0 + k * kEvictThreads + tid, n - 1)];
+    if (j0 < row.settled) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) p[k] = token_pos[min(j0 + k * kEvictThreads + tid, n - 1)];
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int32_t j = j0 + k * kEvictThreads + tid;
+      if (j < n && (!row.cut || (kept[j / 64] >> lane & 1))) {
+        A.score_out[at + j] = s[k];
+        A.token_pos_out[at + j] = j < row.settled ? p[k] : j + row.gone;
+      }
+    }
+  }
+  __syncthreads();  // the lists are there for the whole workgroup
+
+  // ---- moves ----
+  const int32_t* table = A.block_table + static_cast<size_t>(i) * A.max_pages;
+  constexpr int M = 2;
+#pragma unroll 1
+  for (int32_t m0 = tid; m0 < moves; m0 += M * kEvictThreads) {
+    int32_t j[M][2], p[M], e[M][2], page[M][2];  // source and destination
+    float s[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      // past the last pair this thread's own first one again: other entries become slots under way
+      const int32_t m = m0 + k * kEvictThreads < moves ? m0 + k * kEvictThreads : m0;
+      j[k][0] = A.move_src[list + m];
+      j[k][1] = A.move_dst[list + m];
+    }
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      s[k] = score[j[k][0]];
+      p[k] = token_pos[j[k][0]];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        e[k][o] = static_cast<int32_t>(__umulhi(static_cast<uint32_t>(j[k][o]) / 16 * 2, L.page_m));
+        page[k][o] = table[e[k][o]];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      const int32_t m = m0 + k * kEvictThreads;
+      if (m < moves) {
+        A.score_out[at + j[k][1]] = s[k];
+        A.token_pos_out[at + j[k][1]] = j[k][0] < row.settled ? p[k] : j[k][0] + row.gone;
+        int32_t slot[2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const bool ok = page[k][o] >= 0 && page[k][o] < A.n_pages;
+          slot[o] = ok ? page[k][o] * A.page + (j[k][o] - e[k][o] * A.page) : -1;
+        }
+        if (slot[0] < 0 || slot[1] < 0) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+        A.move_src[list + m] = slot[0];
+        A.move_dst[list + m] = slot[1];
+      }
+    }
+  }
+#pragma unroll 1
+  for (int32_t m = moves + tid; m < A.max_moves; m += kEvictThreads) A.move_src[list + m] = A.move_dst[list + m] = -1;
+
+  // ---- pages behind the budget: onto the stack ----
+  const int32_t first = row.cut ? pages_of(b, A.page) : 0, freed = row.cut ? pages_of(c, A.page) - first : 0;
+#pragma unroll 1
+  for (int32_t e = tid; e < freed; e += kEvictThreads) {
+    const int32_t page = table[first + e];
+    if (page < 0 || page >= A.n_pages) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+    A.free_pages[static_cast<int64_t>(nf) + before + e] = page;
+  }
   if (tid == 0) {
+    A.n_moves[i] = moves;
+    A.kv_len_out[i] = b;
+    A.row_state_out[2 * i] = row.cut ? b : row.settled;
+    A.row_state_out[2 * i + 1] = row.cut ? row.gone + (c - b) : row.gone;
     if (i == 0) {
       *A.n_free_out = stack_ok ? static_cast<int32_t>(nf + total) : nf;
       if (!stack_ok) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
     }
-    A.kv_len_out[i] = b;
-    A.row_state_out[2 * i] = row.cut ? b : row.settled;
-    A.row_state_out[2 * i + 1] = row.cut ? row.gone + (c - b) : row.gone;
-    if (!row.cut) A.n_moves[i] = 0;
-  }
-  const size_t at = static_cast<size_t>(i) * A.width, list = static_cast<size_t>(i) * A.max_moves;
-  const int32_t* table = A.block_table + static_cast<size_t>(i) * A.max_pages;
-  auto position = [&](int32_t j) { return j < row.settled ? A.token_pos[at + j] : j + row.gone; };
-  if (!row.cut) {
-    for (int32_t j = tid; row.ok && j < c; j += kEvictThreads) {
-      const int32_t p = position(j);
-      A.score_out[at + j] = A.score[at + j];
-      A.token_pos_out[at + j] = p;
-    }
-    for (int32_t m = tid; m < A.max_moves; m += kEvictThreads) A.move_src[list + m] = A.move_dst[list + m] = -1;
-    return;
-  }
-
-  // ---- keys ----
-  const int64_t recent_from = static_cast<int64_t>(c) + row.gone - A.recent;
-  auto make_key = [&](int32_t j) {
-    const int32_t p = position(j);
-    return p < A.sink || p >= recent_from ? kProtected : score_key(A.score[at + j]);
-  };
-  const int32_t in_lds = min(c, kLdsKeys);
-  for (int32_t j = tid; j < in_lds; j += kEvictThreads) lds_keys[j] = make_key(j);
-  __syncthreads();
-  auto key_at = [&](int32_t j) { return j < kLdsKeys ? lds_keys[j] : make_key(j); };
-
-  // ---- the b-th largest key, and how many of its equals stay ----
-  uint32_t T = 0, need = b;
-  if (b == 0) {
-    T = kProtected;
-  } else {
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : 2048;
-      const uint32_t known = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
-      for (int e = tid; e < 2048; e += kEvictThreads) hist[e] = 0;
-      __syncthreads();
-      for (int32_t j0 = wave * kWave; j0 < c; j0 += kEvictThreads) {
-        const int32_t j = j0 + lane;
-        const uint32_t key = j < c ? key_at(j) : 0;
-        const bool in = j < c && ((key ^ T) & known) == 0;
-        // the two keys that many tokens share take one addition per wave
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t often = k == 0 ? kZeroKey : kProtected;
-          const uint64_t same = __ballot(in && key == often);
-          if (same != 0 && lane == 0) atomicAdd(&hist[(often >> shift) & (bins - 1)], __popcll(same));
-        }
-        if (in && key != kZeroKey && key != kProtected) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
-      }
-      __syncthreads();
-      // from the highest bin down, two per thread
-      const int top = bins - 1 - 2 * tid;
-      const uint32_t h0 = top >= 0 ? hist[top] : 0, h1 = top >= 1 ? hist[top - 1] : 0;
-      uint32_t inc = h0 + h1;
-#pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) {
-        const uint32_t up = __shfl_up(inc, d, kWave);
-        if (lane >= d) inc += up;
-      }
-      if (lane == kWave - 1) waves[wave][0] = inc;
-      __syncthreads();
-      uint32_t start = inc - h0 - h1;
-      for (int w = 0; w < wave; ++w) start += waves[w][0];
-      if (start < need && need <= start + h0) {
-        found[0] = top;
-        found[1] = need - start;
-      } else if (start + h0 < need && need <= start + h0 + h1) {
-        found[0] = top - 1;
-        found[1] = need - start - h0;
-      }
-      __syncthreads();
-      T |= found[0] << shift;
-      need = found[1];
-    }
-  }
-
-  // ---- ranks: a wave takes a run of tokens, 64 at a time ----
-  const int32_t run = static_cast<int32_t>((static_cast<uint32_t>(c) + kEvictThreads - 1) / kEvictThreads) * kWave;
-  const int64_t from = static_cast<int64_t>(wave) * run;
-  const int32_t lo = static_cast<int32_t>(from < c ? from : c), hi = static_cast<int32_t>(from + run < c ? from + run : c);
-  uint32_t equals = 0;
-  for (int32_t j0 = lo; j0 < hi; j0 += kWave) equals += __popcll(__ballot(j0 + lane < c && key_at(j0 + lane) == T));
-  if (lane == 0) waves[wave][0] = equals;
-  __syncthreads();
-  uint32_t equal0 = 0;
-  for (int w = 0; w < wave; ++w) equal0 += waves[w][0];
-  __syncthreads();
-  // f(j, within the row, kept) for the run
-  auto walk = [&](auto f) {
-    uint32_t rank0 = equal0;
-    for (int32_t j0 = lo; j0 < hi; j0 += kWave) {
-      const int32_t j = j0 + lane;
-      const uint32_t key = j < c ? key_at(j) : 0;
-      const uint64_t same = __ballot(j < c && key == T);
-      f(j, j < c, j < c && (key > T || (key == T && rank0 + __popcll(same & below) < need)));
-      rank0 += __popcll(same);
-    }
-  };
-  uint32_t holes = 0, movers = 0;
-  walk([&](int32_t j, bool in, bool keep) {
-    holes += __popcll(__ballot(in && j < b && !keep));
-    movers += __popcll(__ballot(j >= b && keep));
-  });
-  if (lane == 0) {
-    waves[wave][0] = holes;
-    waves[wave][1] = movers;
-  }
-  __syncthreads();
-  uint32_t hole0 = 0, mover0 = 0, count = 0;
-  for (int w = 0; w < kEvictWaves; ++w) {
-    if (w < wave) {
-      hole0 += waves[w][0];
-      mover0 += waves[w][1];
-    }
-    count += waves[w][0];
-  }
-  // the lists, of indexes for now; what stays where it is
-  walk([&](int32_t j, bool in, bool keep) {
-    const bool hole = in && j < b && !keep, mover = j >= b && keep;
-    const uint64_t hs = __ballot(hole), ms = __ballot(mover);
-    if (hole) A.move_dst[list + hole0 + __popcll(hs & below)] = j;
-    if (mover) A.move_src[list + mover0 + __popcll(ms & below)] = j;
-    if (keep && j < b) {
-      const int32_t p = position(j);
-      A.score_out[at + j] = A.score[at + j];
-      A.token_pos_out[at + j] = p;
-    }
-    hole0 += __popcll(hs);
-    mover0 += __popcll(ms);
-  });
-  __syncthreads();  // the lists are there for the whole workgroup
-
-  // ---- moves ----
-  auto slot_of = [&](int32_t j) {
-    const int32_t e = j / A.page, page = table[e];
-    if (page < 0 || page >= A.n_pages) {
-      report_error(A.dev_err, GDN_DEV_BAD_PAGE);
-      return -1;
-    }
-    return page * A.page + (j - e * A.page);
-  };
-  for (int32_t m = tid; m < A.max_moves; m += kEvictThreads) {
-    int32_t src = -1, dst = -1;
-    if (m < static_cast<int32_t>(count)) {
-      const int32_t j = A.move_src[list + m], h = A.move_dst[list + m], p = position(j);
-      A.score_out[at + h] = A.score[at + j];
-      A.token_pos_out[at + h] = p;
-      src = slot_of(j);
-      dst = slot_of(h);
-    }
-    A.move_src[list + m] = src;
-    A.move_dst[list + m] = dst;
-  }
-  if (tid == 0) A.n_moves[i] = static_cast<int32_t>(count);
-
-  // ---- pages behind the budget: onto the stack ----
-  const int32_t first = pages_of(b, A.page), freed = pages_of(c, A.page) - first;
-  for (int32_t e = tid; e < freed; e += kEvictThreads) {
-    const int32_t page = table[first + e];
-    if (page < 0 || page >= A.n_pages) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
-    A.free_pages[nf + before + e] = page;
   }
 }
 
@@ -294,8 +563,19 @@ __global__ __launch_bounds__(256) void kv_move_kernel(MoveArgs A) {
 }
 
 int launch_evict_plan(const EvictArgs& a, void* stream) {
-  const size_t lds = static_cast<size_t>(a.width < kLdsKeys ? a.width : kLdsKeys) * sizeof(uint32_t);
-  hipLaunchKernelGGL(evict_plan_kernel, dim3(a.batch), dim3(kEvictThreads), lds, static_cast<hipStream_t>(stream), a);
+  EvictPlan l{};
+  l.words = (a.width + 1023) / 1024 * (4 * kGroupWords);  // what follows the ranks is 16-byte aligned
+  const size_t fixed = static_cast<size_t>(l.words) * (sizeof(uint64_t) + sizeof(uint32_t) / kGroupWords) +
+                       kDigits * kCopies * sizeof(uint32_t);
+  static_assert((kEvictMaxWidth / 64) * 9 + kDigits * kCopies * 4 + kFewCandidates * 8 + 8 < kEvictLds, "the longest rows fit");
+  const size_t room = (kEvictLds - fixed) / sizeof(uint2) - 1, most = room < kMaxCandidates ? room : kMaxCandidates;
+  l.candidates = static_cast<int32_t>(static_cast<size_t>(a.width) < most ? a.width : most);
+  // in units of 16 tokens: x / q = (2 x m) >> 32 with m = ceil(2^31 / q) for x (q - 1) < 2^31; x < 2^14, so
+  // larger q give 0 as 2^14 does
+  const uint32_t q = a.page / 16 < (1 << 14) ? a.page / 16 : 1 << 14;
+  l.page_m = static_cast<uint32_t>(((1ull << 31) + q - 1) / q);
+  hipLaunchKernelGGL(evict_plan_kernel, dim3(a.batch), dim3(kEvictThreads), fixed + (l.candidates + 1) * sizeof(uint2),
+                     static_cast<hipStream_t>(stream), a, l);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -91,7 +91,7 @@ struct MoveArgs {
   int32_t* dev_err;
   int32_t batch, max_moves, heads, row_bytes, page, n_pages;
 };
-constexpr int kEvictMaxBatch = 4096;
+constexpr int kEvictMaxBatch = 4096, kEvictMaxWidth = 1 << 18;  // width: a bit per token in LDS
 
 // Launchers: return 0 on success, else the hipError_t value.
 int launch_verify_tree(const TreeArgs& a, bool bf16, void* stream);

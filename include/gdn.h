@@ -707,7 +707,7 @@ size_t gdn_attn_weights_workspace_bytes(const gdn_attn_geometry* g, int32_t batc
  * b < sink + recent or min(b, c - b) > max_moves sets GDN_DEV_BAD_LENGTH and keeps all its tokens.
  * GDN_DEV_BAD_PAGE: n_free outside [0, n_pages], or more pages on the stack than the cache has (all rows then keep
  * all their tokens), or a page id outside the cache (the slots are then -1 and the token is not moved).
- * 1 <= batch <= 4096, width >= 1, max_moves >= 1, sink, recent >= 0.
+ * 1 <= batch <= 4096, 1 <= width <= 2^18, max_moves >= 1, sink, recent >= 0.
  */
 gdn_status gdn_evict_plan(const gdn_attn_geometry* g, const int32_t* kv_len, const int32_t* budget, const float* score,
                           const int32_t* token_pos, const int32_t* row_state, const int32_t* block_table,

@@ -227,6 +227,7 @@ int main(void) {
     CHECK(71, E(&g, 0, 100, 0, 0, 10) == GDN_ERR_RANGE && has("batch: 0"));
     CHECK(72, E(&g, 4097, 100, 0, 0, 10) == GDN_ERR_RANGE && has("batch: 4097, required: 1..4096"));
     CHECK(73, E(&g, 4, 0, 0, 0, 10) == GDN_ERR_RANGE && has("width: 0"));
+    CHECK(78, E(&g, 4, (1 << 18) + 1, 0, 0, 10) == GDN_ERR_RANGE && has("width: 262145, required: 1..262144"));
     CHECK(74, E(&g, 4, 100, -1, 0, 10) == GDN_ERR_RANGE && has("sink: -1"));
     CHECK(75, E(&g, 4, 100, 0, -1, 10) == GDN_ERR_RANGE && has("recent: -1"));
     CHECK(76, E(&g, 4, 100, 0, 0, 0) == GDN_ERR_RANGE && has("max_moves: 0"));
