@@ -6,14 +6,22 @@
 // weights of one key are a column of the softmax, whose normaliser is known only once
 // a query has seen all its keys, so there are three steps: maximum and sum of every
 // (query, part of the keys); their join to one lse per query; the sums per key.
-// V does not enter, so K is all that has to be read, and K is read once: at most 32 rows
-// (queries of one KV head) store their logits for the last step, 4 bytes each
-// beside a key's 2 D or 4 D; more rows compute them again.
+// V does not enter, so K is all that has to be read.  At most 32 rows (queries of one KV
+// head) store their logits for the last step, 4 bytes each beside a key's 2 D or 4 D, and K is
+// read once; more rows compute them again, from K read a second time.
 //
 // K goes from memory to registers as it lies (each lane 16 bytes of one key per step,
 // the A or B operand of a 32 x 32 matrix instruction) and Q comes from LDS, where it
 // lies in the order of the operands.  A wave owns its keys and walks over the rows,
-// so waves share nothing but Q.  In base 2: z log2(e) is what is stored and compared.
+// so waves share nothing but Q, and one wave's loads hide behind the others' products.
+// In base 2: z log2(e) is what is stored and compared.
+//
+// Bound by bytes.  24 heads on 4, d 256: one query at 4 x 8K tokens 23 us (67 MB: 15.6 us for
+// the logits, 4.3 TB/s, 5.5 for the sums), 32 queries over 4 x 100K 407 us (820 MB twice, 4.0
+// TB/s); 32 heads on 8, d 128, 4 queries in each of 64 ragged rows 116 us (303 MB of K, 190 MB of
+// logits written and read).  Many rows, measured and dropped: 64 keys per wave in 8
+// waves instead of 32 in 16, 580 us; workgroups of a fixed number of keys, 473; one group of
+// heads at a time, so that the second reading might find K in the last-level cache, 512 - 940.
 #include "gdn_attn_device.h"
 
 namespace gdn {
@@ -49,25 +57,42 @@ __device__ __forceinline__ float half_sum(float x) {
 
 // Sizes of a call, the same on the host and on the device.
 struct WeightPlan {
-  int32_t R, row_tiles, Rp;    // rows of a KV head (n G), tiles of 32 of them, rows in whole tiles
-  int32_t part_keys, parts;    // keys of a part, parts of a row of `width` tokens
-  int32_t W;                   // row length of the logits or sums: width in whole tiles of keys
-  bool stored;                 // logits are stored
-  size_t lse, keys, total;     // byte offsets of lse [batch][Hk][Rp] and of the logits [batch][Hk][R][W] or
-                               // the heads' sums [batch][Hk][W]; (max, sum) [batch][Hk][parts][Rp] is at 0
+  int32_t R, row_tiles, Rp;  // rows of a KV head (n G), tiles of 32 of them, rows in whole tiles
+  int32_t W;                 // row length of the logits or sums: width in whole tiles of keys
+  int32_t parts;             // few rows: parts (of kStoredKeys keys) of a row of `width` tokens
+  int32_t workgroups;        // many rows: those that share the keys
+  bool stored;               // few rows: logits are stored
+  // byte offsets; (maximum, sum) of a row over a part at 0, [unit][parts][Rp] or [unit + workgroup][Rp], a unit being a
+  // KV head of a batch row; many rows: (first workgroup, number of them) of each unit; few rows: lse
+  // [unit][Rp]; the logits [unit][R][W] or the heads' sums [unit][W]
+  size_t meta, lse, keys, total;
 };
 
 constexpr int kTileKeys = 32;
-// Few rows: keys of a wave, and waves of a workgroup
-constexpr int kStoredKeys = 64, kStoredWaves = 4;
-// Many rows: 32-key blocks that a wave holds in registers (a Q operand then serves as many
-// instructions), tiles that it takes one after the other, waves of a workgroup
-constexpr int many_blocks(int D, bool bf16) { return D * (bf16 ? 2 : 4) <= 512 ? 2 : 1; }
-constexpr int kManyTiles = 2, kManyWaves = 8;
-// Row tiles whose Q lies in LDS at a time: 128 KB
-constexpr int many_row_tiles(int D, bool bf16) { return (128 << 10) / (32 * D * (bf16 ? 2 : 4)); }
+// Few rows: waves of a workgroup, a tile of keys each
+constexpr int kStoredWaves = 4, kStoredKeys = kStoredWaves * kTileKeys;
+// Few rows: parts of a batch row's KV heads, and of all rows', up to which the last kernel joins them itself, a
+// launch less against a join per 64 keys.  24 heads on 4, d 256, us with a kernel for the join / without: 4
+// rows of 4000 tokens (128 parts) 18.7 / 16.7, of 8000 25.5 / 23.1, of 16000 42.9 / 43.4; 64 rows of 4000 129 / 132, of
+// 8000 245 / 262; 16 rows of 4000, 8 KV heads 69.0 / 67.6.
+constexpr int kFewParts = 320, kFewPartsAll = 4096;
+// Many rows: waves of a workgroup, as the registers allow (a tile's K takes D / 4 (bf16) or D / 2 of them), and
+// what they take at a time, a step of the keys
+constexpr int many_waves(int D, bool bf16) { return D * (bf16 ? 2 : 4) <= 512 ? 16 : 8; }
+constexpr int many_keys(int D, bool bf16) { return many_waves(D, bf16) * kTileKeys; }
+// Row tiles whose Q lies in LDS at a time: 112 KB, and no more than 8 (each has 8 bytes per row and wave beside it)
+constexpr int many_row_tiles(int D, bool bf16) {
+  const int fit = (112 << 10) / (32 * D * (bf16 ? 2 : 4));
+  return fit < 8 ? fit : 8;
+}
 
 __host__ __device__ inline size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+// LDS of the many-row kernels: Q, and (maximum, sum) of each row and wave.
+size_t many_lds(int row_tiles, int D, bool bf16) {
+  const int rt = row_tiles < many_row_tiles(D, bf16) ? row_tiles : many_row_tiles(D, bf16);
+  return static_cast<size_t>(rt) * 32 * (D * (bf16 ? 2 : 4) + many_waves(D, bf16) * sizeof(float2));
+}
 
 WeightPlan weight_plan(int32_t batch, int32_t n, int32_t width, int Hk, int G, int D, bool bf16) {
   WeightPlan p{};
@@ -75,12 +100,14 @@ WeightPlan weight_plan(int32_t batch, int32_t n, int32_t width, int Hk, int G, i
   p.row_tiles = (p.R + 31) / 32;
   p.Rp = p.row_tiles * 32;
   p.stored = p.row_tiles == 1;
-  p.part_keys = p.stored ? kStoredKeys : kTileKeys * many_blocks(D, bf16);
-  p.parts = static_cast<int32_t>((static_cast<int64_t>(width) + p.part_keys - 1) / p.part_keys);
+  p.parts = static_cast<int32_t>((static_cast<int64_t>(width) + kStoredKeys - 1) / kStoredKeys);
+  // one or two workgroups per CU, as LDS and 32 waves allow
+  p.workgroups = many_lds(p.row_tiles, D, bf16) <= (78 << 10) ? 512 : 256;
   p.W = static_cast<int32_t>(round_up(width, 64));
   const size_t units = static_cast<size_t>(batch) * Hk;
-  p.lse = round_up(units * p.parts * p.Rp * sizeof(float2), 256);
-  p.keys = p.lse + round_up(units * p.Rp * sizeof(float), 256);
+  p.meta = round_up((p.stored ? units * p.parts : units + p.workgroups) * p.Rp * sizeof(float2), 256);
+  p.lse = p.meta + round_up(p.stored ? 0 : units * sizeof(int2), 256);
+  p.keys = p.lse + round_up(p.stored ? units * p.Rp * sizeof(float) : 0, 256);
   p.total = p.keys + units * (p.stored ? p.R : 1) * p.W * sizeof(float);
   return p;
 }
@@ -89,7 +116,7 @@ WeightPlan weight_plan(int32_t batch, int32_t n, int32_t width, int Hk, int G, i
 struct WeightRow {
   int32_t n, kv;
 };
-__device__ __forceinline__ WeightRow weight_row(const WeightArgs& A, int i, bool report) {
+__device__ __forceinline__ WeightRow any_row(const WeightArgs& A, int i, bool report) {
   WeightRow r{A.n_row ? A.n_row[i] : A.n, A.kv_len[i]};
   if (r.n < 0 || r.n > A.n) {
     if (report) report_error(A.dev_err, GDN_DEV_BAD_K);
@@ -101,25 +128,95 @@ __device__ __forceinline__ WeightRow weight_row(const WeightArgs& A, int i, bool
       r.n = 0;
     }
   }
+  return r;
+}
+__device__ __forceinline__ WeightRow weight_row(const WeightArgs& A, int i, bool report) {
+  const WeightRow r = any_row(A, i, report);
   return WeightRow{uniform(r.n), uniform(r.kv)};
 }
 
-// Q of row tiles [t0, t0 + tiles) of KV head h of row i, in the order of the operands:
-// [tile][step][lane] of 16 bytes.  Rows past the last are zeros.
-template <int D, bool BF16, int THREADS>
-__device__ __forceinline__ void load_q(const WeightArgs& A, int i, int h, int32_t rows, int t0, int tiles, uint4* lds) {
-  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32;
-  for (int e = threadIdx.x; e < tiles * STEPS * 64; e += THREADS) {
-    const int lane = e % 64, s = e / 64 % STEPS, r = (t0 + e / 64 / STEPS) * 32 + lane % 32;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const int t = r / A.G;
-      const char* q = static_cast<const char*>(A.q) +
-                      ((static_cast<int64_t>(i) * A.n + t) * A.q_stride + static_cast<int64_t>(h * A.G + r - t * A.G) * D) * ES;
-      v = *reinterpret_cast<const uint4*>(q + (2 * s + lane / 32) * 16);
+// A workgroup's share of the keys of a unit: steps [lo, hi) of its `steps`; `place` + lo is where it begins on the
+// line of all units' steps.
+struct Share {
+  int i, h;
+  WeightRow row;
+  int32_t lo, hi, steps;
+  int64_t place;
+};
+// The steps of all units lie on one line, row by row and head by head, and workgroup w of W = min(grid, total)
+// takes places [w total / W, (w + 1) total / W), whatever the rows' lengths: f(share, w, W, total) for
+// every unit that it has a part of, in order.  All waves together.
+template <int KEYS, class F>
+__device__ __forceinline__ void each_share(const WeightArgs& A, bool report, F f) {
+  const int lane = threadIdx.x & 63;
+  auto steps_of = [&](const WeightRow& r) { return r.n > 0 ? (r.kv + KEYS - 1) / KEYS : 0; };
+  // inclusive sum over the lanes of the places of rows base + lane
+  auto scan = [&](int base, int64_t* mine, bool tell) {
+    const bool in = base + lane < A.batch;
+    const WeightRow r = in ? any_row(A, base + lane, tell) : WeightRow{0, 0};
+    int64_t inc = *mine = static_cast<int64_t>(steps_of(r)) * A.Hk;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t up = __shfl_up(inc, d, 64);
+      if (lane >= d) inc += up;
     }
-    lds[e] = v;
+    return inc;
+  };
+  int64_t total = 0, mine = 0, inc = 0;
+  for (int base = 0; base < A.batch; base += 64) {
+    inc = scan(base, &mine, report);
+    total += __shfl(inc, 63, 64);
   }
+  total = uniform(total);
+  const int64_t W = gridDim.x < total ? gridDim.x : total, w = blockIdx.x;
+  if (w >= W) return;
+  const int64_t first = uniform(w * total / W), last = uniform((w + 1) * total / W);
+  // the row that holds place `first`: the last one that does not begin after it
+  int i = 0;
+  int64_t row_at = 0;
+  for (int base = 0;; base += 64) {
+    if (A.batch > 64) inc = scan(base, &mine, false);  // else it is at hand
+    const int64_t chunk = __shfl(inc, 63, 64);
+    if (row_at + chunk > first) {
+      const int at = 63 - __builtin_clzll(__ballot(base + lane < A.batch && row_at + inc - mine <= first));
+      i = base + at;
+      row_at += __shfl(inc - mine, at, 64);
+      break;
+    }
+    row_at += chunk;
+  }
+  i = uniform(i);
+  row_at = uniform(row_at);
+  for (int64_t at = first; at < last;) {
+    Share s;
+    s.i = i;
+    s.row = weight_row(A, i, false);
+    s.steps = steps_of(s.row);
+    if (at >= row_at + static_cast<int64_t>(s.steps) * A.Hk) {
+      row_at += static_cast<int64_t>(s.steps) * A.Hk;
+      ++i;
+      continue;
+    }
+    s.h = static_cast<int>((at - row_at) / s.steps);
+    s.place = row_at + static_cast<int64_t>(s.h) * s.steps;
+    s.lo = static_cast<int32_t>(at - s.place);
+    s.hi = static_cast<int32_t>(last - s.place < s.steps ? last - s.place : s.steps);
+    f(s, w, W, total);
+    at = s.place + s.hi;
+  }
+}
+
+// 16 bytes of Q of KV head h of row i, number e of row tiles [t0, ..) in the order of the operands: [tile][step][lane].
+// Rows past the last are zeros.
+template <int D, bool BF16>
+__device__ __forceinline__ uint4 q_piece(const WeightArgs& A, int i, int h, int32_t rows, int t0, int e) {
+  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32;
+  const int lane = e % 64, s = e / 64 % STEPS, r = (t0 + e / 64 / STEPS) * 32 + lane % 32;
+  if (r >= rows) return make_uint4(0, 0, 0, 0);
+  const int t = r / A.G;
+  const char* q = static_cast<const char*>(A.q) +
+                  ((static_cast<int64_t>(i) * A.n + t) * A.q_stride + static_cast<int64_t>(h * A.G + r - t * A.G) * D) * ES;
+  return *reinterpret_cast<const uint4*>(q + (2 * s + lane / 32) * 16);
 }
 
 // This lane's 16-byte pieces of the K rows of 32 keys from key0 on, one key per pair of
@@ -140,6 +237,7 @@ __device__ __forceinline__ void load_k(const WeightArgs& A, int i, int h, int32_
                   ((static_cast<size_t>(page) * A.Hk + h) * A.page + off) * (static_cast<size_t>(D) * ES) + lane / 32 * 16;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) k[s] = *reinterpret_cast<const uint4*>(p + s * 32);
+  __builtin_amdgcn_sched_barrier(0);  // all of them under way before the first is used
 }
 
 // Element e of a 32 x 32 result is row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32.
@@ -147,233 +245,263 @@ __device__ __forceinline__ int result_row(int e) { return 8 * (e / 4) + 4 * ((th
 
 }  // namespace
 
-// Few rows: logits of a wave's keys (stored), maximum and sum of each row over them.
+// Few rows: logits of a tile of keys per wave (stored), maximum and sum of each row over the workgroup's.
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * kStoredWaves) void weights_stored_kernel(WeightArgs A, WeightPlan P) {
   constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32;
   __shared__ uint4 qs[STEPS * 64];
-  const int h = blockIdx.y, i = blockIdx.z, lane = threadIdx.x & 63;
-  const WeightRow w = weight_row(A, i, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-  if (w.n == 0 || static_cast<int64_t>(blockIdx.x) * kStoredWaves * kStoredKeys >= w.kv) return;
-  load_q<D, BF16, 64 * kStoredWaves>(A, i, h, w.n * A.G, 0, 1, qs);
-  __syncthreads();
-  const int part = blockIdx.x * kStoredWaves + uniform(static_cast<int32_t>(threadIdx.x / 64));
-  const int32_t lo = part * kStoredKeys, hi = min(lo + kStoredKeys, w.kv);
-  if (lo >= hi) return;
-  const int row = lane % 32;
-  const int32_t last = w.kv - w.n + row / A.G;  // this row's last key
-  const size_t unit = static_cast<size_t>(i) * A.Hk + h;
-  float* z = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.keys) + (unit * P.R + row) * P.W;
-  float m = -INFINITY, l = 0.f;
-  for (int32_t key0 = lo; key0 < hi; key0 += kTileKeys) {
-    uint4 k[STEPS];
-    load_k<D, BF16>(A, i, h, key0, w.kv, k);
-    f32x16_t S;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) S[e] = 0.f;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) S = mfma_step<BF16>(k[s], qs[s * 64 + lane], S);
-    float mx = m;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      S[e] = key0 + result_row(e) <= last ? S[e] * A.scale_log2 : -INFINITY;
-      mx = fmaxf(mx, S[e]);
-    }
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    l *= __builtin_amdgcn_exp2f(m - ref);
-    m = mx;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(S[e] - ref);
-    if (row < P.R) {
-#pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<f32x4_t*>(z + key0 + result_row(e)) = f32x4_t{S[e], S[e + 1], S[e + 2], S[e + 3]};
-    }
-  }
-  // the halves' maxima differ
-  const float both = half_max(m), ref = both == -INFINITY ? 0.f : both;
-  l = half_sum(l * __builtin_amdgcn_exp2f(m - ref));
-  if (lane < 32) static_cast<float2*>(A.workspace)[(unit * P.parts + part) * P.Rp + row] = make_float2(both, l);
-}
-
-// Many rows: maximum and sum of every row over each of a wave's tiles of keys.
-template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kManyWaves, 2) void weights_stats_kernel(WeightArgs A, WeightPlan P) {
-  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, KB = many_blocks(D, BF16), RT = many_row_tiles(D, BF16);
-  extern __shared__ __align__(16) uint4 q_lds[];
+  __shared__ float2 ml[kStoredWaves][32];
   const int h = blockIdx.y, i = blockIdx.z, lane = threadIdx.x & 63;
   const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
   const WeightRow w = weight_row(A, i, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-  if (w.n == 0 || static_cast<int64_t>(blockIdx.x) * kManyWaves * kManyTiles * KB * kTileKeys >= w.kv) return;
-  const int32_t rows = w.n * A.G, tiles = (rows + 31) / 32;
+  const int64_t from = static_cast<int64_t>(blockIdx.x) * kStoredKeys;
+  if (w.n == 0 || from >= w.kv) return;
+  const int32_t key0 = static_cast<int32_t>(from) + wave * kTileKeys;
+  // Q is asked for before K, and used first
+  constexpr int PIECES = STEPS * 64 / (64 * kStoredWaves);
+  uint4 q[PIECES], k[STEPS];
+#pragma unroll
+  for (int e = 0; e < PIECES; ++e) q[e] = q_piece<D, BF16>(A, i, h, w.n * A.G, 0, e * 64 * kStoredWaves + threadIdx.x);
+  load_k<D, BF16>(A, i, h, key0, w.kv, k);
+#pragma unroll
+  for (int e = 0; e < PIECES; ++e) qs[e * 64 * kStoredWaves + threadIdx.x] = q[e];
+  lds_barrier();
+  const int row = lane % 32;
+  const int32_t last = w.kv - w.n + row / A.G;  // this row's last key
   const size_t unit = static_cast<size_t>(i) * A.Hk + h;
-  for (int t0 = 0; t0 < tiles; t0 += RT) {
-    const int nt = min(RT, tiles - t0);
-    if (t0 > 0) __syncthreads();
-    load_q<D, BF16, 64 * kManyWaves>(A, i, h, rows, t0, nt, q_lds);
-    __syncthreads();
-    for (int c = 0; c < kManyTiles; ++c) {
-      const int part = (blockIdx.x * kManyTiles + c) * kManyWaves + wave;
-      const int32_t key0 = part * (KB * kTileKeys);
-      if (key0 >= w.kv) break;
-      uint4 k[KB][STEPS];
+  f32x16_t S;
 #pragma unroll
-      for (int b = 0; b < KB; ++b) load_k<D, BF16>(A, i, h, key0 + b * kTileKeys, w.kv, k[b]);
-      const bool masked = key0 + KB * kTileKeys > w.kv - w.n + 1;
-      for (int t = 0; t < nt; ++t) {
-        f32x16_t S[KB];
+  for (int e = 0; e < 16; ++e) S[e] = 0.f;
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+  for (int s = 0; s < STEPS; ++s) S = mfma_step<BF16>(k[s], qs[s * 64 + lane], S);
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) S[b][e] = 0.f;
+  for (int e = 0; e < 16; ++e) {
+    S[e] = key0 + result_row(e) <= last ? S[e] * A.scale_log2 : -INFINITY;
+    m = fmaxf(m, S[e]);
+  }
+  m = half_max(m);
+  const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const uint4 q = q_lds[(t * STEPS + s) * 64 + lane];
+  for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(S[e] - ref);
+  l = half_sum(l);
+  if (row < P.R && key0 < w.kv) {
+    float* z = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.keys) + (unit * P.R + row) * P.W + key0;
 #pragma unroll
-          for (int b = 0; b < KB; ++b) S[b] = mfma_step<BF16>(k[b][s], q, S[b]);
-        }
-        const int row = (t0 + t) * 32 + lane % 32;
-        if (masked) {
-          const int32_t last = w.kv - w.n + row / A.G;
+    for (int e = 0; e < 16; e += 4) *reinterpret_cast<f32x4_t*>(z + result_row(e)) = f32x4_t{S[e], S[e + 1], S[e + 2], S[e + 3]};
+  }
+  if (lane < 32) ml[wave][row] = make_float2(m, l);
+  lds_barrier();
+  if (threadIdx.x < 32) {
+    float both = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int b = 0; b < KB; ++b)
+    for (int o = 0; o < kStoredWaves; ++o) both = fmaxf(both, ml[o][row].x);
+    const float to = both == -INFINITY ? 0.f : both;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) S[b][e] = key0 + b * kTileKeys + result_row(e) <= last ? S[b][e] : -INFINITY;
-        }
-        float m = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) m = fmaxf(m, S[b][e]);
-        m = half_max(m) * A.scale_log2;
-        const float off = m == -INFINITY ? 0.f : -m;
-        float l = 0.f;
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(fmaf(S[b][e], A.scale_log2, off));
-        l = half_sum(l);
-        if (lane < 32) static_cast<float2*>(A.workspace)[(unit * P.parts + part) * P.Rp + row] = make_float2(m, l);
-      }
-    }
+    for (int o = 0; o < kStoredWaves; ++o) sum += ml[o][row].y * __builtin_amdgcn_exp2f(ml[o][row].x - to);
+    static_cast<float2*>(A.workspace)[(unit * P.parts + blockIdx.x) * P.Rp + row] = make_float2(both, sum);
   }
 }
 
-// Joins the parts of 32 rows of a KV head, in a fixed order: log2 of the sum of 2^z.
-// Rows past the last get +inf, which takes every weight to 0.
+// Many rows: maximum and sum of every row over a workgroup's share of the keys.
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * many_waves(D, BF16), many_waves(D, BF16) / 4) void weights_stats_kernel(WeightArgs A, WeightPlan P) {
+  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, RT = many_row_tiles(D, BF16), NW = many_waves(D, BF16), THREADS = 64 * NW;
+  extern __shared__ __align__(16) uint4 q_lds[];
+  const int held = min(RT, P.row_tiles) * 32;  // rows of a round
+  float2* ml = reinterpret_cast<float2*>(q_lds + static_cast<size_t>(held) * STEPS * 2);  // [wave][row of the round]
+  const int lane = threadIdx.x & 63;
+  const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
+  each_share<many_keys(D, BF16)>(A, blockIdx.x == 0 && threadIdx.x < 64, [&](const Share& s, int64_t w, int64_t W, int64_t total) {
+    const int32_t rows = s.row.n * A.G, tiles = (rows + 31) / 32, kv = s.row.kv;
+    const int64_t unit = static_cast<int64_t>(s.i) * A.Hk + s.h;
+    if (s.lo == 0 && threadIdx.x == 0) {
+      // its last workgroup: the largest w' with w' total / W <= its last place
+      const int64_t count = ((s.place + s.steps) * W - 1) / total - w + 1;
+      reinterpret_cast<int2*>(static_cast<char*>(A.workspace) + P.meta)[unit] = make_int2(static_cast<int>(w), static_cast<int>(count));
+    }
+    uint4 k[STEPS];
+    auto key_of = [&](int32_t step) { return (step * NW + wave) * kTileKeys; };
+    for (int t0 = 0; t0 < tiles; t0 += RT) {
+      const int nt = min(RT, tiles - t0);
+      lds_barrier();  // Q and the sums of what came before are read
+      for (int e = threadIdx.x; e < nt * STEPS * 64; e += THREADS) q_lds[e] = q_piece<D, BF16>(A, s.i, s.h, rows, t0, e);
+      for (int r = lane; r < nt * 32; r += 64) ml[wave * held + r] = make_float2(-INFINITY, 0.f);
+      lds_barrier();
+#pragma unroll 1
+      for (int32_t step = s.lo; step < s.hi; ++step) {
+        const int32_t key0 = key_of(step);
+        if (key0 >= kv) break;
+        load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
+        const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          f32x16_t S;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[e] = 0.f;
+#pragma unroll
+          for (int o = 0; o < STEPS; ++o) S = mfma_step<BF16>(k[o], q_lds[(t * STEPS + o) * 64 + lane], S);
+          const int row = t * 32 + lane % 32;
+          if (masked) {
+            const int32_t last = kv - s.row.n + (t0 * 32 + row) / A.G;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[e] = key0 + result_row(e) <= last ? S[e] : -INFINITY;
+          }
+          const float2 was = ml[wave * held + row];
+          float m = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) m = fmaxf(m, S[e]);
+          m = fmaxf(half_max(m) * A.scale_log2, was.x);
+          const float ref = m == -INFINITY ? 0.f : m;
+          float l = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, -ref));
+          l = fmaf(was.y, __builtin_amdgcn_exp2f(was.x - ref), half_sum(l));
+          if (lane < 32) ml[wave * held + row] = make_float2(m, l);
+        }
+      }
+      __syncthreads();
+      for (int r = threadIdx.x; r < nt * 32; r += THREADS) {
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int o = 0; o < NW; ++o) m = fmaxf(m, ml[o * held + r].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int o = 0; o < NW; ++o) l += ml[o * held + r].y * __builtin_amdgcn_exp2f(ml[o * held + r].x - ref);
+        static_cast<float2*>(A.workspace)[(unit + w) * P.Rp + t0 * 32 + r] = make_float2(m, l);
+      }
+    }
+  });
+}
+
+// (maximum, sum) of the keys of two parts.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * __builtin_amdgcn_exp2f(a.x - ref) + b.y * __builtin_amdgcn_exp2f(b.x - ref));
+}
+
+// Few rows: joins the parts of a KV head's rows, in a fixed order: log2 of the sum of 2^z.
 __global__ __launch_bounds__(256) void weights_join_kernel(WeightArgs A, WeightPlan P) {
   __shared__ float2 parts[8][32];
-  const int i = blockIdx.z, h = blockIdx.y, lr = threadIdx.x % 32, g = threadIdx.x / 32, row = blockIdx.x * 32 + lr;
+  const int i = blockIdx.y, h = blockIdx.x, row = threadIdx.x % 32, g = threadIdx.x / 32;
   const WeightRow w = weight_row(A, i, false);
   if (w.n == 0) return;
   const size_t unit = static_cast<size_t>(i) * A.Hk + h;
   const float2* ml = static_cast<const float2*>(A.workspace) + unit * P.parts * P.Rp + row;
-  const bool live = row < w.n * A.G;
-  const int count = live ? (w.kv + P.part_keys - 1) / P.part_keys : 0;
-  float m = -INFINITY, l = 0.f;
-  auto add = [&](float2 x) {
-    const float mx = fmaxf(m, x.x), ref = mx == -INFINITY ? 0.f : mx;
-    l = l * __builtin_amdgcn_exp2f(m - ref) + x.y * __builtin_amdgcn_exp2f(x.x - ref);
-    m = mx;
-  };
-#pragma unroll 4
-  for (int p = g; p < count; p += 8) add(ml[static_cast<size_t>(p) * P.Rp]);
-  parts[g][lr] = make_float2(m, l);
+  const int count = (w.kv + kStoredKeys - 1) / kStoredKeys;
+  float2 sum = make_float2(-INFINITY, 0.f);
+#pragma unroll 8
+  for (int p = g; p < count; p += 8) sum = join(sum, ml[static_cast<size_t>(p) * P.Rp]);
+  parts[g][row] = sum;
   __syncthreads();
   if (g != 0) return;
-  for (int o = 1; o < 8; ++o) add(parts[o][lr]);
-  float* lse = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.lse);
-  lse[unit * P.Rp + row] = live ? m + __builtin_amdgcn_logf(l) : INFINITY;
+#pragma unroll
+  for (int o = 1; o < 8; ++o) sum = join(sum, parts[o][row]);
+  reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.lse)[unit * P.Rp + row] = sum.x + __builtin_amdgcn_logf(sum.y);
 }
 
-// Few rows: the weights of one key from the stored logits, all heads.
+// Few rows: the weights of 64 keys from the stored logits; wave w takes heads w, w + 4, ..  JOIN: it joins the
+// parts of its rows itself, which saves a launch where they are few (kFewParts).
+template <bool JOIN>
 __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPlan P) {
-  const int i = blockIdx.y;
-  const WeightRow w = weight_row(A, i, false);
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (w.n == 0 || j >= w.kv) return;
-  const char* ws = static_cast<const char*>(A.workspace);
-  const float* lse = reinterpret_cast<const float*>(ws + P.lse) + static_cast<size_t>(i) * A.Hk * P.Rp;
-  const float* z = reinterpret_cast<const float*>(ws + P.keys) + static_cast<size_t>(i) * A.Hk * P.R * P.W + j;
-  float sum = 0.f;
-  for (int h = 0; h < A.Hk; ++h)
-    for (int t = 0; t < w.n; ++t) {
-      const bool seen = j <= w.kv - w.n + t;
-#pragma unroll 4
-      for (int g = 0; g < A.G; ++g) {
-        const int r = t * A.G + g;
-        const float p = __builtin_amdgcn_exp2f(z[(static_cast<size_t>(h) * P.R + r) * P.W] - lse[h * P.Rp + r]);
-        sum += seen ? p : 0.f;
-      }
-    }
-  const size_t at = static_cast<size_t>(i) * A.width + j;
-  const bool old = A.score_in && (!A.have_len || j < A.have_len[i]);
-  A.score_out[at] = (old ? A.score_in[at] : 0.f) + sum;
-}
-
-// Many rows: each head's weights of a wave's keys, the logits computed again with the
-// operands the other way round, so that a lane holds one key's logits.
-template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kManyWaves, 2) void weights_keys_kernel(WeightArgs A, WeightPlan P) {
-  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, KB = many_blocks(D, BF16), RT = many_row_tiles(D, BF16);
-  extern __shared__ __align__(16) uint4 q_lds[];
-  __shared__ __align__(16) float lse[RT * 32];
-  const int h = blockIdx.y, i = blockIdx.z, lane = threadIdx.x & 63;
+  __shared__ float sums[4][64], joined[4][32];
+  const int i = blockIdx.y, lane = threadIdx.x & 63;
   const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
   const WeightRow w = weight_row(A, i, false);
-  if (w.n == 0 || static_cast<int64_t>(blockIdx.x) * kManyWaves * kManyTiles * KB * kTileKeys >= w.kv) return;
-  const int32_t rows = w.n * A.G, tiles = (rows + 31) / 32;
-  const size_t unit = static_cast<size_t>(i) * A.Hk + h;
-  float* out = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.keys) + unit * P.W;
-  const float* all = reinterpret_cast<const float*>(static_cast<const char*>(A.workspace) + P.lse) + unit * P.Rp;
-  for (int t0 = 0; t0 < tiles; t0 += RT) {
-    const int nt = min(RT, tiles - t0);
-    if (t0 > 0) __syncthreads();
-    load_q<D, BF16, 64 * kManyWaves>(A, i, h, rows, t0, nt, q_lds);
-    for (int r = threadIdx.x; r < nt * 32; r += 64 * kManyWaves) lse[r] = all[t0 * 32 + r];
-    __syncthreads();
-    for (int c = 0; c < kManyTiles; ++c) {
-      const int32_t key0 = ((blockIdx.x * kManyTiles + c) * kManyWaves + wave) * (KB * kTileKeys);
-      if (key0 >= w.kv) break;
-      uint4 k[KB][STEPS];
-#pragma unroll
-      for (int b = 0; b < KB; ++b) load_k<D, BF16>(A, i, h, key0 + b * kTileKeys, w.kv, k[b]);
-      const bool masked = key0 + KB * kTileKeys > w.kv - w.n + 1;
-      float sum[KB];
-#pragma unroll
-      for (int b = 0; b < KB; ++b) sum[b] = 0.f;
-      for (int t = 0; t < nt; ++t) {
-        f32x16_t S[KB];
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) S[b][e] = 0.f;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          const uint4 q = q_lds[(t * STEPS + s) * 64 + lane];
-#pragma unroll
-          for (int b = 0; b < KB; ++b) S[b] = mfma_step<BF16>(q, k[b][s], S[b]);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int row = t * 32 + result_row(e);
-          const float off = -lse[row];
-          const int32_t last = masked ? w.kv - w.n + (t0 * 32 + row) / A.G : 0;
-#pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(S[b][e], A.scale_log2, off));
-            sum[b] += !masked || key0 + b * kTileKeys + lane % 32 <= last ? p : 0.f;
-          }
-        }
+  const int64_t from = static_cast<int64_t>(blockIdx.x) * 64, j = from + lane;
+  if (w.n == 0 || from >= w.kv) return;
+  const char* ws = static_cast<const char*>(A.workspace);
+  const float* z = reinterpret_cast<const float*>(ws + P.keys) + static_cast<size_t>(i) * A.Hk * P.R * P.W + j;
+  const int32_t rows = w.n * A.G, span = static_cast<int32_t>(j - (w.kv - w.n));  // tokens before `span` do not attend j
+  float sum = 0.f;
+  for (int h = wave; h < A.Hk; h += 4) {
+    const size_t unit = static_cast<size_t>(i) * A.Hk + h;
+    const float* lse = reinterpret_cast<const float*>(ws + P.lse) + unit * P.Rp;
+    if constexpr (JOIN) {
+      // a lane per row and every 64 / 2^bits-th part, 2^bits >= rows
+      const int bits = rows <= 8 ? 3 : (rows <= 16 ? 4 : 5), row = lane & ((1 << bits) - 1);
+      const float2* ml = reinterpret_cast<const float2*>(ws) + unit * P.parts * P.Rp + row;
+      const int count = (w.kv + kStoredKeys - 1) / kStoredKeys;
+      float2 s = make_float2(-INFINITY, 0.f);
+#pragma unroll 8
+      for (int p = lane >> bits; p < count; p += 64 >> bits) s = join(s, ml[static_cast<size_t>(p) * P.Rp]);
+      for (int d = 1 << bits; d < 64; d <<= 1) s = join(s, make_float2(__shfl_xor(s.x, d, 64), __shfl_xor(s.y, d, 64)));
+      if (lane >> bits == 0) joined[wave][row] = s.x + __builtin_amdgcn_logf(s.y);
+    }
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) {
+      const float p = __builtin_amdgcn_exp2f(z[(static_cast<size_t>(h) * P.R + r) * P.W] - (JOIN ? joined[wave][r] : lse[r]));
+      sum += r >= span * A.G ? p : 0.f;
+    }
+  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave != 0 || j >= w.kv) return;
+  const size_t at = static_cast<size_t>(i) * A.width + j;
+  const bool old = A.score_in && (!A.have_len || j < A.have_len[i]);
+  A.score_out[at] = (old ? A.score_in[at] : 0.f) + ((sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]));
+}
+
+// Many rows: each head's weights of the keys, the logits computed again with the
+// operands the other way round, so that a lane holds one key's logits.
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * many_waves(D, BF16), many_waves(D, BF16) / 4) void weights_keys_kernel(WeightArgs A, WeightPlan P) {
+  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, RT = many_row_tiles(D, BF16), NW = many_waves(D, BF16), THREADS = 64 * NW;
+  extern __shared__ __align__(16) uint4 q_lds[];
+  __shared__ __align__(16) float lse[RT * 32];
+  const int lane = threadIdx.x & 63;
+  const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
+  each_share<many_keys(D, BF16)>(A, false, [&](const Share& s, int64_t, int64_t, int64_t) {
+    const int32_t rows = s.row.n * A.G, tiles = (rows + 31) / 32, kv = s.row.kv;
+    const size_t unit = static_cast<size_t>(s.i) * A.Hk + s.h;
+    float* out = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.keys) + unit * P.W;
+    const int2 meta = reinterpret_cast<const int2*>(static_cast<const char*>(A.workspace) + P.meta)[unit];
+    uint4 k[STEPS];
+    auto key_of = [&](int32_t step) { return (step * NW + wave) * kTileKeys; };
+    for (int t0 = 0; t0 < tiles; t0 += RT) {
+      const int nt = min(RT, tiles - t0);
+      lds_barrier();  // what came before is read
+      for (int e = threadIdx.x; e < nt * STEPS * 64; e += THREADS) q_lds[e] = q_piece<D, BF16>(A, s.i, s.h, rows, t0, e);
+      // the parts of each row, joined in a fixed order: log2 of the sum of 2^z; past the last row
+      // +inf, which takes every weight to 0
+      for (int r = threadIdx.x; r < nt * 32; r += THREADS) {
+        const float2* ml = static_cast<const float2*>(A.workspace) + (static_cast<int64_t>(unit) + meta.x) * P.Rp + t0 * 32 + r;
+        float2 sum = make_float2(-INFINITY, 0.f);
+#pragma unroll 8
+        for (int p = 0; p < meta.y; ++p) sum = join(sum, ml[static_cast<size_t>(p) * P.Rp]);
+        lse[r] = t0 * 32 + r < rows ? sum.x + __builtin_amdgcn_logf(sum.y) : INFINITY;
       }
+      lds_barrier();
+#pragma unroll 1
+      for (int32_t step = s.hi - 1; step >= s.lo; --step) {  // the last keys first: they may still be in the last-level cache
+        const int32_t key0 = key_of(step);
+        load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
+        if (key0 >= kv) continue;
+        const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
+        float sum = 0.f;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          f32x16_t S;
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const float total = half_sum(sum[b]);
-        float* at = out + key0 + b * kTileKeys + lane;  // within W, whole pairs of tiles
+          for (int e = 0; e < 16; ++e) S[e] = 0.f;
+#pragma unroll
+          for (int o = 0; o < STEPS; ++o) S = mfma_step<BF16>(q_lds[(t * STEPS + o) * 64 + lane], k[o], S);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[e] = __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, -lse[t * 32 + result_row(e)]));
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              S[e] = key0 + lane % 32 <= kv - s.row.n + (t0 * 32 + t * 32 + result_row(e)) / A.G ? S[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum += S[e];
+        }
+        const float total = half_sum(sum);
+        float* at = out + key0 + lane;  // within W
         if (lane < 32) *at = t0 > 0 ? *at + total : total;
       }
     }
-  }
+  });
 }
 
 // Many rows: the heads' sums of one key.
@@ -403,25 +531,26 @@ size_t weights_workspace_bytes(int32_t batch, int32_t n, int32_t width, int Hk, 
 template <int D, bool BF16>
 static int launch_weights_t(const WeightArgs& a, hipStream_t s) {
   const WeightPlan p = weight_plan(a.batch, a.n, a.width, a.Hk, a.G, a.D, BF16);
-  const int64_t tiles = (static_cast<int64_t>(a.width) + 255) / 256;
   if (p.stored) {
-    const int64_t wgs = (static_cast<int64_t>(p.parts) + kStoredWaves - 1) / kStoredWaves;
-    if (!grid_fits(wgs, 64 * kStoredWaves)) return static_cast<int>(hipErrorInvalidValue);
-    hipLaunchKernelGGL((weights_stored_kernel<D, BF16>), dim3(static_cast<unsigned>(wgs), a.Hk, a.batch),
-                       dim3(64 * kStoredWaves), 0, s, a, p);
-    hipLaunchKernelGGL(weights_join_kernel, dim3(1, a.Hk, a.batch), dim3(256), 0, s, a, p);
-    hipLaunchKernelGGL(weights_sum_kernel, dim3(static_cast<unsigned>(tiles), a.batch), dim3(256), 0, s, a, p);
+    if (!grid_fits(p.parts, 64 * kStoredWaves)) return static_cast<int>(hipErrorInvalidValue);
+    const int64_t blocks = (static_cast<int64_t>(a.width) + 63) / 64;
+    if (!grid_fits(blocks, 256)) return static_cast<int>(hipErrorInvalidValue);
+    hipLaunchKernelGGL((weights_stored_kernel<D, BF16>), dim3(p.parts, a.Hk, a.batch), dim3(64 * kStoredWaves), 0, s, a, p);
+    const dim3 grid(static_cast<unsigned>(blocks), a.batch);
+    const int64_t parts = static_cast<int64_t>(p.parts) * a.Hk;
+    if (parts <= kFewParts && parts * a.batch <= kFewPartsAll) {
+      hipLaunchKernelGGL(weights_sum_kernel<true>, grid, dim3(256), 0, s, a, p);
+    } else {
+      hipLaunchKernelGGL(weights_join_kernel, dim3(a.Hk, a.batch), dim3(256), 0, s, a, p);
+      hipLaunchKernelGGL(weights_sum_kernel<false>, grid, dim3(256), 0, s, a, p);
+    }
   } else {
-    constexpr int per = kManyWaves * kManyTiles;
-    const int64_t wgs = (static_cast<int64_t>(p.parts) + per - 1) / per;
-    if (!grid_fits(wgs, 64 * kManyWaves)) return static_cast<int>(hipErrorInvalidValue);
-    const int rt = p.row_tiles < many_row_tiles(D, BF16) ? p.row_tiles : many_row_tiles(D, BF16);
-    const size_t lds = static_cast<size_t>(rt) * 32 * D * (BF16 ? 2 : 4);
-    const dim3 grid(static_cast<unsigned>(wgs), a.Hk, a.batch);
-    hipLaunchKernelGGL((weights_stats_kernel<D, BF16>), grid, dim3(64 * kManyWaves), lds, s, a, p);
-    hipLaunchKernelGGL(weights_join_kernel, dim3(p.row_tiles, a.Hk, a.batch), dim3(256), 0, s, a, p);
-    hipLaunchKernelGGL((weights_keys_kernel<D, BF16>), grid, dim3(64 * kManyWaves), lds, s, a, p);
-    hipLaunchKernelGGL(weights_heads_kernel, dim3(static_cast<unsigned>(tiles), a.batch), dim3(256), 0, s, a, p);
+    constexpr int threads = 64 * many_waves(D, BF16);
+    const size_t lds = many_lds(p.row_tiles, D, BF16);
+    const int64_t blocks = (static_cast<int64_t>(a.width) + 255) / 256;
+    hipLaunchKernelGGL((weights_stats_kernel<D, BF16>), dim3(p.workgroups), dim3(threads), lds, s, a, p);
+    hipLaunchKernelGGL((weights_keys_kernel<D, BF16>), dim3(p.workgroups), dim3(threads), lds, s, a, p);
+    hipLaunchKernelGGL(weights_heads_kernel, dim3(static_cast<unsigned>(blocks), a.batch), dim3(256), 0, s, a, p);
   }
   return static_cast<int>(hipGetLastError());
 }
