@@ -621,8 +621,12 @@ class KVCache:
 def _need_rows(t: Optional[torch.Tensor], name: str, shape, dtype, device: Optional[int] = None) -> int:
     """Rows of heads, any row stride, contiguous within a row; returns the row stride in elements."""
     if (t is not None and (t.is_cuda if device is None else t.get_device() == device) and t.dtype == dtype
-            and t.shape == shape and t.is_contiguous()):
-        return shape[-2] * shape[-1]
+            and t.shape == shape):
+        if t.is_contiguous():
+            return shape[-2] * shape[-1]
+        st = t.stride()
+        if len(st) == 3 and st[2] == 1 and st[1] == shape[2] and st[0] >= 0 and shape[0] > 1:
+            return st[0]
     if t is None:
         raise ValueError(f"{name}: missing")
     if not t.is_cuda:

@@ -59,13 +59,14 @@ __device__ __forceinline__ float half_sum(float x) {
 struct WeightPlan {
   int32_t R, row_tiles, Rp;  // rows of a KV head (n G), tiles of 32 of them, rows in whole tiles
   int32_t W;                 // row length of the logits or sums: width in whole tiles of keys
-  int32_t parts;             // few rows: parts (of kStoredKeys keys) of a row of `width` tokens
-  int32_t workgroups;        // many rows: those that share the keys
   bool stored;               // few rows: logits are stored
-  // byte offsets; (maximum, sum) of a row over a part at 0, [unit][parts][Rp] or [unit + workgroup][Rp], a unit being a
-  // KV head of a batch row; many rows: (first workgroup, number of them) of each unit; few rows: lse
-  // [unit][Rp]; the logits [unit][R][W] or the heads' sums [unit][W]
-  size_t meta, lse, keys, total;
+  int32_t parts;             // few rows: parts (of kStoredKeys keys) of a row of `width` tokens
+  // many rows: row tiles whose Q is in LDS together, and rounds of so many; a unit is a round of a KV head of a batch row
+  int32_t round_tiles, rounds;
+  // byte offsets; (maximum, sum) of a row over a part at 0, [batch Hk][parts][Rp] or [unit + workgroup][32
+  // round_tiles]; (first workgroup, number of them) [unit] or lse [batch Hk][Rp]; the logits
+  // [batch Hk][R][W] or a unit's sums [unit][W]
+  size_t lse, keys, total;
 };
 
 constexpr int kTileKeys = 32;
@@ -88,11 +89,7 @@ constexpr int many_row_tiles(int D, bool bf16) {
 
 __host__ __device__ inline size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-// LDS of the many-row kernels: Q, and (maximum, sum) of each row and wave.
-size_t many_lds(int row_tiles, int D, bool bf16) {
-  const int rt = row_tiles < many_row_tiles(D, bf16) ? row_tiles : many_row_tiles(D, bf16);
-  return static_cast<size_t>(rt) * 32 * (D * (bf16 ? 2 : 4) + many_waves(D, bf16) * sizeof(float2));
-}
+constexpr int kManyWorkgroups = 256;  // one per CU: 16 waves of 128 registers
 
 WeightPlan weight_plan(int32_t batch, int32_t n, int32_t width, int Hk, int G, int D, bool bf16) {
   WeightPlan p{};
@@ -101,14 +98,24 @@ WeightPlan weight_plan(int32_t batch, int32_t n, int32_t width, int Hk, int G, i
   p.Rp = p.row_tiles * 32;
   p.stored = p.row_tiles == 1;
   p.parts = static_cast<int32_t>((static_cast<int64_t>(width) + kStoredKeys - 1) / kStoredKeys);
-  // one or two workgroups per CU, as LDS and 32 waves allow
-  p.workgroups = many_lds(p.row_tiles, D, bf16) <= (78 << 10) ? 512 : 256;
   p.W = static_cast<int32_t>(round_up(width, 64));
-  const size_t units = static_cast<size_t>(batch) * Hk;
-  p.meta = round_up((p.stored ? units * p.parts : units + p.workgroups) * p.Rp * sizeof(float2), 256);
-  p.lse = p.meta + round_up(p.stored ? 0 : units * sizeof(int2), 256);
-  p.keys = p.lse + round_up(p.stored ? units * p.Rp * sizeof(float) : 0, 256);
-  p.total = p.keys + units * (p.stored ? p.R : 1) * p.W * sizeof(float);
+  const int64_t heads = static_cast<int64_t>(batch) * Hk;
+  // as many row tiles to a round as fit, or fewer where that leaves workgroups without work (64 queries of 8 heads over 100
+  // tokens, d 256: 20 us, with the most that fit 71; 8 KV heads of 20000 tokens, d 128, 512 rows each: 233, 247)
+  const int64_t steps = (static_cast<int64_t>(width) + many_keys(D, bf16) - 1) / many_keys(D, bf16);
+  const int64_t most = many_row_tiles(D, bf16), even = steps * heads >= kManyWorkgroups ? most : p.row_tiles * heads * steps / kManyWorkgroups;
+  p.round_tiles = static_cast<int32_t>(even < 1 ? 1 : (even < most ? even : most));
+  p.rounds = (p.row_tiles + p.round_tiles - 1) / p.round_tiles;
+  p.round_tiles = (p.row_tiles + p.rounds - 1) / p.rounds;  // as many rounds, of like size
+  p.rounds = (p.row_tiles + p.round_tiles - 1) / p.round_tiles;
+  // A size that grows with each argument.  Units are heads x the rounds of `most`; or, where there are more
+  // rounds than that, steps x heads < kManyWorkgroups, and they are at most 2 kManyWorkgroups / steps + heads,
+  // so their sums at most 2 kManyWorkgroups many_keys() + heads W.
+  const size_t base = heads * ((p.row_tiles + most - 1) / most), units = base + 2 * kManyWorkgroups + heads;
+  p.lse = round_up(p.stored ? heads * p.parts * p.Rp * sizeof(float2) : (units + kManyWorkgroups) * most * 32 * sizeof(float2), 256);
+  p.keys = p.lse + round_up(p.stored ? heads * p.Rp * sizeof(float) : units * sizeof(int2), 256);
+  const size_t sums = (base + heads) * p.W + static_cast<size_t>(2 * kManyWorkgroups) * many_keys(D, bf16);
+  p.total = p.keys + (p.stored ? heads * p.R * static_cast<size_t>(p.W) : sums) * sizeof(float);
   return p;
 }
 
@@ -135,26 +142,29 @@ __device__ __forceinline__ WeightRow weight_row(const WeightArgs& A, int i, bool
   return WeightRow{uniform(r.n), uniform(r.kv)};
 }
 
-// A workgroup's share of the keys of a unit: steps [lo, hi) of its `steps`; `place` + lo is where it begins on the
-// line of all units' steps.
+// A workgroup's share of the keys of a unit (head h of row i, `tiles` row tiles from t0 on): steps [lo, hi) of
+// its `steps`; `place` + lo is where it begins on the line of all units' steps.
 struct Share {
-  int i, h;
+  int i, h, t0, tiles;
+  int64_t unit;
   WeightRow row;
   int32_t lo, hi, steps;
   int64_t place;
 };
-// The steps of all units lie on one line, row by row and head by head, and workgroup w of W = min(grid, total)
+// The steps of all units lie on one line, row by row, head by head and round by round, and workgroup w of W = min(grid, total)
 // takes places [w total / W, (w + 1) total / W), whatever the rows' lengths: f(share, w, W, total) for
 // every unit that it has a part of, in order.  All waves together.
 template <int KEYS, class F>
-__device__ __forceinline__ void each_share(const WeightArgs& A, bool report, F f) {
+__device__ __forceinline__ void each_share(const WeightArgs& A, const WeightPlan& P, bool report, F f) {
   const int lane = threadIdx.x & 63;
   auto steps_of = [&](const WeightRow& r) { return r.n > 0 ? (r.kv + KEYS - 1) / KEYS : 0; };
+  auto tiles_of = [&](const WeightRow& r) { return (r.n * A.G + 31) / 32; };
+  auto units_of = [&](const WeightRow& r) { return (tiles_of(r) + P.round_tiles - 1) / P.round_tiles * A.Hk; };
   // inclusive sum over the lanes of the places of rows base + lane
   auto scan = [&](int base, int64_t* mine, bool tell) {
     const bool in = base + lane < A.batch;
     const WeightRow r = in ? any_row(A, base + lane, tell) : WeightRow{0, 0};
-    int64_t inc = *mine = static_cast<int64_t>(steps_of(r)) * A.Hk;
+    int64_t inc = *mine = static_cast<int64_t>(steps_of(r)) * units_of(r);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int64_t up = __shfl_up(inc, d, 64);
@@ -192,13 +202,19 @@ __device__ __forceinline__ void each_share(const WeightArgs& A, bool report, F f
     s.i = i;
     s.row = weight_row(A, i, false);
     s.steps = steps_of(s.row);
-    if (at >= row_at + static_cast<int64_t>(s.steps) * A.Hk) {
-      row_at += static_cast<int64_t>(s.steps) * A.Hk;
+    const int units = units_of(s.row);
+    if (at >= row_at + static_cast<int64_t>(s.steps) * units) {
+      row_at += static_cast<int64_t>(s.steps) * units;
       ++i;
       continue;
     }
-    s.h = static_cast<int>((at - row_at) / s.steps);
-    s.place = row_at + static_cast<int64_t>(s.h) * s.steps;
+    const int u = static_cast<int>((at - row_at) / s.steps), rounds = units / A.Hk;
+    s.h = u / rounds;
+    const int round = u - s.h * rounds;
+    s.t0 = round * P.round_tiles;
+    s.tiles = min(P.round_tiles, tiles_of(s.row) - s.t0);
+    s.unit = (static_cast<int64_t>(i) * A.Hk + s.h) * P.rounds + round;
+    s.place = row_at + static_cast<int64_t>(u) * s.steps;
     s.lo = static_cast<int32_t>(at - s.place);
     s.hi = static_cast<int32_t>(last - s.place < s.steps ? last - s.place : s.steps);
     f(s, w, W, total);
@@ -306,70 +322,65 @@ __global__ __launch_bounds__(64 * kStoredWaves) void weights_stored_kernel(Weigh
 // Many rows: maximum and sum of every row over a workgroup's share of the keys.
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * many_waves(D, BF16), many_waves(D, BF16) / 4) void weights_stats_kernel(WeightArgs A, WeightPlan P) {
-  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, RT = many_row_tiles(D, BF16), NW = many_waves(D, BF16), THREADS = 64 * NW;
+  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, NW = many_waves(D, BF16), THREADS = 64 * NW;
   extern __shared__ __align__(16) uint4 q_lds[];
-  const int held = min(RT, P.row_tiles) * 32;  // rows of a round
+  const int held = P.round_tiles * 32;
   float2* ml = reinterpret_cast<float2*>(q_lds + static_cast<size_t>(held) * STEPS * 2);  // [wave][row of the round]
   const int lane = threadIdx.x & 63;
   const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
-  each_share<many_keys(D, BF16)>(A, blockIdx.x == 0 && threadIdx.x < 64, [&](const Share& s, int64_t w, int64_t W, int64_t total) {
-    const int32_t rows = s.row.n * A.G, tiles = (rows + 31) / 32, kv = s.row.kv;
-    const int64_t unit = static_cast<int64_t>(s.i) * A.Hk + s.h;
+  each_share<many_keys(D, BF16)>(A, P, blockIdx.x == 0 && threadIdx.x < 64, [&](const Share& s, int64_t w, int64_t W, int64_t total) {
+    const int32_t kv = s.row.kv;
     if (s.lo == 0 && threadIdx.x == 0) {
       // its last workgroup: the largest w' with w' total / W <= its last place
       const int64_t count = ((s.place + s.steps) * W - 1) / total - w + 1;
-      reinterpret_cast<int2*>(static_cast<char*>(A.workspace) + P.meta)[unit] = make_int2(static_cast<int>(w), static_cast<int>(count));
+      reinterpret_cast<int2*>(static_cast<char*>(A.workspace) + P.lse)[s.unit] = make_int2(static_cast<int>(w), static_cast<int>(count));
     }
-    uint4 k[STEPS];
-    auto key_of = [&](int32_t step) { return (step * NW + wave) * kTileKeys; };
-    for (int t0 = 0; t0 < tiles; t0 += RT) {
-      const int nt = min(RT, tiles - t0);
-      lds_barrier();  // Q and the sums of what came before are read
-      for (int e = threadIdx.x; e < nt * STEPS * 64; e += THREADS) q_lds[e] = q_piece<D, BF16>(A, s.i, s.h, rows, t0, e);
-      for (int r = lane; r < nt * 32; r += 64) ml[wave * held + r] = make_float2(-INFINITY, 0.f);
-      lds_barrier();
+    __syncthreads();  // Q and the sums of what came before are read
+    for (int e = threadIdx.x; e < s.tiles * STEPS * 64; e += THREADS) q_lds[e] = q_piece<D, BF16>(A, s.i, s.h, s.row.n * A.G, s.t0, e);
+    for (int r = lane; r < s.tiles * 32; r += 64) ml[wave * held + r] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
 #pragma unroll 1
-      for (int32_t step = s.lo; step < s.hi; ++step) {
-        const int32_t key0 = key_of(step);
-        if (key0 >= kv) break;
-        load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
-        const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
+    for (int32_t step = s.lo; step < s.hi; ++step) {
+      const int32_t key0 = (step * NW + wave) * kTileKeys;
+      if (key0 >= kv) break;
+      uint4 k[STEPS];
+      load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
+      const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-          f32x16_t S;
+      for (int t = 0; t < s.tiles; ++t) {
+        f32x16_t S;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) S[e] = 0.f;
+        for (int e = 0; e < 16; ++e) S[e] = 0.f;
 #pragma unroll
-          for (int o = 0; o < STEPS; ++o) S = mfma_step<BF16>(k[o], q_lds[(t * STEPS + o) * 64 + lane], S);
-          const int row = t * 32 + lane % 32;
-          if (masked) {
-            const int32_t last = kv - s.row.n + (t0 * 32 + row) / A.G;
+        for (int o = 0; o < STEPS; ++o) S = mfma_step<BF16>(k[o], q_lds[(t * STEPS + o) * 64 + lane], S);
+        const int row = t * 32 + lane % 32;
+        if (masked) {
+          const int32_t last = kv - s.row.n + (s.t0 * 32 + row) / A.G;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) S[e] = key0 + result_row(e) <= last ? S[e] : -INFINITY;
-          }
-          const float2 was = ml[wave * held + row];
-          float m = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) m = fmaxf(m, S[e]);
-          m = fmaxf(half_max(m) * A.scale_log2, was.x);
-          const float ref = m == -INFINITY ? 0.f : m;
-          float l = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, -ref));
-          l = fmaf(was.y, __builtin_amdgcn_exp2f(was.x - ref), half_sum(l));
-          if (lane < 32) ml[wave * held + row] = make_float2(m, l);
+          for (int e = 0; e < 16; ++e) S[e] = key0 + result_row(e) <= last ? S[e] : -INFINITY;
         }
-      }
-      __syncthreads();
-      for (int r = threadIdx.x; r < nt * 32; r += THREADS) {
-        float m = -INFINITY, l = 0.f;
+        const float2 was = ml[wave * held + row];
+        float m = -INFINITY;
 #pragma unroll
-        for (int o = 0; o < NW; ++o) m = fmaxf(m, ml[o * held + r].x);
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, S[e]);
+        m = fmaxf(half_max(m) * A.scale_log2, was.x);
         const float ref = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
 #pragma unroll
-        for (int o = 0; o < NW; ++o) l += ml[o * held + r].y * __builtin_amdgcn_exp2f(ml[o * held + r].x - ref);
-        static_cast<float2*>(A.workspace)[(unit + w) * P.Rp + t0 * 32 + r] = make_float2(m, l);
+        for (int e = 0; e < 16; ++e) l += __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, -ref));
+        l = fmaf(was.y, __builtin_amdgcn_exp2f(was.x - ref), half_sum(l));
+        if (lane < 32) ml[wave * held + row] = make_float2(m, l);
       }
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < s.tiles * 32; r += THREADS) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int o = 0; o < NW; ++o) m = fmaxf(m, ml[o * held + r].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int o = 0; o < NW; ++o) l += ml[o * held + r].y * __builtin_amdgcn_exp2f(ml[o * held + r].x - ref);
+      static_cast<float2*>(A.workspace)[(s.unit + w) * held + r] = make_float2(m, l);
     }
   });
 }
@@ -442,79 +453,77 @@ __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPl
   A.score_out[at] = (old ? A.score_in[at] : 0.f) + ((sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]));
 }
 
-// Many rows: each head's weights of the keys, the logits computed again with the
+// Many rows: a unit's weights of the keys, the logits computed again with the
 // operands the other way round, so that a lane holds one key's logits.
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * many_waves(D, BF16), many_waves(D, BF16) / 4) void weights_keys_kernel(WeightArgs A, WeightPlan P) {
-  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, RT = many_row_tiles(D, BF16), NW = many_waves(D, BF16), THREADS = 64 * NW;
+  constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32, NW = many_waves(D, BF16), THREADS = 64 * NW;
   extern __shared__ __align__(16) uint4 q_lds[];
-  __shared__ __align__(16) float lse[RT * 32];
-  const int lane = threadIdx.x & 63;
+  __shared__ __align__(16) float lse[many_row_tiles(D, BF16) * 32];
+  const int held = P.round_tiles * 32, lane = threadIdx.x & 63;
   const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
-  each_share<many_keys(D, BF16)>(A, false, [&](const Share& s, int64_t, int64_t, int64_t) {
-    const int32_t rows = s.row.n * A.G, tiles = (rows + 31) / 32, kv = s.row.kv;
-    const size_t unit = static_cast<size_t>(s.i) * A.Hk + s.h;
-    float* out = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.keys) + unit * P.W;
-    const int2 meta = reinterpret_cast<const int2*>(static_cast<const char*>(A.workspace) + P.meta)[unit];
-    uint4 k[STEPS];
-    auto key_of = [&](int32_t step) { return (step * NW + wave) * kTileKeys; };
-    for (int t0 = 0; t0 < tiles; t0 += RT) {
-      const int nt = min(RT, tiles - t0);
-      lds_barrier();  // what came before is read
-      for (int e = threadIdx.x; e < nt * STEPS * 64; e += THREADS) q_lds[e] = q_piece<D, BF16>(A, s.i, s.h, rows, t0, e);
-      // the parts of each row, joined in a fixed order: log2 of the sum of 2^z; past the last row
-      // +inf, which takes every weight to 0
-      for (int r = threadIdx.x; r < nt * 32; r += THREADS) {
-        const float2* ml = static_cast<const float2*>(A.workspace) + (static_cast<int64_t>(unit) + meta.x) * P.Rp + t0 * 32 + r;
-        float2 sum = make_float2(-INFINITY, 0.f);
+  each_share<many_keys(D, BF16)>(A, P, false, [&](const Share& s, int64_t, int64_t, int64_t) {
+    const int32_t kv = s.row.kv, rows = s.row.n * A.G;
+    float* out = reinterpret_cast<float*>(static_cast<char*>(A.workspace) + P.keys) + s.unit * P.W;
+    const int2 meta = reinterpret_cast<const int2*>(static_cast<const char*>(A.workspace) + P.lse)[s.unit];
+    __syncthreads();  // what came before is read
+    for (int e = threadIdx.x; e < s.tiles * STEPS * 64; e += THREADS) q_lds[e] = q_piece<D, BF16>(A, s.i, s.h, rows, s.t0, e);
+    // the parts of each row, joined in a fixed order: log2 of the sum of 2^z; past the last row
+    // +inf, which takes every weight to 0
+    for (int r = threadIdx.x; r < s.tiles * 32; r += THREADS) {
+      const float2* ml = static_cast<const float2*>(A.workspace) + (s.unit + meta.x) * held + r;
+      float2 sum = make_float2(-INFINITY, 0.f);
 #pragma unroll 8
-        for (int p = 0; p < meta.y; ++p) sum = join(sum, ml[static_cast<size_t>(p) * P.Rp]);
-        lse[r] = t0 * 32 + r < rows ? sum.x + __builtin_amdgcn_logf(sum.y) : INFINITY;
-      }
-      lds_barrier();
+      for (int p = 0; p < meta.y; ++p) sum = join(sum, ml[static_cast<size_t>(p) * held]);
+      lse[r] = s.t0 * 32 + r < rows ? sum.x + __builtin_amdgcn_logf(sum.y) : INFINITY;
+    }
+    __syncthreads();
 #pragma unroll 1
-      for (int32_t step = s.hi - 1; step >= s.lo; --step) {  // the last keys first: they may still be in the last-level cache
-        const int32_t key0 = key_of(step);
-        load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
-        if (key0 >= kv) continue;
-        const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
-        float sum = 0.f;
+    for (int32_t step = s.hi - 1; step >= s.lo; --step) {  // the last keys first: they may still be in the last-level cache
+      const int32_t key0 = (step * NW + wave) * kTileKeys;
+      if (key0 >= kv) continue;
+      uint4 k[STEPS];
+      load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
+      const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
+      float sum = 0.f;
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-          f32x16_t S;
+      for (int t = 0; t < s.tiles; ++t) {
+        f32x16_t S;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) S[e] = 0.f;
+        for (int e = 0; e < 16; ++e) S[e] = 0.f;
 #pragma unroll
-          for (int o = 0; o < STEPS; ++o) S = mfma_step<BF16>(q_lds[(t * STEPS + o) * 64 + lane], k[o], S);
+        for (int o = 0; o < STEPS; ++o) S = mfma_step<BF16>(q_lds[(t * STEPS + o) * 64 + lane], k[o], S);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) S[e] = __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, -lse[t * 32 + result_row(e)]));
-          if (masked) {
+        for (int e = 0; e < 16; ++e) S[e] = __builtin_amdgcn_exp2f(fmaf(S[e], A.scale_log2, -lse[t * 32 + result_row(e)]));
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              S[e] = key0 + lane % 32 <= kv - s.row.n + (t0 * 32 + t * 32 + result_row(e)) / A.G ? S[e] : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sum += S[e];
+          for (int e = 0; e < 16; ++e) S[e] = key0 + lane % 32 <= kv - s.row.n + ((s.t0 + t) * 32 + result_row(e)) / A.G ? S[e] : 0.f;
         }
-        const float total = half_sum(sum);
-        float* at = out + key0 + lane;  // within W
-        if (lane < 32) *at = t0 > 0 ? *at + total : total;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += S[e];
       }
+      const float total = half_sum(sum);
+      if (lane < 32) out[key0 + lane] = total;  // within W
     }
   });
 }
 
-// Many rows: the heads' sums of one key.
-__global__ __launch_bounds__(256) void weights_heads_kernel(WeightArgs A, WeightPlan P) {
+// Many rows: the units' sums of one key.
+__global__ __launch_bounds__(256) void weights_units_kernel(WeightArgs A, WeightPlan P) {
   const int i = blockIdx.y;
   const WeightRow w = weight_row(A, i, false);
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (w.n == 0 || j >= w.kv) return;
   const float* k = reinterpret_cast<const float*>(static_cast<const char*>(A.workspace) + P.keys) +
-                   static_cast<size_t>(i) * A.Hk * P.W + j;
+                   static_cast<size_t>(i) * A.Hk * P.rounds * P.W + j;
+  // a row of fewer queries has fewer rounds
+  const int rounds = ((w.n * A.G + 31) / 32 + P.round_tiles - 1) / P.round_tiles;
   float sum = 0.f;
-#pragma unroll 4
-  for (int h = 0; h < A.Hk; ++h) sum += k[static_cast<size_t>(h) * P.W];
+#pragma unroll 8
+  for (int u = 0; u < A.Hk * P.rounds; ++u) {
+    const float v = k[static_cast<size_t>(u) * P.W];
+    sum += u % P.rounds < rounds ? v : 0.f;
+  }
   const size_t at = static_cast<size_t>(i) * A.width + j;
   const bool old = A.score_in && (!A.have_len || j < A.have_len[i]);
   A.score_out[at] = (old ? A.score_in[at] : 0.f) + sum;
@@ -546,11 +555,12 @@ static int launch_weights_t(const WeightArgs& a, hipStream_t s) {
     }
   } else {
     constexpr int threads = 64 * many_waves(D, BF16);
-    const size_t lds = many_lds(p.row_tiles, D, BF16);
+    const size_t q = static_cast<size_t>(p.round_tiles) * 32 * D * (BF16 ? 2 : 4);
+    const size_t ml = static_cast<size_t>(p.round_tiles) * 32 * many_waves(D, BF16) * sizeof(float2);
     const int64_t blocks = (static_cast<int64_t>(a.width) + 255) / 256;
-    hipLaunchKernelGGL((weights_stats_kernel<D, BF16>), dim3(p.workgroups), dim3(threads), lds, s, a, p);
-    hipLaunchKernelGGL((weights_keys_kernel<D, BF16>), dim3(p.workgroups), dim3(threads), lds, s, a, p);
-    hipLaunchKernelGGL(weights_heads_kernel, dim3(static_cast<unsigned>(blocks), a.batch), dim3(256), 0, s, a, p);
+    hipLaunchKernelGGL((weights_stats_kernel<D, BF16>), dim3(kManyWorkgroups), dim3(threads), q + ml, s, a, p);
+    hipLaunchKernelGGL((weights_keys_kernel<D, BF16>), dim3(kManyWorkgroups), dim3(threads), q, s, a, p);
+    hipLaunchKernelGGL(weights_units_kernel, dim3(static_cast<unsigned>(blocks), a.batch), dim3(256), 0, s, a, p);
   }
   return static_cast<int>(hipGetLastError());
 }
