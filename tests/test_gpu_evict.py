@@ -184,6 +184,97 @@ def test_weights_refused_rows_stay():
         assert code == m.DEV_BAD_PAGE and torch.equal(out[:3], good[:3])
 
 
+@pytest.mark.parametrize("n,G", [(1, 2), (40, 2)])
+def test_weights_of_idle_rows_alone(n, G):
+    m = AH.gdn()
+    P, geom, q, qd, score, width = _weights_case(85, (70, 90), n, None, G, 1, 64, 16, BF16)
+    out = score.cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.attn_weights(geom, P.k.cuda(), P.table.cuda(), _i32((0, 2 ** 31 - 1)), qd, out, m.alloc_attn_weights_workspace(geom, 2, n, width),
+                   n_row=_i32((0, 0)), dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(out, score.cuda())
+
+
+@pytest.mark.parametrize("n", [1, 9])
+def test_weights_many_rows_of_the_batch(n):
+    """More rows than a wave has lanes, most of them short, every third idle; a workspace of a larger call."""
+    m = AH.gdn()
+    ctx = tuple(n + (i * 37) % 90 for i in range(150))
+    n_row = tuple(0 if i % 3 == 2 else 1 + i % n for i in range(150))
+    P, geom, q, qd, score, width = _weights_case(86, ctx, n, n_row, 4, 1, 64, 16, BF16)
+    ws = m.alloc_attn_weights_workspace(geom, 170, geom.max_tree, width + 1000)
+    out = torch.full_like(score, -7.0).cuda()
+    m.attn_weights(geom, P.k.cuda(), P.table.cuda(), _i32(ctx), qd, out, ws, n_row=_i32(n_row))
+    torch.cuda.synchronize()
+    got = AH.host(out)
+    for i, (w, q64, keys) in enumerate(_weights_ref(P, geom, q, ctx, n_row, 16)):
+        if w is None:
+            assert np.all(got[i] == -7.0)
+            continue
+        d = np.abs(got[i, :ctx[i]] - w)
+        assert np.all(d <= _weights_bound(w, 0 * w, q64, keys, geom.c_struct().scale)), (i, d.max())
+        assert np.all(got[i, ctx[i]:] == -7.0)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own: the results of calls one after the other."""
+    m = AH.gdn()
+    for n in (1, 20):
+        cases = [_weights_case(87 + k, (3000 + 100 * k, 50), n, None, 6, 2, 128, 16, BF16) for k in range(2)]
+        args = [(g, P.k.cuda(), P.table.cuda(), _i32((3000 + 100 * k, 50)), qd) for k, (P, g, _, qd, _, _) in enumerate(cases)]
+        outs = [torch.zeros(2, c[5], device="cuda") for c in cases]
+        ws = [m.alloc_attn_weights_workspace(c[1], 2, n, c[5]) for c in cases]
+        for a, o, w in zip(args, outs, ws):
+            m.attn_weights(*a, o, w)
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for _ in range(3):
+            for o in outs:
+                o.zero_()
+            torch.cuda.synchronize()
+            for _ in range(4):
+                for a, o, w, s in zip(args, outs, ws, streams):
+                    m.attn_weights(*a, o, w, stream=s)
+            torch.cuda.synchronize()
+            for o, t in zip(outs, want):
+                assert torch.equal(o, t)
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes: its last pages are written, weighed and moved."""
+    m = AH.gdn()
+    Hk, D, pages = 4, 256, 140000
+    geom = m.AttnGeometry(n_q_heads=8, n_kv_heads=Hk, d_head=D, page_tokens=16, n_pages=pages, max_pages=2)
+    assert pages * Hk * 16 * D * 2 > 2 ** 32
+    cache = m.KVCache(torch.zeros(pages, Hk, 16, D, dtype=BF16, device="cuda"), torch.zeros(pages, Hk, 16, D, dtype=BF16, device="cuda"))
+    g = torch.Generator().manual_seed(130)
+    k, v = (torch.randn(32, Hk, D, generator=g).to(BF16).cuda() for _ in range(2))
+    table = torch.tensor([[pages - 1, pages - 70001]], dtype=torch.int32)
+    slots = torch.cat([table[0, e] * 16 + torch.arange(16, dtype=torch.int32) for e in range(2)]).cuda()
+    rope = m.Rope(rot_dims=256)
+    k_out = torch.empty_like(k)
+    pos = torch.arange(32, dtype=torch.int32, device="cuda")
+    m.rope_rotate(geom, rope, m.rope_turns(rope), pos, k=k, k_out=k_out, v=v, cache=cache, slot_map=slots)
+    torch.cuda.synchronize()
+    for e in range(2):
+        assert torch.equal(cache.k[table[0, e]].transpose(0, 1), k_out[16 * e:16 * e + 16])
+        assert torch.equal(cache.v[table[0, e]].transpose(0, 1), v[16 * e:16 * e + 16])
+    q = torch.randn(1, 1, 8, D, generator=g).to(BF16)
+    score = torch.zeros(1, 32, device="cuda")
+    m.attn_weights(geom, cache.k, table.cuda(), _i32([32]), q.cuda(), score, m.alloc_attn_weights_workspace(geom, 1, 1, 32))
+    keys, q64 = AH.host(k_out), AH.host(q[0])
+    w = co.weights(q64, keys, geom.c_struct().scale)
+    assert np.all(np.abs(AH.host(score[0]) - w) <= _weights_bound(w, 0 * w, q64, keys, geom.c_struct().scale))
+    to = torch.tensor([[(pages - 2) * 16 + 3]], dtype=torch.int32, device="cuda")
+    m.kv_move(geom, cache, slots[31:].view(1, 1), to, _i32([1]))
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k[pages - 2, :, 3], k_out[31]) and torch.equal(cache.v[pages - 2, :, 3], v[31])
+    del cache
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- plans
 
 def _plan_case(seed, ctx, budget, page, sink, recent, settled=None, gone=None, ties=False, width_extra=3, free_extra=0, moves_extra=0):
@@ -280,6 +371,38 @@ def test_plan_against_plain_loops(case, in_place):
     out, err = _plan(c, in_place)
     bad, stack = _check_plan(c, out, in_place)
     assert not bad and stack is not None and err == 0
+
+
+@pytest.mark.parametrize("value", [0.0, -3.5, float("nan"), float("-inf"), float("inf"), 1e-42])
+@pytest.mark.parametrize("ctx,budget", [((8192, 16384, 300), (4000, 16383, 1)), ((20011,), (12345,)), ((100000, 24576), (3, 9000))])
+def test_plan_with_equal_scores(value, ctx, budget):
+    """Rows of one score alone: the lowest indexes stay, whatever the number of equals."""
+    c = _plan_case(96, ctx, budget, 16, 0, 0)
+    c["score"][:] = value
+    out, err = _plan(c)
+    bad, _ = _check_plan(c, out)
+    assert not bad and err == 0
+    # nothing moves: what stays is in place
+    assert out["n_moves"].tolist() == [0] * len(ctx)
+
+
+def test_plan_of_the_widest_rows():
+    m = AH.gdn()
+    c = _plan_case(97, (2 ** 18, 200001), (100000, 200000), 16, 4, 1000, settled=(2 ** 18, 0), gone=(77, 0), width_extra=0)
+    assert c["score"].shape[1] == 2 ** 18
+    out, err = _plan(c)
+    bad, _ = _check_plan(c, out)
+    assert not bad and err == 0
+    with pytest.raises(m.GdnError, match="width: 262145"):
+        _plan(_plan_case(98, (2 ** 18 + 1,), (5,), 16, 0, 0, width_extra=0))
+
+
+@pytest.mark.parametrize("page", [16, 48, 528, 4096, 2 ** 20])
+def test_plan_page_sizes(page):
+    c = _plan_case(99, (5000, 4097, 100), (2500, 4096, 31), page, 1, 7)
+    out, err = _plan(c)
+    bad, _ = _check_plan(c, out)
+    assert not bad and err == 0
 
 
 def test_plan_again_gives_the_same():

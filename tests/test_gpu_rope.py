@@ -233,6 +233,25 @@ def test_infinities_and_nan_stay_in_their_pair():
     assert torch.equal(bad, want)
 
 
+def test_long_rows_of_many_heads():
+    """More units in a token than a workgroup has threads, and more than a product divides exactly."""
+    m = AH.gdn()
+    case = (3, 3000, 300, 256, 256, "pairs", "none", BF16, 0)
+    geom, (rope, freq) = _geom(m, case), _rope(m, case)
+    q, k, pos = _rows(40, 3, 3000, 256, BF16, 0), _rows(41, 3, 300, 256, BF16, 0), _positions(42, 3)
+    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+    m.rope_rotate(geom, rope, m.rope_turns(rope), pos, q=q, k=k, q_out=q_out, k_out=k_out)
+    torch.cuda.synchronize()
+    for a, b in ((q, q_out), (k, k_out)):
+        pick = [0, 1, 2, 149, a.shape[1] - 1]
+        _check(b[:, pick], a[:, pick], pos, rope, freq, BF16)
+    # every head turns by the same angles: heads with the same contents come out the same
+    q[:, 1:] = q[:, :1]
+    m.rope_rotate(geom, rope, m.rope_turns(rope), pos, q=q, q_out=q_out)
+    torch.cuda.synchronize()
+    assert torch.equal(q_out, q_out[:, :1].expand_as(q_out))
+
+
 def test_nothing_to_do():
     m = AH.gdn()
     case = (0, 2, 1, 64, 32, "half", "none", BF16, 0)
