@@ -223,12 +223,12 @@ __device__ __forceinline__ void each_share(const WeightArgs& A, const WeightPlan
 }
 
 // 16 bytes of Q of KV head h of row i, number e of row tiles [t0, ..) in the order of the operands: [tile][step][lane].
-// Rows past the last are zeros.
+// Rows past the last repeat it, whose logits are infinite or NaN only where that row's are: zeros would meet an infinite
+// key as NaN, which no weight of 0 takes out of a key's sum.
 template <int D, bool BF16>
 __device__ __forceinline__ uint4 q_piece(const WeightArgs& A, int i, int h, int32_t rows, int t0, int e) {
   constexpr int ES = BF16 ? 2 : 4, STEPS = D * ES / 32;
-  const int lane = e % 64, s = e / 64 % STEPS, r = (t0 + e / 64 / STEPS) * 32 + lane % 32;
-  if (r >= rows) return make_uint4(0, 0, 0, 0);
+  const int lane = e % 64, s = e / 64 % STEPS, r = min((t0 + e / 64 / STEPS) * 32 + lane % 32, rows - 1);
   const int t = r / A.G;
   const char* q = static_cast<const char*>(A.q) +
                   ((static_cast<int64_t>(i) * A.n + t) * A.q_stride + static_cast<int64_t>(h * A.G + r - t * A.G) * D) * ES;

@@ -154,6 +154,27 @@ def test_weights_masked_keys_do_not_enter(n, G):
             assert np.all(d <= _weights_bound(w, 0 * w, q64, keys, geom.c_struct().scale))
 
 
+@pytest.mark.parametrize("n,G", [(1, 6), (6, 8), (9, 40)])
+def test_weights_of_a_key_with_logits_of_minus_infinity(n, G):
+    """A key that holds an infinity which every query meets with the other sign: its logits are -inf, its weight is 0, and
+    all others are as the oracle has them (rows that only fill a tile of 32 meet it too: 6, 48 and 360 rows)."""
+    m = AH.gdn()
+    ctx = (45 + n,)
+    P, geom, q, _, _, width = _weights_case(75, ctx, n, None, G, 1, 64, 16, BF16)
+    q = q.clone()
+    q[..., 3] = -1.0
+    P.k[P.table[0, 0], :, 5, 3] = float("inf")
+    out = torch.zeros(1, width, device="cuda")
+    m.attn_weights(geom, P.k.cuda(), P.table.cuda(), _i32(ctx), q.cuda(), out, m.alloc_attn_weights_workspace(geom, 1, n, width))
+    torch.cuda.synchronize()
+    w, q64, keys = _weights_ref(P, geom, q, ctx, None, 16)[0]
+    assert w[5] == 0 and np.all(np.isfinite(w))
+    finite = np.where(np.isinf(keys), 0.0, keys)
+    d = np.abs(AH.host(out[0, :ctx[0]]) - w)
+    assert np.all(d <= _weights_bound(w, 0 * w, q64, finite, geom.c_struct().scale)), d
+    assert float(out[0, 5]) == 0.0
+
+
 def test_weights_refused_rows_stay():
     m = AH.gdn()
     ctx = (40, 50, 60, 70)
