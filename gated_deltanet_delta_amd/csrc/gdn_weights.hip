@@ -423,7 +423,8 @@ __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPl
   if (w.n == 0 || from >= w.kv) return;
   const char* ws = static_cast<const char*>(A.workspace);
   const float* z = reinterpret_cast<const float*>(ws + P.keys) + static_cast<size_t>(i) * A.Hk * P.R * P.W + j;
-  const int32_t rows = w.n * A.G, span = static_cast<int32_t>(j - (w.kv - w.n));  // tokens before `span` do not attend j
+  const int64_t span = j - (w.kv - w.n);  // tokens before `span` do not attend j
+  const int32_t rows = w.n * A.G, first = span > 0 ? static_cast<int32_t>(span) * A.G : 0;
   float sum = 0.f;
   for (int h = wave; h < A.Hk; h += 4) {
     const size_t unit = static_cast<size_t>(i) * A.Hk + h;
@@ -442,7 +443,7 @@ __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPl
 #pragma unroll 8
     for (int r = 0; r < rows; ++r) {
       const float p = __builtin_amdgcn_exp2f(z[(static_cast<size_t>(h) * P.R + r) * P.W] - (JOIN ? joined[wave][r] : lse[r]));
-      sum += r >= span * A.G ? p : 0.f;
+      sum += r >= first ? p : 0.f;
     }
   }
   sums[wave][lane] = sum;

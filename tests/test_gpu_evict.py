@@ -175,6 +175,38 @@ def test_weights_of_a_key_with_logits_of_minus_infinity(n, G):
     assert float(out[0, 5]) == 0.0
 
 
+def test_weights_of_a_row_of_2_to_26_tokens():
+    """Keys times heads past 2^31: 32 heads over 2^26 + 1000 tokens, whose pages are all the same one, so that key j has the
+    weight of key j % 512 over the number of its copies.  Parts of 128 keys are joined in eight chains of 65544, four
+    roundings to a join: 4 x 65544 U = 0.0157 of a weight; its own logit, exponential and the parts' own sums are below
+    0.001 of it as _weights_bound has them over 512 keys."""
+    m = AH.gdn()
+    G, D, page, c = 32, 64, 512, 2 ** 26 + 1000
+    pages = -(-c // page)
+    geom = m.AttnGeometry(n_q_heads=G, n_kv_heads=1, d_head=D, page_tokens=page, n_pages=1, max_pages=pages, max_tree=1)
+    g = torch.Generator().manual_seed(140)
+    k, q = torch.randn(1, 1, page, D, generator=g).to(BF16), torch.randn(1, 1, G, D, generator=g).to(BF16)
+    out = torch.full((1, c), float("nan"), device="cuda")
+    ws = m.alloc_attn_weights_workspace(geom, 1, 1, c)
+    m.attn_weights(geom, k.cuda(), torch.zeros(1, pages, dtype=torch.int32, device="cuda"), _i32([c]), q.cuda(), out, ws)
+    torch.cuda.synchronize()
+    del ws
+    q64, keys = AH.host(q[0, 0]), AH.host(k[0, 0])
+    scale = geom.c_struct().scale
+    assert np.all(_weights_bound(np.ones(page), np.zeros(page), q64[None], keys[:, None], scale) < 0.001)
+    e = np.exp(scale * keys @ q64.T)  # [page][G]
+    copies = c // page + (np.arange(page) < c % page)
+    want = torch.tensor((e / (copies[:, None] * e).sum(axis=0)).sum(axis=1)).cuda()
+    for at in range(0, c, 2 ** 20 * page // 16):  # whole pages at a time, and the last part of one
+        part = out[0, at:at + 2 ** 20 * page // 16].double()
+        part = torch.nn.functional.pad(part, (0, -len(part) % page)).view(-1, page)
+        rest = c - at
+        off = (part / want - 1).abs().flatten()[:rest]
+        assert float(off.max()) < 0.017
+    del out
+    torch.cuda.empty_cache()
+
+
 def test_weights_refused_rows_stay():
     m = AH.gdn()
     ctx = (40, 50, 60, 70)
