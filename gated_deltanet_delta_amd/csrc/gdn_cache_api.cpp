@@ -19,7 +19,8 @@ using gdn::launched;
 using gdn::ok;
 
 constexpr int32_t kMaxTokens = 1 << 30;
-constexpr int32_t kMaxWidth = 1 << 30;
+constexpr int32_t kMaxMoves = 1 << 30;
+constexpr int32_t kWeightsMaxWidth = 1 << 29;  // a workgroup of 256 threads to 64 keys: 2^31 threads along x
 constexpr long double kTwoPiLong = 6.283185307179586476925286766559L;
 constexpr double kTwoPi = static_cast<double>(kTwoPiLong);
 
@@ -168,7 +169,7 @@ gdn_status gdn_rope_rotate(const gdn_attn_geometry* g, const gdn_rope* r, const 
 }
 
 size_t gdn_attn_weights_workspace_bytes(const gdn_attn_geometry* g, int32_t batch, int32_t n, int32_t width) {
-  if (check_attn(g) != GDN_OK || batch < 1 || batch > 65535 || n < 1 || n > g->max_tree || check_width(width, kMaxWidth) != GDN_OK)
+  if (check_attn(g) != GDN_OK || batch < 1 || batch > 65535 || n < 1 || n > g->max_tree || check_width(width, kWeightsMaxWidth) != GDN_OK)
     return 0;
   return gdn::weights_workspace_bytes(batch, n, width, g->n_kv_heads, g->n_q_heads / g->n_kv_heads, g->d_head,
                                       g->dtype == GDN_BF16);
@@ -182,7 +183,7 @@ gdn_status gdn_attn_weights(const gdn_attn_geometry* g, const void* q, int64_t q
   if (s != GDN_OK) return s;
   if (n < 1 || n > g->max_tree) return fail(GDN_ERR_RANGE, "n: %d, required: 1..max_tree = %d", n, g->max_tree);
   if (batch < 1 || batch > 65535) return fail(GDN_ERR_RANGE, "batch: %d, required: 1..65535", batch);
-  if ((s = check_width(width, kMaxWidth)) != GDN_OK) return s;
+  if ((s = check_width(width, kWeightsMaxWidth)) != GDN_OK) return s;
   if ((s = check_stride(g, q_stride, g->n_q_heads, "q_stride")) != GDN_OK) return s;
   s = check_workspace(workspace, workspace_bytes, gdn_attn_weights_workspace_bytes(g, batch, n, width));
   if (s != GDN_OK) return s;
@@ -230,8 +231,8 @@ gdn_status gdn_evict_plan(const gdn_attn_geometry* g, const int32_t* kv_len, con
   if (batch < 1 || batch > gdn::kEvictMaxBatch)
     return fail(GDN_ERR_RANGE, "batch: %d, required: 1..%d", batch, gdn::kEvictMaxBatch);
   if ((s = check_width(width, gdn::kEvictMaxWidth)) != GDN_OK) return s;
-  if (max_moves < 1 || max_moves > kMaxWidth)
-    return fail(GDN_ERR_RANGE, "max_moves: %d, required: 1..%d", max_moves, kMaxWidth);
+  if (max_moves < 1 || max_moves > kMaxMoves)
+    return fail(GDN_ERR_RANGE, "max_moves: %d, required: 1..%d", max_moves, kMaxMoves);
   if (sink < 0) return fail(GDN_ERR_RANGE, "sink: %d, required: >= 0", sink);
   if (recent < 0) return fail(GDN_ERR_RANGE, "recent: %d, required: >= 0", recent);
   GDN_NEED_PTR4(kv_len, "kv_len");
@@ -291,8 +292,8 @@ gdn_status gdn_kv_move(const gdn_attn_geometry* g, void* k_cache, void* v_cache,
   if (s != GDN_OK) return s;
   if (batch < 1 || batch > gdn::kEvictMaxBatch)
     return fail(GDN_ERR_RANGE, "batch: %d, required: 1..%d", batch, gdn::kEvictMaxBatch);
-  if (max_moves < 1 || max_moves > kMaxWidth)
-    return fail(GDN_ERR_RANGE, "max_moves: %d, required: 1..%d", max_moves, kMaxWidth);
+  if (max_moves < 1 || max_moves > kMaxMoves)
+    return fail(GDN_ERR_RANGE, "max_moves: %d, required: 1..%d", max_moves, kMaxMoves);
   GDN_NEED_PTR(k_cache, "k_cache");
   GDN_NEED_PTR(v_cache, "v_cache");
   GDN_NEED_PTR4(move_src, "move_src");

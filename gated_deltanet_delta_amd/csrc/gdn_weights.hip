@@ -542,9 +542,7 @@ template <int D, bool BF16>
 static int launch_weights_t(const WeightArgs& a, hipStream_t s) {
   const WeightPlan p = weight_plan(a.batch, a.n, a.width, a.Hk, a.G, a.D, BF16);
   if (p.stored) {
-    if (!grid_fits(p.parts, 64 * kStoredWaves)) return static_cast<int>(hipErrorInvalidValue);
     const int64_t blocks = (static_cast<int64_t>(a.width) + 63) / 64;
-    if (!grid_fits(blocks, 256)) return static_cast<int>(hipErrorInvalidValue);
     hipLaunchKernelGGL((weights_stored_kernel<D, BF16>), dim3(p.parts, a.Hk, a.batch), dim3(64 * kStoredWaves), 0, s, a, p);
     const dim3 grid(static_cast<unsigned>(blocks), a.batch);
     const int64_t parts = static_cast<int64_t>(p.parts) * a.Hk;

@@ -670,7 +670,8 @@ gdn_status gdn_rope_rotate(const gdn_attn_geometry* g, const gdn_rope* r, const 
  * score_in NULL: old = 0; have_len NULL: kv_len.  score_out may be score_in.
  * Rows with n_i = 0 and entries from kv_len[i] on are left as they are.
  *   q [batch][n][H_q][D] (consecutive tokens one row stride apart, row i starting at
- *   token i n; only the first n_i of a row are read); 1 <= n <= max_tree; 1 <= batch <= 65535.
+ *   token i n; only the first n_i of a row are read); 1 <= n <= max_tree; 1 <= batch <= 65535;
+ *   1 <= width <= 2^29.
  *   workspace: device, >= gdn_attn_weights_workspace_bytes() of this batch, n and width (it
  *   grows with each of them); calls that share a workspace must be ordered on one stream.
  * Logits, weights and sums are fp32, each sum in a fixed order.  Masked keys do not enter, whatever

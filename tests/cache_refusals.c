@@ -186,6 +186,7 @@ int main(void) {
   CHECK(44, W(&g, P, 6144, 65536, 1, P, PI, PI, PF, PF, 100, P, BIG) == GDN_ERR_RANGE && has("batch: 65536"));
   CHECK(45, W(&g, P, 6144, 4, 1, P, PI, PI, PF, PF, 0, P, BIG) == GDN_ERR_RANGE && has("width: 0"));
   CHECK(46, W(&g, P, 6144, 4, 1, P, PI, PI, PF, PF, (1 << 30) + 1, P, BIG) == GDN_ERR_RANGE && has("width"));
+  CHECK(39, W(&g, P, 6144, 4, 1, P, PI, PI, PF, PF, (1 << 29) + 1, P, BIG) == GDN_ERR_RANGE && has("width: 536870913, required: 1..536870912"));
   CHECK(47, W(&g, P, 6136, 4, 1, P, PI, PI, PF, PF, 100, P, BIG) == GDN_ERR_RANGE && has("q_stride: 6136"));
   const size_t need = gdn_attn_weights_workspace_bytes(&g, 4, 1, 100);
   CHECK(48, need > 0 && W(&g, P, 6144, 4, 1, P, PI, PI, PF, PF, 100, P, need - 1) == GDN_ERR_WORKSPACE);
