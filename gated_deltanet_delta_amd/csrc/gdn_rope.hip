@@ -9,10 +9,18 @@
 // are what reaches fp32: at most an eighth of a turn, on which the Taylor
 // polynomials below are good to 2^-25.
 //
-// Bound by bytes: a token's cosines and sines (R/2 pairs) are computed once by its
-// workgroup into LDS and serve all its heads.  A unit of work is 16 dimensions of
-// one head of one token, two groups of 8: of a rotated unit, the two halves of
-// eight pairs; of a copied one, 16 dimensions behind one another.
+// A token's cosines and sines (R/2 pairs) are computed once by its workgroup into LDS
+// and serve all its heads.  A unit of work is 16 dimensions of one head of one token,
+// two groups of 8: of a rotated unit, the two halves of eight pairs; of a copied one, 16
+// dimensions behind one another.
+//
+// Bound by bytes; a unit's loads are under way while the angles are made.  bf16, q and k
+// out of place: 32771 tokens of 24 + 4 heads, d 256, 64 dimensions turned, with the cache
+// 201 us (1141 MB, 5.7 TB/s); 5003 tokens of 32 + 8 heads, d 128, all turned, 21.7 (102
+// MB, 4.7 TB/s).  A unit to each of 512 threads; with 2 or 4 units to a thread 202 / 23.3
+// and 217 / 25.0, with 256 threads and 2, 4 or 8 units 206 / 24.3, 217 / 25.2 and 230 / 24.2,
+// with 1024 threads and one unit 205 / 24.2; a thread's next unit loaded ahead is no
+// faster.  4 tokens take 2 - 3 us, the launch and two loads behind one another.
 #include "gdn_device.h"
 #include "gdn_ops.h"
 
@@ -20,7 +28,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 512;
 constexpr int kRopeMaxTokens = 16;  // of a workgroup
 
 // cos and sin of x turns, |x| <= 1/8, as Taylor polynomials in y = 2 pi x, |y| <= pi / 4:
@@ -123,6 +131,7 @@ __device__ __forceinline__ uint32_t divide(uint32_t e, Divisor v) {
 // `k_units` and D / 16 (v only with a cache).
 struct RopePlan {
   Divisor token, q_units, k_units, v_units;  // token: all units of one (m = 0: a workgroup has one token)
+  Divisor pairs;                             // R / 2
   uint32_t q_end, k_end;                     // first unit of k, of v
   int32_t tokens;                            // of a workgroup
 };
@@ -133,11 +142,11 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A, RopePlan
   // cosine and sine of pairs 8 u .. 8 u + 7 of a token: [token][4][R / 16] of two pairs each, so that
   // lanes of neighbouring units read neighbouring words
   extern __shared__ __align__(16) float4 turn[];
-  __shared__ int32_t slots[kRopeMaxTokens];
+  __shared__ int64_t cells[kRopeMaxTokens];  // byte offset of head 0 in the cache, -1: not cached
   const int tid = threadIdx.x, RU = A.R / 16;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * P.tokens;
   const int nt = static_cast<int>(A.n_tokens - t0 < P.tokens ? A.n_tokens - t0 : P.tokens);
-  const uint32_t units = nt * P.token.d, step = gridDim.y * kRopeThreads;
+  const uint32_t units = nt * P.token.d;
 
   struct Unit {
     Eight<BF16> a, b;
@@ -185,23 +194,26 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A, RopePlan
   };
 
   // the first unit's loads are under way while the angles are made
-  uint32_t e = blockIdx.y * kRopeThreads + tid;
+  uint32_t e = tid;
   Unit u;
   if (e < units) fetch(e, u);
-  if (tid < nt) slots[tid] = A.k_cache ? A.slot_map[t0 + tid] : -1;
+  const uint32_t head_bytes = A.D * ES;
+  if (tid < nt && A.k_cache) {
+    const int32_t slot = A.slot_map[t0 + tid];
+    const bool in = slot >= 0 && slot < static_cast<int64_t>(A.n_pages) * A.page;
+    if (!in && slot != -1) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+    const int32_t page = slot / A.page, off = slot - page * A.page;
+    cells[tid] = in ? (static_cast<int64_t>(page) * A.Hk * A.page + off) * head_bytes : -1;
+  }
   float2* turn2 = reinterpret_cast<float2*>(turn);
   for (int i = tid; i < nt * RU * 8; i += kRopeThreads) {
-    const int tt = i / (RU * 8), pair = i - tt * (RU * 8);
+    const int tt = divide(i, P.pairs), pair = i - tt * (RU * 8);
     turn2[(tt * 4 + pair % 8 / 2) * RU * 2 + pair / 8 * 2 + pair % 2] =
         turned(A.position[t0 + tt], A.turns[pair], A.inverse, A.amplitude);
   }
   __syncthreads();
 
-  const int64_t cap = static_cast<int64_t>(A.n_pages) * A.page;
-  for (; e < units;) {
-    Unit next;
-    const bool more = e + step < units;
-    if (more) fetch(e + step, next);
+  while (e < units) {
     if (u.pair >= 0) {
       float a[8], b[8];
       u.a.get(a);
@@ -229,20 +241,17 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A, RopePlan
       u.b.store(u.out + u.bt);
     }
     if (u.cached >= 0) {
-      const int32_t slot = slots[u.token];
-      if (slot >= 0 && slot < cap) {
-        const int32_t page = slot / A.page, off = slot - page * A.page, h = u.cached & ~(1 << 30);
-        char* row = static_cast<char*>(u.cached >> 30 ? A.v_cache : A.k_cache) +
-                    ((static_cast<size_t>(page) * A.Hk + h) * A.page + off) * A.D * ES;
+      const int64_t cell = cells[u.token];
+      if (cell >= 0) {
+        const int32_t h = u.cached & ~(1 << 30);
+        char* row = static_cast<char*>(u.cached >> 30 ? A.v_cache : A.k_cache) + cell +
+                    static_cast<int64_t>(h) * A.page * head_bytes;
         u.a.store(row + u.at);
         u.b.store(row + u.bt);
-      } else if (slot != -1) {
-        report_error(A.dev_err, GDN_DEV_BAD_PAGE);
       }
     }
-    if (!more) break;
-    u = next;
-    e += step;
+    e += kRopeThreads;
+    if (e < units) fetch(e, u);
   }
 }
 
@@ -257,18 +266,16 @@ int launch_rope(const RopeArgs& a, bool bf16, bool pairs, void* stream) {
   p.q_end = a.q ? a.Hq * qu : 0;
   p.k_end = p.q_end + (a.k ? a.Hk * ku : 0);
   p.token = divisor(p.k_end + (a.k_cache ? a.Hk * all : 0));
-  // 2048 units to a workgroup, or one token where it has more; few tokens are
-  // spread over as many workgroups as have a unit per thread
-  int64_t tokens = 2048 / p.token.d;
+  p.pairs = divisor(a.R / 2);
+  // a unit to a thread, or one token to a workgroup where it has more units; fewer tokens where there would be less than 1024 workgroups
+  int64_t tokens = kRopeThreads / p.token.d;
   tokens = tokens < 1 ? 1 : (tokens > kRopeMaxTokens ? kRopeMaxTokens : tokens);
   while (tokens > 1 && a.n_tokens / tokens < 1024) --tokens;
   p.tokens = static_cast<int32_t>(tokens);
-  if (tokens == 1) p.token.m = 0;  // a token may have more units than a product divides; else there are 2048 at most
+  if (tokens == 1) p.token.m = 0;  // a token may have more units than a product divides; else there are kRopeThreads at most
   const int64_t wgs = (a.n_tokens + tokens - 1) / tokens;
-  int64_t split = 1;
-  while (wgs * split < 1024 && split * kRopeThreads < tokens * p.token.d) ++split;
   const size_t lds = static_cast<size_t>(tokens) * a.R / 2 * sizeof(float2);
-  const dim3 grid(static_cast<unsigned>(wgs), static_cast<unsigned>(split));
+  const dim3 grid(static_cast<unsigned>(wgs));
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (!grid_fits(wgs, kRopeThreads)) return static_cast<int>(hipErrorInvalidValue);
   if (bf16 && pairs) hipLaunchKernelGGL((rope_kernel<true, true>), grid, dim3(kRopeThreads), lds, s, a, p);
