@@ -184,7 +184,7 @@ __device__ __forceinline__ void each_share(const WeightArgs& A, const WeightPlan
   // the row that holds place `first`: the last one that does not begin after it
   int i = 0;
   int64_t row_at = 0;
-  for (int base = 0;; base += 64) {
+  for (int base = 0; base < A.batch; base += 64) {
     if (A.batch > 64) inc = scan(base, &mine, false);  // else it is at hand
     const int64_t chunk = __shfl(inc, 63, 64);
     if (row_at + chunk > first) {
@@ -197,7 +197,7 @@ __device__ __forceinline__ void each_share(const WeightArgs& A, const WeightPlan
   }
   i = uniform(i);
   row_at = uniform(row_at);
-  for (int64_t at = first; at < last;) {
+  for (int64_t at = first; at < last && i < A.batch;) {
     Share s;
     s.i = i;
     s.row = weight_row(A, i, false);
