@@ -530,35 +530,53 @@ __global__ __launch_bounds__(kEvictThreads) void evict_plan_kernel(EvictArgs A, 
   }
 }
 
-// K and V rows of the moves: 16 bytes of each per thread and step, a row's moves over
-// the workgroups along x.
-__global__ __launch_bounds__(256) void kv_move_kernel(MoveArgs A) {
+// How the pieces (16 bytes of K and of V) of moves lie: vph of a head, a power of two, vpt of a token.  A workgroup takes
+// `moves` moves at a time; move = e / vpt of piece e is (e vpt_m) >> 32 (0: one move), page = slot / page tokens is
+// (slot page_m) >> (32 + page_s).
+struct MovePlan {
+  int32_t vph_bits, vpt, moves;
+  uint32_t vpt_m, page_m, page_s;
+};
+
+constexpr int kMoveThreads = 256;
+
+// K and V rows of the moves: 16 bytes of each per thread and step, a row's moves over the workgroups along x.
+//
+// Bound by bytes, for few moves by two loads behind one another.  64 rows of up to 2048 moves, 468 MB in pieces of
+// 256 bytes: 97 us, 4.8 TB/s; 4 rows of 128 moves 3 us in a graph of such calls.  Up to 8192 workgroups in all: 4096 103,
+// 16384 93, but a call of 64 rows with room for 2048 moves and none to do takes 3.4 us, then 2.6 and 5.1.  Measured and
+// dropped: two or four pieces of a thread under way at once 102 - 103; the moves of all rows on a line that is cut
+// evenly 96 - 101, and 9 - 13 instead of 9 for 256 rows of 2 moves.
+__global__ __launch_bounds__(kMoveThreads) void kv_move_kernel(MoveArgs A, MovePlan P) {
   const int i = blockIdx.y;
   const int32_t count = A.n_moves[i];
   if (count < 0 || count > A.max_moves) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_error(A.dev_err, GDN_DEV_BAD_LENGTH);
     return;
   }
-  const int vph = A.row_bytes / 16, vpt = vph * A.heads;  // vectors of one head, of one token
-  const int64_t total = static_cast<int64_t>(count) * vpt, cap = static_cast<int64_t>(A.n_pages) * A.page;
+  const int64_t cap = static_cast<int64_t>(A.n_pages) * A.page;
   const size_t list = static_cast<size_t>(i) * A.max_moves;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total; e += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t m = e / vpt;
-    const int v = static_cast<int>(e - m * vpt), h = v / vph, w = v - h * vph;
-    const int32_t src = A.move_src[list + m], dst = A.move_dst[list + m];
-    if (src < 0 || src >= cap || dst < 0 || dst >= cap) {
-      if ((src < -1 || src >= cap) || (dst < -1 || dst >= cap)) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
-      continue;
+  for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * P.moves; m0 < count; m0 += static_cast<int64_t>(gridDim.x) * P.moves) {
+    const int64_t left = count - m0;
+    const uint32_t pieces = (left < P.moves ? static_cast<int32_t>(left) : P.moves) * P.vpt;
+    for (uint32_t e = threadIdx.x; e < pieces; e += kMoveThreads) {
+      const uint32_t m = static_cast<uint32_t>((static_cast<uint64_t>(e) * P.vpt_m) >> 32), v = e - m * P.vpt;
+      const uint32_t h = v >> P.vph_bits, w = v & ((1u << P.vph_bits) - 1);
+      const int32_t src = A.move_src[list + m0 + m], dst = A.move_dst[list + m0 + m];
+      if (src < 0 || src >= cap || dst < 0 || dst >= cap) {
+        if ((src < -1 || src >= cap) || (dst < -1 || dst >= cap)) report_error(A.dev_err, GDN_DEV_BAD_PAGE);
+        continue;
+      }
+      auto place = [&](uint32_t slot) {
+        const uint32_t page = __umulhi(slot, P.page_m) >> P.page_s, off = slot - page * A.page;
+        return ((static_cast<size_t>(page) * A.heads + h) * A.page + off) * A.row_bytes + 16 * w;
+      };
+      const size_t from = place(src), to = place(dst);
+      const uint4 kv = *reinterpret_cast<const uint4*>(static_cast<const char*>(A.k_cache) + from);
+      const uint4 vv = *reinterpret_cast<const uint4*>(static_cast<const char*>(A.v_cache) + from);
+      *reinterpret_cast<uint4*>(static_cast<char*>(A.k_cache) + to) = kv;
+      *reinterpret_cast<uint4*>(static_cast<char*>(A.v_cache) + to) = vv;
     }
-    auto place = [&](int32_t slot) {
-      const int32_t page = slot / A.page, off = slot - page * A.page;
-      return ((static_cast<size_t>(page) * A.heads + h) * A.page + off) * A.row_bytes + 16 * w;
-    };
-    const size_t from = place(src), to = place(dst);
-    const uint4 kv = *reinterpret_cast<const uint4*>(static_cast<const char*>(A.k_cache) + from);
-    const uint4 vv = *reinterpret_cast<const uint4*>(static_cast<const char*>(A.v_cache) + from);
-    *reinterpret_cast<uint4*>(static_cast<char*>(A.k_cache) + to) = kv;
-    *reinterpret_cast<uint4*>(static_cast<char*>(A.v_cache) + to) = vv;
   }
 }
 
@@ -580,12 +598,22 @@ int launch_evict_plan(const EvictArgs& a, void* stream) {
 }
 
 int launch_kv_move(const MoveArgs& a, void* stream) {
-  const int64_t total = static_cast<int64_t>(a.max_moves) * a.heads * (a.row_bytes / 16);
-  int64_t wgs = (total + 255) / 256;
-  const int64_t most = a.batch < 4096 ? 4096 / a.batch : 1;
-  if (wgs > most) wgs = most;
-  hipLaunchKernelGGL(kv_move_kernel, dim3(static_cast<unsigned>(wgs), a.batch), dim3(256), 0,
-                     static_cast<hipStream_t>(stream), a);
+  MovePlan p{};
+  const uint32_t vph = a.row_bytes / 16;  // 8, 16, 32 or 64
+  p.vph_bits = 31 - __builtin_clz(vph);
+  p.vpt = static_cast<int32_t>(vph) * a.heads;
+  p.moves = p.vpt < kMoveThreads ? kMoveThreads / p.vpt : 1;
+  // e / d = (e m) >> 32 with m = ceil(2^32 / d) for e and d up to kMoveThreads: m d exceeds 2^32 by less than d, so
+  // e m / 2^32 exceeds e / d by less than e / 2^32 < 1 / d
+  p.vpt_m = p.moves == 1 ? 0 : static_cast<uint32_t>(((1ull << 32) + p.vpt - 1) / p.vpt);
+  // s / d = (s m) >> (31 + l) with 2^(l - 1) < d <= 2^l and m = ceil(2^(31 + l) / d) for s < 2^31: m d exceeds
+  // 2^(31 + l) by less than d <= 2^l, so s m / 2^(31 + l) exceeds s / d by less than 1 / d
+  const int l = 32 - __builtin_clz(a.page - 1);
+  p.page_m = static_cast<uint32_t>(((1ull << (31 + l)) + a.page - 1) / a.page);
+  p.page_s = l - 1;
+  const int64_t all = (static_cast<int64_t>(a.max_moves) + p.moves - 1) / p.moves, most = 8192 / a.batch;  // batch <= kEvictMaxBatch = 4096
+  hipLaunchKernelGGL(kv_move_kernel, dim3(static_cast<unsigned>(all < most ? all : most), a.batch), dim3(kMoveThreads), 0,
+                     static_cast<hipStream_t>(stream), a, p);
   return static_cast<int>(hipGetLastError());
 }
 
