@@ -18,7 +18,7 @@
 //
 // Bound by bytes.  24 heads on 4, d 256: one query at 4 x 8K tokens 23 us (67 MB: 15.6 us for
 // the logits, 4.3 TB/s, 5.5 for the sums), 32 queries over 4 x 100K 407 us (820 MB twice, 4.0
-// TB/s); 32 heads on 8, d 128, 4 queries in each of 64 ragged rows 116 us (303 MB of K, 190 MB of
+// TB/s); 32 heads on 8, d 128, 4 queries in each of 64 ragged rows 116 us (330 MB of K, 170 MB of
 // logits written and read).  Many rows, measured and dropped: 64 keys per wave in 8
 // waves instead of 32 in 16, 580 us; workgroups of a fixed number of keys, 473; one group of
 // heads at a time, so that the second reading might find K in the last-level cache, 512 - 940.
