@@ -546,6 +546,15 @@ def test_moves(Hk, D, page, dtype, counts):
     assert torch.equal(cache.k.view(bits), want[0].view(bits)) and torch.equal(cache.v.view(bits), want[1].view(bits))
 
 
+@pytest.mark.parametrize("Hk,D,page,dtype,counts", [
+    (40, 64, 48, BF16, (5, 9)),                                  # a token's pieces are more than a workgroup's threads
+    (3, 64, 80, BF16, (200, 31, 11)),                            # ten moves of 24 pieces to a workgroup
+    (1, 64, 16, BF16, (1000,) + (0,) * 597 + (40, 999)),         # 600 rows: 13 workgroups to a row, which go round
+    (7, 128, 4096, F32, (64,))])
+def test_moves_of_many_heads_rows_and_page_sizes(Hk, D, page, dtype, counts):
+    test_moves(Hk, D, page, dtype, counts)
+
+
 def test_moves_refused():
     m = AH.gdn()
     geom = m.AttnGeometry(n_q_heads=1, n_kv_heads=1, d_head=64, page_tokens=16, n_pages=4, max_pages=4)

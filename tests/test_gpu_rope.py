@@ -148,6 +148,40 @@ def test_write_into_the_cache(case, k_in_place):
     assert torch.equal(cache.k.view(bits), want_k.view(bits)) and torch.equal(cache.v.view(bits), want_v.view(bits))
 
 
+@pytest.mark.parametrize("n,Hq,Hk,D,rot,dtype", [(17001, 2, 1, 64, 32, BF16), (5003, 5, 1, 128, 128, BF16), (20000, 1, 1, 64, 16, F32)])
+def test_many_tokens_give_the_bits_of_few(n, Hq, Hk, D, rot, dtype):
+    """Calls whose workgroups take several tokens, the last one fewer, against calls of at most 700 tokens, cache and
+    in-place rotation included; the first tokens against the oracle."""
+    m = AH.gdn()
+    case = (n, Hq, Hk, D, rot, "half", "parts", dtype, 0)
+    rope, freq = _rope(m, case)
+    turns, pages = m.rope_turns(rope), -(-n // 16) + 3
+    g = _geom(m, case, pages=pages)
+    q, k, v, pos = _rows(20, n, Hq, D, dtype, 0), _rows(21, n, Hk, D, dtype, 0), _rows(22, n, Hk, D, dtype, 0), _positions(23, n)
+    slots = torch.randperm(pages * 16, generator=torch.Generator().manual_seed(24))[:n].to(torch.int32)
+    slots[5::11] = -1
+    slots = slots.cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(step):
+        cache = m.KVCache(*(torch.zeros(pages, Hk, 16, D, dtype=dtype, device="cuda") for _ in range(2)))
+        q_out, k_in = torch.empty_like(q), k.clone()
+        for at in range(0, n, step):
+            e = slice(at, min(n, at + step))
+            m.rope_rotate(g, rope, turns, pos[e], q=q[e], q_out=q_out[e], k=k_in[e], v=v[e], cache=cache, slot_map=slots[e], dev_err=err)
+        alone = k.clone()
+        m.rope_rotate(g, rope, turns, pos, k=alone, dev_err=err)  # the rotated dimensions alone move
+        return q_out, k_in, cache.k, cache.v, alone
+    whole, parts = run(n), run(700)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for a, b in zip(whole, parts):
+        assert torch.equal(a, b)
+    assert torch.equal(whole[4], whole[1])
+    _check(whole[0][:200], q[:200], pos[:200], rope, freq, dtype)
+    _check(whole[1][-200:], k[-200:], pos[-200:], rope, freq, dtype)
+
+
 def test_slots_outside_the_cache():
     m = AH.gdn()
     case = (4, 2, 2, 64, 32, "half", "none", BF16, 0)
