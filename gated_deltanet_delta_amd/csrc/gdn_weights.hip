@@ -100,21 +100,21 @@ WeightPlan weight_plan(int32_t batch, int32_t n, int32_t width, int Hk, int G, i
   p.parts = static_cast<int32_t>((static_cast<int64_t>(width) + kStoredKeys - 1) / kStoredKeys);
   p.W = static_cast<int32_t>(round_up(width, 64));
   const int64_t heads = static_cast<int64_t>(batch) * Hk;
-  // as many row tiles to a round as fit, or fewer where that leaves workgroups without work (64 queries of 8 heads over 100
-  // tokens, d 256: 20 us, with the most that fit 71; 8 KV heads of 20000 tokens, d 128, 512 rows each: 233, 247)
+  // as many row tiles to a round as fit, or fewer where that leaves workgroups without work, but not so few that there are
+  // more units of one step than workgroups (64 queries of 8 heads over 100 tokens, d 256: 20 us, with the most that fit 71;
+  // 8 KV heads of 20000 tokens, d 128, 512 rows each: 233, with fewer 247; 4 rows of 5000 tokens, 4 KV heads, d 256, 192
+  // query rows each: 54, with twice the rounds 60)
   const int64_t steps = (static_cast<int64_t>(width) + many_keys(D, bf16) - 1) / many_keys(D, bf16);
-  const int64_t most = many_row_tiles(D, bf16), even = steps * heads >= kManyWorkgroups ? most : p.row_tiles * heads * steps / kManyWorkgroups;
-  p.round_tiles = static_cast<int32_t>(even < 1 ? 1 : (even < most ? even : most));
+  const int64_t most = many_row_tiles(D, bf16), least = (p.row_tiles + most - 1) / most, fill = kManyWorkgroups / (steps * heads);
+  const int64_t rounds = fill < least ? least : (fill < p.row_tiles ? fill : p.row_tiles);
+  p.round_tiles = static_cast<int32_t>((p.row_tiles + rounds - 1) / rounds);
   p.rounds = (p.row_tiles + p.round_tiles - 1) / p.round_tiles;
-  p.round_tiles = (p.row_tiles + p.rounds - 1) / p.rounds;  // as many rounds, of like size
-  p.rounds = (p.row_tiles + p.round_tiles - 1) / p.round_tiles;
-  // A size that grows with each argument.  Units are heads x the rounds of `most`; or, where there are more
-  // rounds than that, steps x heads < kManyWorkgroups, and they are at most 2 kManyWorkgroups / steps + heads,
-  // so their sums at most 2 kManyWorkgroups many_keys() + heads W.
-  const size_t base = heads * ((p.row_tiles + most - 1) / most), units = base + 2 * kManyWorkgroups + heads;
+  // A size that grows with each argument.  Units are heads x least; or, where there are more rounds than that, at
+  // most kManyWorkgroups / steps, whose sums are kManyWorkgroups many_keys() at most, as W <= steps many_keys().
+  const size_t base = heads * least, units = base + kManyWorkgroups;
   p.lse = round_up(p.stored ? heads * p.parts * p.Rp * sizeof(float2) : (units + kManyWorkgroups) * most * 32 * sizeof(float2), 256);
   p.keys = p.lse + round_up(p.stored ? heads * p.Rp * sizeof(float) : units * sizeof(int2), 256);
-  const size_t sums = (base + heads) * p.W + static_cast<size_t>(2 * kManyWorkgroups) * many_keys(D, bf16);
+  const size_t sums = base * p.W + static_cast<size_t>(kManyWorkgroups) * many_keys(D, bf16);
   p.total = p.keys + (p.stored ? heads * p.R * static_cast<size_t>(p.W) : sums) * sizeof(float);
   return p;
 }
