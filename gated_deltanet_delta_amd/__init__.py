@@ -849,8 +849,7 @@ def rope_frequencies(rope: Rope) -> list:
 def rope_turns(rope: Rope, device="cuda") -> torch.Tensor:
     """gdn_rope_turns: the frequencies as 64-bit fractions of a turn (int64 [rot_dims / 2], the bits of uint64), made
     once and kept by the caller for rope_rotate."""
-    signed = [t - (1 << 64) if t >> 63 else t for t in _rope_tables(rope)[1]]
-    return torch.tensor(signed, dtype=torch.int64, device=device)
+    return torch.frombuffer(_rope_tables(rope)[1], dtype=torch.int64).to(device)
 
 
 def rope_rotate(geom: AttnGeometry, rope: Rope, turns, position, q=None, k=None, q_out=None, k_out=None, v=None,
