@@ -346,6 +346,9 @@ __global__ __launch_bounds__(64 * many_waves(D, BF16), many_waves(D, BF16) / 4) 
       uint4 k[STEPS];
       load_k<D, BF16>(A, s.i, s.h, key0, kv, k);
       const bool masked = key0 + kTileKeys > kv - s.row.n + 1;
+      // lanes l + 32 read below what lanes l wrote in the step before
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
       for (int t = 0; t < s.tiles; ++t) {
         f32x16_t S;
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(256) void weights_join_kernel(WeightArgs A, WeightP
 // parts of its rows itself, which saves a launch where they are few (kFewParts).
 template <bool JOIN>
 __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPlan P) {
-  __shared__ float sums[4][64], joined[4][32];
+  __shared__ float sums[4][64];
   const int i = blockIdx.y, lane = threadIdx.x & 63;
   const int32_t wave = uniform(static_cast<int32_t>(threadIdx.x / 64));
   const WeightRow w = weight_row(A, i, false);
@@ -429,6 +432,7 @@ __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPl
   for (int h = wave; h < A.Hk; h += 4) {
     const size_t unit = static_cast<size_t>(i) * A.Hk + h;
     const float* lse = reinterpret_cast<const float*>(ws + P.lse) + unit * P.Rp;
+    float joined = 0.f;  // of row `lane`
     if constexpr (JOIN) {
       // a lane per row and every 64 / 2^bits-th part, 2^bits >= rows
       const int bits = rows <= 8 ? 3 : (rows <= 16 ? 4 : 5), row = lane & ((1 << bits) - 1);
@@ -438,11 +442,12 @@ __global__ __launch_bounds__(256) void weights_sum_kernel(WeightArgs A, WeightPl
 #pragma unroll 8
       for (int p = lane >> bits; p < count; p += 64 >> bits) s = join(s, ml[static_cast<size_t>(p) * P.Rp]);
       for (int d = 1 << bits; d < 64; d <<= 1) s = join(s, make_float2(__shfl_xor(s.x, d, 64), __shfl_xor(s.y, d, 64)));
-      if (lane >> bits == 0) joined[wave][row] = s.x + __builtin_amdgcn_logf(s.y);
+      joined = s.x + __builtin_amdgcn_logf(s.y);
     }
 #pragma unroll 8
     for (int r = 0; r < rows; ++r) {
-      const float p = __builtin_amdgcn_exp2f(z[(static_cast<size_t>(h) * P.R + r) * P.W] - (JOIN ? joined[wave][r] : lse[r]));
+      const float norm = JOIN ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(joined), r)) : lse[r];
+      const float p = __builtin_amdgcn_exp2f(z[(static_cast<size_t>(h) * P.R + r) * P.W] - norm);
       sum += r >= first ? p : 0.f;
     }
   }

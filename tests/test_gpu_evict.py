@@ -270,6 +270,17 @@ def test_weights_many_rows_of_the_batch(n):
         assert np.all(got[i, ctx[i]:] == -7.0)
 
 
+@pytest.mark.parametrize("case", [
+    # up to 320 parts of 128 keys times KV heads, and 4096 over all rows: the parts are joined where the weights are summed,
+    # a wave taking KV heads 0, 4, .. one after the other; 3, 12 and 32 query rows of a head, fewer in some batch rows
+    ((1000, 130, 5), 1, None, 24, 8, 64, 16, BF16),
+    ((1000, 130, 6), 6, (6, 1, 5), 10, 5, 128, 16, BF16),
+    ((999, 8, 257), 8, (8, 8, 3), 28, 7, 64, 16, F32)],
+    ids=lambda c: f"{len(c[0])}x{c[0][0]}-{c[1]}-{c[3]}on{c[4]}-{c[5]}")
+def test_weights_of_few_rows_and_more_heads_than_waves(case):
+    test_weights_against_the_oracle(case)
+
+
 def test_two_calls_at_once():
     """On two streams, each with a workspace of its own: the results of calls one after the other."""
     m = AH.gdn()
