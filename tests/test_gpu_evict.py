@@ -275,7 +275,11 @@ def test_weights_many_rows_of_the_batch(n):
     # a wave taking KV heads 0, 4, .. one after the other; 3, 12 and 32 query rows of a head, fewer in some batch rows
     ((1000, 130, 5), 1, None, 24, 8, 64, 16, BF16),
     ((1000, 130, 6), 6, (6, 1, 5), 10, 5, 128, 16, BF16),
-    ((999, 8, 257), 8, (8, 8, 3), 28, 7, 64, 16, F32)],
+    ((999, 8, 257), 8, (8, 8, 3), 28, 7, 64, 16, F32),
+    # more parts of a row, or of all rows: they are joined in a kernel of their own
+    ((6000, 70, 129), 3, (3, 1, 2), 16, 8, 128, 16, BF16),
+    ((8200, 40), 8, (8, 7), 20, 5, 64, 48, F32),
+    (tuple(4 + (i * 37) % 590 for i in range(150)), 4, tuple((1 + i) % 5 for i in range(150)), 16, 8, 64, 16, BF16)],
     ids=lambda c: f"{len(c[0])}x{c[0][0]}-{c[1]}-{c[3]}on{c[4]}-{c[5]}")
 def test_weights_of_few_rows_and_more_heads_than_waves(case):
     test_weights_against_the_oracle(case)
