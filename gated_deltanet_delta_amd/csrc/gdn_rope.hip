@@ -255,6 +255,22 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs A, RopePlan
   }
 }
 
+// The call of n tokens from token t on.
+static RopeArgs rope_part(const RopeArgs& a, int64_t t, int64_t n) {
+  RopeArgs part = a;
+  auto in = [t](const void* p, int64_t stride) { return p ? static_cast<const char*>(p) + t * stride : nullptr; };
+  auto out = [t](void* p, int64_t stride) { return p ? static_cast<char*>(p) + t * stride : nullptr; };
+  part.q = in(a.q, a.q_stride);
+  part.k = in(a.k, a.k_stride);
+  part.v = in(a.v, a.v_stride);
+  part.q_out = out(a.q_out, a.q_out_stride);
+  part.k_out = out(a.k_out, a.k_out_stride);
+  part.position = a.position + t;
+  part.slot_map = a.slot_map ? a.slot_map + t : nullptr;
+  part.n_tokens = static_cast<int32_t>(n);
+  return part;
+}
+
 int launch_rope(const RopeArgs& a, bool bf16, bool pairs, void* stream) {
   RopePlan p{};
   const uint32_t all = a.D / 16, rot = a.R / 16;
@@ -273,16 +289,21 @@ int launch_rope(const RopeArgs& a, bool bf16, bool pairs, void* stream) {
   while (tokens > 1 && a.n_tokens / tokens < 1024) --tokens;
   p.tokens = static_cast<int32_t>(tokens);
   if (tokens == 1) p.token.m = 0;  // a token may have more units than a product divides; else there are kRopeThreads at most
-  const int64_t wgs = (a.n_tokens + tokens - 1) / tokens;
   const size_t lds = static_cast<size_t>(tokens) * a.R / 2 * sizeof(float2);
-  const dim3 grid(static_cast<unsigned>(wgs));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!grid_fits(wgs, kRopeThreads)) return static_cast<int>(hipErrorInvalidValue);
-  if (bf16 && pairs) hipLaunchKernelGGL((rope_kernel<true, true>), grid, dim3(kRopeThreads), lds, s, a, p);
-  else if (bf16) hipLaunchKernelGGL((rope_kernel<true, false>), grid, dim3(kRopeThreads), lds, s, a, p);
-  else if (pairs) hipLaunchKernelGGL((rope_kernel<false, true>), grid, dim3(kRopeThreads), lds, s, a, p);
-  else hipLaunchKernelGGL((rope_kernel<false, false>), grid, dim3(kRopeThreads), lds, s, a, p);
-  return static_cast<int>(hipGetLastError());
+  // more tokens than a launch's workgroups take go in several launches
+  const int64_t most = 0xffffffffll / kRopeThreads * tokens;
+  for (int64_t t = 0; t < a.n_tokens; t += most) {
+    const RopeArgs part = rope_part(a, t, a.n_tokens - t < most ? a.n_tokens - t : most);
+    const dim3 grid(static_cast<unsigned>((part.n_tokens + tokens - 1) / tokens));
+    if (bf16 && pairs) hipLaunchKernelGGL((rope_kernel<true, true>), grid, dim3(kRopeThreads), lds, s, part, p);
+    else if (bf16) hipLaunchKernelGGL((rope_kernel<true, false>), grid, dim3(kRopeThreads), lds, s, part, p);
+    else if (pairs) hipLaunchKernelGGL((rope_kernel<false, true>), grid, dim3(kRopeThreads), lds, s, part, p);
+    else hipLaunchKernelGGL((rope_kernel<false, false>), grid, dim3(kRopeThreads), lds, s, part, p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return static_cast<int>(err);
+  }
+  return 0;
 }
 
 }  // namespace gdn

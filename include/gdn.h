@@ -637,6 +637,7 @@ gdn_status gdn_rope_turns(const gdn_rope* r, double* freq, uint64_t* turns);
  *   k_cache NULL: no cache (v_cache, v, slot_map are not used).
  * All arithmetic is fp32, rounded once; the copied dimensions keep their bits.
  * A slot outside the cache sets GDN_DEV_BAD_PAGE and is skipped.  Equal slots in one call race.
+ * 0 <= n_tokens <= 2^30.
  */
 gdn_status gdn_rope_rotate(const gdn_attn_geometry* g, const gdn_rope* r, const uint64_t* turns, const int32_t* position,
                            int32_t n_tokens, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,

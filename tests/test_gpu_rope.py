@@ -286,6 +286,39 @@ def test_long_rows_of_many_heads():
     assert torch.equal(q_out, q_out[:, :1].expand_as(q_out))
 
 
+def test_more_tokens_than_a_launch_takes():
+    """2^27 + 100 tokens of 64 dimensions of q, k and v in one row each, 16 tokens to a workgroup of 512 threads: past 2^32
+    threads, so the call takes two launches, 116 tokens in the second.  Equal to calls of 2^20 tokens; the slots of the first
+    tokens, of those on both sides of 2^27 - 16, where the second launch begins, and of the last are in the cache."""
+    m = AH.gdn()
+    step, n = 2 ** 20, 2 ** 27 + 100
+    g = torch.Generator(device="cuda").manual_seed(9)
+    geom = m.AttnGeometry(n_q_heads=1, n_kv_heads=1, d_head=64, page_tokens=16, n_pages=40, max_pages=40)
+    rope = m.Rope(rot_dims=16)
+    turns = m.rope_turns(rope)
+    block = torch.randn(step, 3, 64, generator=g, device="cuda").to(BF16)
+    rows = torch.empty(n, 3, 64, dtype=BF16, device="cuda")
+    for at in range(0, n, step):
+        rows[at:at + step] = block[:min(step, n - at)]
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    here = [0, 1, 511, 2 ** 27 - 18, 2 ** 27 - 17, 2 ** 27 - 16, 2 ** 27 - 15, n - 2, n - 1]
+    slots[torch.tensor(here, device="cuda")] = torch.arange(len(here), dtype=torch.int32, device="cuda") * 17
+    cache, err = m.KVCache.zeros(geom), torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.rope_rotate(geom, rope, turns, pos, q=rows[:, :1], k=rows[:, 1:2], v=rows[:, 2:], cache=cache, slot_map=slots, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for i, t in enumerate(here):
+        assert torch.equal(cache.k[i * 17 // 16, :, i * 17 % 16], rows[t, 1:2]) and torch.equal(cache.v[i * 17 // 16, :, i * 17 % 16], rows[t, 2:])
+    for at in range(0, n, step):
+        part = block[:min(step, n - at)].clone()
+        m.rope_rotate(geom, rope, turns, pos[at:at + step], q=part[:, :1], k=part[:, 1:2], dev_err=err)
+        assert torch.equal(rows[at:at + step], part), at
+    assert int(err.item()) == 0
+    del rows, pos, slots
+    torch.cuda.empty_cache()
+
+
 def test_nothing_to_do():
     m = AH.gdn()
     case = (0, 2, 1, 64, 32, "half", "none", BF16, 0)
