@@ -271,6 +271,22 @@ def test_weights_many_rows_of_the_batch(n):
 
 
 @pytest.mark.parametrize("case", [
+    # where 256 workgroups have more to do than one step of keys (512, fp32 d 256: 256) of one round of row tiles each, they take
+    # steps one after the other and go from one round, KV head and batch row to the next: 320 steps over all, 6 row tiles to
+    # a round; 720 of 2 tiles, an idle row; 324 of two rounds of 7 tiles, of one round in a batch row of fewer queries; 1112 of
+    # 2 tiles; 294 of two rounds of 2.  (The longer ones of the cases further up make at most 256 steps, a workgroup each: 64
+    # heads of 9 queries eighteen rounds of one tile, 5 heads of 48 queries on each of 2 KV heads eight.)
+    ((17000, 9001, 700, 12345, 40), 32, None, 24, 4, 256, 528, BF16),
+    ((20000, 9001, 700, 40, 15000), 5, (5, 4, 5, 0, 3), 64, 8, 64, 16, BF16),
+    ((25000, 700, 15001, 64), 64, (64, 10, 64, 64), 14, 2, 64, 16, BF16),
+    ((40000, 50, 30000), 7, None, 40, 8, 64, 528, F32),
+    ((9000, 30, 5001, 300), 30, (30, 30, 7, 29), 12, 3, 256, 48, F32)],
+    ids=lambda c: f"{len(c[0])}x{c[0][0]}-{c[1]}-{c[3]}on{c[4]}-{c[5]}")
+def test_weights_of_many_rows_and_several_steps_to_a_workgroup(case):
+    test_weights_against_the_oracle(case)
+
+
+@pytest.mark.parametrize("case", [
     # up to 320 parts of 128 keys times KV heads, and 4096 over all rows: the parts are joined where the weights are summed,
     # a wave taking KV heads 0, 4, .. one after the other; 3, 12 and 32 query rows of a head, fewer in some batch rows
     ((1000, 130, 5), 1, None, 24, 8, 64, 16, BF16),
