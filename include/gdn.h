@@ -707,8 +707,10 @@ size_t gdn_attn_weights_workspace_bytes(const gdn_attn_geometry* g, int32_t batc
  * A row with c outside [0, min(width, max_pages P)], settled outside [0, c], evicted < 0 or c + evicted beyond 2^31 - 1
  * sets GDN_DEV_BAD_LENGTH; it is left as it is, nothing of its score_out and token_pos_out written.  A row to be cut with
  * b < sink + recent or min(b, c - b) > max_moves sets GDN_DEV_BAD_LENGTH and keeps all its tokens.
- * GDN_DEV_BAD_PAGE: n_free outside [0, n_pages], or more pages on the stack than the cache has (all rows then keep
- * all their tokens), or a page id outside the cache (the slots are then -1 and the token is not moved).
+ * GDN_DEV_BAD_PAGE: n_free outside [0, n_pages], or more pages on the stack than the cache has, counted with every entry
+ * that comes free (all rows then keep all their tokens); or a page id outside the cache among the entries that a row's
+ * moves or freed pages take: a slot on such a page is -1, the pair is not moved and its gap keeps its token,
+ * score and position; freed entries that are no page are left out of the stack.
  * 1 <= batch <= 4096, 1 <= width <= 2^18, max_moves >= 1, sink, recent >= 0.
  */
 gdn_status gdn_evict_plan(const gdn_attn_geometry* g, const int32_t* kv_len, const int32_t* budget, const float* score,

@@ -59,7 +59,8 @@ def weights(q, keys, scale):
 
 
 def evict(page, n_pages, max_pages, kv_len, budget, score, token_pos, row_state, tables, free, n_free, sink, recent, max_moves):
-    """The plan as lists per row; entries that it does not write are None."""
+    """The plan as lists per row; entries that it does not write are None.  A table's entries that are no pages of the cache:
+    slot -1, the gap of such a pair keeps its token, and they do not get onto the stack."""
     B, width = score.shape
     rows, stack = [], [int(x) for x in free[:n_free]]
     most = min(width, max_pages * page)
@@ -94,14 +95,16 @@ def evict(page, n_pages, max_pages, kv_len, budget, score, token_pos, row_state,
 
         kept = set(sorted(range(c), key=rank)[:b])
         movers, holes = [j for j in range(b, c) if j in kept], [j for j in range(b) if j not in kept]
-        left = list(range(b))
-        for j, h in zip(movers, holes):
-            left[h] = j
 
         def slot(j):
-            return int(tables[i, j // page]) * page + j % page
+            p = int(tables[i, j // page])
+            return p * page + j % page if 0 <= p < n_pages else -1
+
+        left = list(range(b))
+        for j, h in zip(movers, holes):
+            left[h] = j if slot(j) >= 0 and slot(h) >= 0 else h
 
         rows.append(dict(kv_len=b, state=[b, gone + c - b], score=[float(score[i, j]) for j in left], pos=[pos[j] for j in left],
                          src=[slot(j) for j in movers], dst=[slot(j) for j in holes]))
-        stack += [int(p) for p in tables[i, -(-b // page):-(-c // page)]]
+        stack += [int(p) for p in tables[i, -(-b // page):-(-c // page)] if 0 <= p < n_pages]
     return rows, stack if stack_ok else None, any(s in ("refused", "kept, bad") for s in states)

@@ -541,6 +541,35 @@ def test_plan_refused_pages():
         assert -1 in want and out["move_src"][2, :n].tolist() == want and out["move_dst"][2, :n].tolist() == rows[2]["dst"]
 
 
+@pytest.mark.parametrize("bad", [
+    [(2, 18, -1)],                                                   # freed, and moved from
+    [(1, 0, 2 ** 31 - 1)],                                           # moved to
+    [(0, 2, -2 ** 31), (0, 6, -1)],                                  # in a row that loses few tokens
+    [(2, e, 10 ** 6 + e) for e in range(19)],                        # no page of a row at all
+    [(i, e, -1 - e) for i in range(3) for e in range(0, 19, 2)]],
+    ids=["source", "destination", "short", "whole", "every second"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_of_rows_with_pages_that_do_not_exist(bad, in_place):
+    """What is on them is not moved: the gap of such a pair keeps its token, score and position; what does not exist does
+    not get onto the stack of free pages, so that rows served from it have pages of the cache."""
+    m = AH.gdn()
+    c = _plan_case(101, (100, 200, 300), (50, 150, 10), 16, 2, 8, settled=(60, 200, 0), gone=(9, 70, 0), moves_extra=3)
+    for i, e, page in bad:
+        if e < -(-c["ctx"][i] // 16):
+            c["tables"][i, e] = page
+    out, err = _plan(c, in_place)
+    refused, stack = _check_plan(c, out, in_place)
+    assert not refused and stack is not None and err == m.DEV_BAD_PAGE
+    freed = [(i, e) for i, (lo, hi) in enumerate(((4, 7), (10, 13), (1, 19))) for e in range(lo, hi)]
+    assert all(0 <= p < c["n_pages"] for p in stack) and len(stack) == 3 + len(freed) - len(set(freed) & {x[:2] for x in bad})
+    geom = m.AttnGeometry(n_q_heads=1, n_kv_heads=1, d_head=64, page_tokens=16, n_pages=c["n_pages"], max_pages=len(stack))
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, cu, slots, pos, kv, n_free, code = z(1, len(stack)), z(2), z(16 * len(stack)), z(16 * len(stack)), z(1), z(1), z(1)
+    m.kv_plan(geom, z(1), _i32([16 * len(stack)]), _i32(out["free"]), _i32(out["n_free_out"]), table, cu, slots, pos, kv, n_free, dev_err=code)
+    torch.cuda.synchronize()
+    assert int(code.item()) == 0 and sorted(table[0].tolist()) == sorted(stack) and int(n_free.item()) == 0
+
+
 # ---------------------------------------------------------------- moves
 
 @pytest.mark.parametrize("Hk,D,page,dtype,counts", [
