@@ -24,6 +24,11 @@ constexpr int32_t kWeightsMaxWidth = 1 << 29;  // a workgroup of 256 threads to 
 constexpr long double kTwoPiLong = 6.283185307179586476925286766559L;
 constexpr double kTwoPi = static_cast<double>(kTwoPiLong);
 
+// The base of the frequencies; rot_dims > 2.
+double scaled_base(const gdn_rope* r) {
+  return r->scaling == GDN_ROPE_BASE ? r->base * std::pow(r->factor, r->rot_dims / (r->rot_dims - 2.0)) : r->base;
+}
+
 gdn_status check_rope(const gdn_rope* r) {
   if (!r) return fail(GDN_ERR_NULL, "rope: NULL, required: a gdn_rope");
   if (r->rot_dims < 2 || r->rot_dims % 2 != 0)
@@ -47,6 +52,8 @@ gdn_status check_rope(const gdn_rope* r) {
     return fail(GDN_ERR_GEOMETRY, "amplitude: %g, required: finite and > 0", r->amplitude);
   if (r->rot_dims % 16 != 0)
     return fail(GDN_ERR_UNSUPPORTED, "rot_dims: %d, supported by this library: a multiple of 16", r->rot_dims);
+  if (!std::isfinite(scaled_base(r)))
+    return fail(GDN_ERR_GEOMETRY, "base, factor: %g, %g, required: a finite base s^(R/(R-2))", r->base, r->factor);
   return ok();
 }
 
@@ -81,7 +88,7 @@ gdn_status gdn_rope_turns(const gdn_rope* r, double* freq, uint64_t* turns) {
   if (s != GDN_OK) return s;
   if (!turns) return fail(GDN_ERR_NULL, "turns: NULL, required: a host pointer");
   const int R = r->rot_dims;
-  const double base = r->scaling == GDN_ROPE_BASE ? r->base * std::pow(r->factor, R / (R - 2.0)) : r->base;
+  const double base = scaled_base(r);
   for (int i = 0; i < R / 2; ++i) {
     double f = std::pow(base, -2.0 * i / R);
     if (r->scaling == GDN_ROPE_LINEAR) f /= r->factor;

@@ -606,7 +606,7 @@ typedef struct gdn_rope {
   int32_t layout;    /* gdn_rope_layout */
   int32_t scaling;   /* gdn_rope_scaling */
   uint32_t flags;    /* GDN_ROPE_INVERSE */
-  double base;       /* > 1 */
+  double base;       /* > 1; with GDN_ROPE_BASE base s^(R/(R-2)) is finite too */
   double factor;     /* s >= 1 (ignored with GDN_ROPE_NONE) */
   double context;    /* GDN_ROPE_PARTS: trained tokens, >= 1 */
   double low, high;  /* GDN_ROPE_PARTS: turns, 0 <= low < high */

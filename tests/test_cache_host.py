@@ -87,6 +87,21 @@ def test_frequencies_by_parts_between_the_others():
     assert np.all(np.diff(parts / plain) <= 1e-15) and 0 < np.sum((turns > 1) & (turns < 32))
 
 
+def test_a_scaled_base_past_the_largest_number_is_refused(gdn):
+    """base s^(R/(R-2)), which as an infinity would make every frequency but the first 0; just below it is taken (the
+    exponents of the reference are up to 710, a few roundings of which are below 710 x 8 x 2^-53 < 1e-12)."""
+    for base, factor, rot in ((1e300, 1e8, 16), (1e300, 1e9, 256), (2.0, 1e300, 16), (1e308, 1.8, 64)):
+        with pytest.raises(gdn.GdnError, match="base, factor: "):
+            gdn.Rope(rot_dims=rot, base=base, scaling="base", factor=factor).check()
+        with pytest.raises(gdn.GdnError, match="base, factor: "):
+            gdn.rope_turns(gdn.Rope(rot_dims=rot, base=base, scaling="base", factor=factor), "cpu")
+        gdn.Rope(rot_dims=rot, base=base, scaling="linear", factor=factor).check()
+    rope = gdn.Rope(rot_dims=64, base=1e300, scaling="base", factor=1e7)
+    rope.check()
+    got, ref = np.array(gdn.rope_frequencies(rope)), co.frequencies(64, 1e300, "base", 1e7)
+    assert np.all(got > 0) and np.max(np.abs(got / ref - 1)) < 1e-12
+
+
 def test_rope_mirror(gdn):
     r = gdn.Rope(layout="pairs", inverse=True)
     s = r.c_struct()
