@@ -848,7 +848,8 @@ def rope_frequencies(rope: Rope) -> list:
 
 def rope_turns(rope: Rope, device="cuda") -> torch.Tensor:
     """gdn_rope_turns: the frequencies as 64-bit fractions of a turn (int64 [rot_dims / 2], the bits of uint64), made
-    once and kept by the caller for rope_rotate."""
+    once and kept by the caller for rope_rotate.  Frequencies of the caller's own, f < 2 pi, go to rope_rotate as such a
+    tensor too: round(f / (2 pi) 2^64) each, less 2^64 from 2^63 on."""
     return torch.frombuffer(_rope_tables(rope)[1], dtype=torch.int64).to(device)
 
 
@@ -896,7 +897,7 @@ def rope_rotate(geom: AttnGeometry, rope: Rope, turns, position, q=None, k=None,
 
 
 def attn_weights_workspace_bytes(geom: AttnGeometry, batch: int, n: int, width: int) -> int:
-    """What a call of these sizes needs; it grows with each of them."""
+    """What a call of these sizes needs; it grows with each of them, with width whatever the rows' lengths (gdn.h)."""
     return int(lib().gdn_attn_weights_workspace_bytes(geom._ref(), batch, n, width))
 
 

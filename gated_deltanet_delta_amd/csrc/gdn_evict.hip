@@ -17,8 +17,8 @@
 // number of instructions per token and pass: no branches and no addresses per token, one
 // form of the loads for all steps.  Short rows are bound by latency: chains of loads,
 // barriers between the digits, and the kernel's own instructions, which a launch fetches
-// anew, so all passes take the same code.  us: 4 rows of 8192 20, 64 rows of 500 - 16384
-// 34, 3 rows of 120000 cut to 16384 72.  (Keys of a row gone over in dependent steps, 2048
+// anew, so all passes take the same code.  us: 4 rows of 8192 19 - 20, 64 rows of 500 - 16384
+// 32 - 34, 3 rows of 120000 cut to 16384 72.  (Keys of a row gone over in dependent steps, 2048
 // counters in one copy: 27, 39 and 351; a branch per token and counter: 49, 45, 303; loads
 // in a form per kind of step, whose results meet in copies of registers and are waited for
 // there: 22, 34, 104.)

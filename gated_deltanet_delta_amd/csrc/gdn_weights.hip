@@ -16,10 +16,12 @@
 // so waves share nothing but Q, and one wave's loads hide behind the others' products.
 // In base 2: z log2(e) is what is stored and compared.
 //
-// Bound by bytes.  24 heads on 4, d 256: one query at 4 x 8K tokens 23 us (67 MB: 15.6 us for
-// the logits, 4.3 TB/s, 5.5 for the sums), 32 queries over 4 x 100K 407 us (820 MB twice, 4.0
-// TB/s); 32 heads on 8, d 128, 4 queries in each of 64 ragged rows 116 us (330 MB of K, 170 MB of
-// logits written and read).  Many rows, measured and dropped: 64 keys per wave in 8
+// Bound by bytes.  24 heads on 4, d 256: one query at 4 x 8K tokens 21 - 23 us (67 MB: 14.0 - 16.2 us for
+// the logits, 4.1 - 4.8 TB/s, 5.4 - 6.0 for the sums), 32 queries over 4 x 100K 377 - 420 us by the card (820 MB
+// twice, 3.9 - 4.3 TB/s); 32 heads on 8, d 128, 4 queries in each of 64 ragged rows 114 - 116 us (330 MB of K, 170 MB of
+// logits written and read).  With few rows the grids, the choice of the join and the workspace follow the score
+// array's width: in one of 131072 the decode step takes 28.5 us, the 64 ragged rows 300, with 4.4 GB of
+// workspace.  Many rows, measured and dropped: 64 keys per wave in 8
 // waves instead of 32 in 16, 580 us; workgroups of a fixed number of keys, 473; one group of
 // heads at a time, so that the second reading might find K in the last-level cache, 512 - 940.
 #include "gdn_attn_device.h"

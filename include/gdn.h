@@ -675,7 +675,12 @@ gdn_status gdn_rope_rotate(const gdn_attn_geometry* g, const gdn_rope* r, const 
  *   1 <= width <= 2^29.
  *   workspace: device, >= gdn_attn_weights_workspace_bytes() of this batch, n and width (it
  *   grows with each of them); calls that share a workspace must be ordered on one stream.
- * Logits, weights and sums are fp32, each sum in a fixed order.  Masked keys do not enter, whatever
+ *   With at most 32 queries of a KV head in a row (n H_q / H_kv) it holds their logits, 4 batch n H_q width
+ *   bytes, and the launches too are for `width` keys a row, whatever kv_len: an array no wider than the
+ *   rows become costs least.  With more it holds sums, 4 batch H_kv width bytes for every 96 - 256 of them; its size has
+ *   room for the logits of a call of fewer tokens all the same, some 128 batch H_kv width bytes.
+ * Logits, weights and sums are fp32, each sum in a fixed order.  A weight is as good as its logit in fp32, whose error
+ * grows with its size: logits past 2^23 leave their query's weights undefined.  Masked keys do not enter, whatever
  * they hold.  A query whose logits hold a NaN or +inf, or are all -inf, gives NaN to every token it attends.
  * Device errors: GDN_DEV_BAD_K (n_row) and GDN_DEV_BAD_LENGTH (kv_len outside
  * [n_i, min(width, max_pages P)], have_len outside [0, kv_len]) leave the row as it is;
@@ -701,7 +706,8 @@ size_t gdn_attn_weights_workspace_bytes(const gdn_attn_geometry* g, int32_t batc
  *   free_pages, n_free, n_free_out: the pages from ceil(b / P) on are pushed, rows in order
  *     (the stack of gdn_kv_plan).  They hold rows that are still to be moved: gdn_kv_move of every layer comes before
  *     the next gdn_kv_write.  block_table is not modified; its entries behind ceil(b / P) are no longer the row's.
- * Pages below a budget must not be shared with another row, since tokens move into them.
+ * A row that is cut must not share pages with another one: tokens move into those below its budget, and those behind it
+ * come free.
  * Inputs other than free_pages are not modified where the outputs are other buffers (kv_len_out,
  * row_state_out and n_free_out have to be), so a call can be repeated.
  * A row with c outside [0, min(width, max_pages P)], settled outside [0, c], evicted < 0 or c + evicted beyond 2^31 - 1
